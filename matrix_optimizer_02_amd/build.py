@@ -20,8 +20,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdmuon_ns.so")
 
-HIP_SOURCES = ["api.hip", "k_adamw.hip", "k_diag.hip", "k_elementwise.hip", "k_gemm_bf16.hip", "k_gemm_f32.hip",
-               "k_resident.hip", "tune.hip"]
+HIP_SOURCES = ["api.hip", "head.hip", "k_adamw.hip", "k_diag.hip", "k_elementwise.hip", "k_gemm_bf16.hip",
+               "k_gemm_f32.hip", "k_head_gemm.hip", "k_head_rows.hip", "k_resident.hip", "tune.hip"]
 CXX_SOURCES = ["plan.cpp"]
 ARCH = "gfx950"
 
@@ -48,11 +48,14 @@ def _run(cmd, verbose):
     return res
 
 
-def exported_symbols():
-    """Names of the functions include/dmuon_ns.h declares with DMUON_API."""
+HEADERS = ["dmuon_ns.h", "dmuon_head.h"]
+
+
+def exported_symbols(header: str = "dmuon_ns.h"):
+    """Names of the functions a header of include/ declares with DMUON_API."""
     import re
 
-    with open(os.path.join(INCLUDE, "dmuon_ns.h")) as f:
+    with open(os.path.join(INCLUDE, header)) as f:
         text = f.read()
     return re.findall(r"^DMUON_API\s+[\w\s\*]*?\b(\w+)\s*\(", text, flags=re.M)
 
@@ -78,7 +81,8 @@ def build(verbose: bool = False, extra_flags=(), out: str = None, build_dir: str
         objs.append(obj)
     version_script = os.path.join(bdir, "exports.map")
     with open(version_script, "w") as f:
-        f.write("{ global: " + " ".join(s + ";" for s in exported_symbols()) + " local: *; };\n")
+        names = [s for h in HEADERS for s in exported_symbols(h)]
+        f.write("{ global: " + " ".join(s + ";" for s in names) + " local: *; };\n")
     tmp = lib + ".tmp"
     _run([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs,
           f"-Wl,--version-script={version_script}", "-o", tmp], verbose)

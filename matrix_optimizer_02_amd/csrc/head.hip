@@ -1,0 +1,543 @@
+// Entry points of the output-head losses: argument checks, the workspace
+// layout, and the launch sequences
+//   forward   (teacher) rows -> pack H -> [pack W piece ->] tile statistics -> join
+//             (-> student logits and loss)
+//   backward  (teacher) rows -> pack H, coefficients -> per piece of the
+//             vocabulary: [pack W piece,] ds, (teacher's ids,) dH sums, dW -> dH
+// No device memory is allocated and nothing is synchronised.  The number of
+// rows that carry a loss stays on the device: the launches are sized for every
+// token and their workgroups read it.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <new>
+#include <vector>
+
+#include "head_internal.h"
+
+using namespace dmuon;
+
+namespace {
+
+int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+int64_t ceil_div(int64_t x, int64_t a) { return (x + a - 1) / a; }
+
+// Workgroups that fill the chip.
+constexpr int64_t kFill = 256;
+// Bytes of ds a piece of the vocabulary may take (one part): it is written
+// once and read by two products, so it should stay in the 256 MB last-level
+// cache next to what those stream.
+constexpr int64_t kPieceBytes = int64_t(256) << 20;
+constexpr int64_t kPieceMin = 8192;  // vocab rows: fewer would leave dW's launch short of tiles
+
+dmuon_status check_desc(const dmuon_head_desc* d) {
+    if (d == nullptr) return DMUON_ERR_INVALID_ARG;
+    if (d->tokens < 0 || d->hidden < 1 || d->vocab < 1 || d->top_k < 0) return DMUON_ERR_INVALID_ARG;
+    if (d->dtype != DMUON_BF16 && d->dtype != DMUON_F32) return DMUON_ERR_INVALID_ARG;
+    if (d->tokens > kHeadMaxTokens || d->hidden > kHeadMaxHidden || d->vocab > kHeadMaxVocab ||
+        d->top_k > kHeadMaxTopK || d->tokens > kHeadMaxLogits / d->vocab)
+        return DMUON_ERR_UNSUPPORTED;
+    return DMUON_OK;
+}
+
+HeadLayout layout_of(const dmuon_head_desc& d, bool backward) {
+    HeadLayout L{};
+    L.tokens = d.tokens;
+    L.hidden = d.hidden;
+    L.vocab = d.vocab;
+    L.top_k = d.top_k;
+    L.planes = head_planes(d.dtype);
+    L.esize = d.dtype == DMUON_BF16 ? 2 : 4;
+    L.tq = d.tokens <= 64 ? 64 : 256;
+    L.t_pad = std::max<int64_t>(round_up(d.tokens, kHeadTile), kHeadTile);
+    L.d_pad = std::max<int64_t>(round_up(d.hidden, kHeadSlab), kHeadMinK);
+    // bf16 rows of whole slabs are read in place; others go through a padded copy
+    L.pack_weight = L.planes > 1 || d.hidden != L.d_pad;
+    const int64_t v_pad = round_up(d.vocab, kHeadTile);
+    const int64_t fit = kPieceBytes / (L.t_pad * 2 * L.planes) / kHeadTile * kHeadTile;
+    int64_t piece = std::max(fit, kPieceMin);
+    if (L.pack_weight) {  // ... and the copy of W's piece
+        const int64_t w = (2 * kPieceBytes) / (L.d_pad * 2 * L.planes) / kHeadTile * kHeadTile;
+        piece = std::min(piece, std::max(w, kPieceMin));
+    }
+    L.pieces = (int32_t)ceil_div(v_pad, piece);
+    L.piece = round_up(ceil_div(v_pad, L.pieces), kHeadTile);
+    L.pieces = (int32_t)ceil_div(v_pad, L.piece);
+    // dH has few tiles when tokens are few: its K axis, the vocabulary, is split
+    const int64_t dh_tiles = ceil_div(L.t_pad, L.tq) * ceil_div(L.hidden, kHeadTile);
+    int64_t splits = std::max<int64_t>(1, kFill / dh_tiles);
+    L.split_k = round_up(ceil_div(L.piece, splits), kHeadMinK);
+    L.splits = (int32_t)ceil_div(L.piece, L.split_k);
+
+    size_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const size_t o = at;
+        at += align_up((size_t)bytes);
+        return o;
+    };
+    L.off_count = take(4);
+    L.off_src = take(4 * L.t_pad);
+    L.off_tgt = take(4 * L.t_pad);
+    L.off_lse = take(4 * L.t_pad);
+    L.off_cp = take(4 * L.t_pad);
+    L.off_ct = take(4 * L.t_pad);
+    L.off_tl = take(4 * L.t_pad);
+    L.off_q = take(8 * L.t_pad);
+    L.off_flag = take(4 * L.t_pad);
+    L.off_h = take(2 * L.planes * L.t_pad * L.d_pad);
+    // a packed piece of W, or the copy of its last, partial tile
+    L.off_w = take(L.pack_weight ? 2 * L.planes * L.piece * L.d_pad : 2 * kHeadTile * L.d_pad);
+    if (backward) {
+        L.off_g = take(2 * L.planes * L.t_pad * L.piece);
+        L.off_dh = take(4 * L.splits * round_up(L.t_pad, L.tq) * round_up(L.hidden, kHeadTile));
+    } else {
+        L.off_part = take(8 * (v_pad / kHeadTile) * head_wave_rows(L.tq) * L.t_pad);
+    }
+    L.bytes = at;
+    return L;
+}
+
+struct Span {
+    uintptr_t lo, hi;
+    bool written;
+};
+
+// Non-null, aligned, and no written buffer overlapping another one.
+struct Buffers {
+    std::vector<Span> spans;
+    bool ok = true;
+    void add(const void* p, int64_t bytes, bool written) {
+        if (bytes == 0) return;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+        if (p == nullptr || (a & 15u) != 0) ok = false;
+        spans.push_back({a, a + (uintptr_t)bytes, written});
+    }
+    bool good() const {
+        if (!ok) return false;
+        for (size_t i = 0; i < spans.size(); ++i)
+            for (size_t j = 0; j < i; ++j)
+                if ((spans[i].written || spans[j].written) && spans[i].lo < spans[j].hi && spans[j].lo < spans[i].hi)
+                    return false;
+        return true;
+    }
+};
+
+struct Call {
+    const dmuon_head_desc* desc;
+    const void* hidden;
+    const void* weight;
+    const int64_t* targets;  // cross entropy
+    int64_t ignore_index;
+    const int64_t* ids;      // distillation
+    const float* teacher;
+    float temp;
+    void* workspace;
+    size_t workspace_bytes;
+    hipStream_t stream;
+};
+
+dmuon_status check_call(const Call& c, bool distill, Buffers& b) {
+    const dmuon_status st = check_desc(c.desc);
+    if (st != DMUON_OK) return st;
+    const dmuon_head_desc& d = *c.desc;
+    if (distill ? d.top_k < 1 : d.top_k != 0) return DMUON_ERR_INVALID_ARG;
+    if (distill && !(std::isfinite(c.temp) && c.temp > 0.f && std::isfinite(1.f / c.temp) && 1.f / c.temp > 0.f))
+        return DMUON_ERR_INVALID_ARG;
+    const int64_t e = d.dtype == DMUON_BF16 ? 2 : 4;
+    b.add(c.hidden, d.tokens * d.hidden * e, false);
+    b.add(c.weight, d.vocab * d.hidden * e, false);
+    if (distill) {
+        b.add(c.ids, 8 * d.tokens * d.top_k, false);
+        b.add(c.teacher, 4 * d.tokens * d.top_k, false);
+    } else {
+        b.add(c.targets, 8 * d.tokens, false);
+    }
+    return DMUON_OK;
+}
+
+dmuon_status check_rest(const Call& c, const HeadLayout& L, Buffers& b) {
+    if (!b.good()) return DMUON_ERR_INVALID_ARG;
+    if (c.workspace == nullptr || (reinterpret_cast<uintptr_t>(c.workspace) & (kAlign - 1)) != 0 ||
+        c.workspace_bytes < L.bytes)
+        return DMUON_ERR_WORKSPACE;
+    b.add(c.workspace, (int64_t)L.bytes, true);
+    return b.good() ? DMUON_OK : DMUON_ERR_INVALID_ARG;
+}
+
+#define HEAD_TRY(X)                                  \
+    do {                                             \
+        if ((X) != hipSuccess) return DMUON_ERR_HIP; \
+    } while (0)
+
+// The arrays of the workspace.
+struct Views {
+    char* ws;
+    const HeadLayout& L;
+    template <typename T>
+    T* at(size_t off) const {
+        return reinterpret_cast<T*>(ws + off);
+    }
+    int32_t* count() const { return at<int32_t>(L.off_count); }
+    int32_t* src() const { return at<int32_t>(L.off_src); }
+    int32_t* target() const { return at<int32_t>(L.off_tgt); }
+    float* lse() const { return at<float>(L.off_lse); }
+    float* cp() const { return at<float>(L.off_cp); }
+    float* ct() const { return at<float>(L.off_ct); }
+    float* target_logit() const { return at<float>(L.off_tl); }
+    float2* q() const { return at<float2>(L.off_q); }
+    int32_t* flag() const { return at<int32_t>(L.off_flag); }
+};
+
+HeadTeacher teacher_of(const Call& c) {
+    return HeadTeacher{c.ids, c.teacher, c.desc->top_k, c.desc->vocab, 1.f / c.temp};
+}
+
+// Which rows carry a loss, and their hidden states packed together.
+dmuon_status gather_rows(const Call& c, const Views& v, float* losses, float* lse, float* student) {
+    const HeadLayout& L = v.L;
+    if (c.ids != nullptr) HEAD_TRY(launch_head_teacher(teacher_of(c), L.tokens, v.q(), v.flag(), student, c.stream));
+    HeadRowsArgs r{};
+    r.targets = c.ids != nullptr ? nullptr : c.targets;
+    r.flag = v.flag();
+    r.ignore_index = c.ignore_index;
+    r.vocab = L.vocab;
+    r.tokens = (int32_t)L.tokens;
+    r.t_pad = (int32_t)L.t_pad;
+    r.count = v.count();
+    r.src = v.src();
+    r.target = v.target();
+    r.losses = losses;
+    r.lse = lse;
+    HEAD_TRY(launch_head_rows(r, c.stream));
+    HeadPackArgs p{};
+    p.in = c.hidden;
+    p.esize = L.esize;
+    p.cols = L.hidden;
+    p.src = v.src();
+    p.count = v.count();
+    p.rows = L.tokens;
+    p.out = v.at<uint16_t>(L.off_h);
+    p.out_rows = L.t_pad;
+    p.ld = L.d_pad;
+    p.plane = L.t_pad * L.d_pad;
+    p.planes = L.planes;
+    HEAD_TRY(launch_head_pack(p, c.stream));
+    return DMUON_OK;
+}
+
+// vocab rows [v0, v0 + rows) of W as the products' P operand: in place, with
+// the last partial tile copied, or packed.
+dmuon_status weight_piece(const Call& c, const Views& v, int64_t v0, int64_t rows, HeadGemmArgs& a) {
+    const HeadLayout& L = v.L;
+    const int64_t left = std::min(rows, L.vocab - v0);  // real rows
+    const char* w = static_cast<const char*>(c.weight) + v0 * L.hidden * L.esize;
+    HeadPackArgs p{};
+    p.esize = L.esize;
+    p.cols = L.hidden;
+    p.out = v.at<uint16_t>(L.off_w);
+    p.ld = L.d_pad;
+    p.planes = L.planes;
+    a.tail_row = INT_MAX;
+    a.p_tail = nullptr;
+    a.p_ld = (int32_t)L.d_pad;
+    if (L.pack_weight) {
+        p.in = w;
+        p.rows = left;
+        p.out_rows = round_up(left, kHeadTile);
+        p.plane = L.piece * L.d_pad;
+        a.p = v.ws + L.off_w;
+        a.p_plane = 2 * p.plane;
+        HEAD_TRY(launch_head_pack(p, c.stream));
+        return DMUON_OK;
+    }
+    a.p = w;
+    a.p_plane = 0;
+    if (left % kHeadTile != 0) {
+        const int64_t whole = left / kHeadTile * kHeadTile;
+        p.in = w + whole * L.hidden * L.esize;
+        p.rows = left - whole;
+        p.out_rows = kHeadTile;
+        p.plane = 0;
+        a.tail_row = (int32_t)whole;
+        a.p_tail = v.ws + L.off_w;
+        HEAD_TRY(launch_head_pack(p, c.stream));
+    }
+    return DMUON_OK;
+}
+
+void logits_args(const Call& c, const Views& v, int64_t v0, int64_t rows, HeadGemmArgs& a) {
+    const HeadLayout& L = v.L;
+    a.count = v.count();
+    a.q = v.ws + L.off_h;
+    a.q_ld = (int32_t)L.d_pad;
+    a.q_plane = 2 * L.t_pad * L.d_pad;
+    a.parts = L.planes;
+    a.k = (int32_t)L.d_pad;
+    a.tiles_i = (int32_t)ceil_div(std::min(rows, L.vocab - v0), kHeadTile);
+    a.v0 = v0;
+    a.vocab = L.vocab;
+    a.inv_temp = 1.f / c.temp;
+    a.target = c.ids != nullptr ? nullptr : v.target();
+    a.t_pad = L.t_pad;
+    a.first_tile = (int32_t)(v0 / kHeadTile);
+}
+
+dmuon_status forward(const Call& c, bool distill, float* losses, float* lse, float* student) {
+    Buffers b;
+    dmuon_status st = check_call(c, distill, b);
+    if (st != DMUON_OK) return st;
+    const dmuon_head_desc& d = *c.desc;
+    b.add(losses, 4 * d.tokens, true);
+    b.add(lse, 4 * d.tokens, true);
+    if (distill) b.add(student, 4 * d.tokens * d.top_k, true);
+    const HeadLayout L = layout_of(d, false);
+    if (d.tokens == 0) return b.good() ? DMUON_OK : DMUON_ERR_INVALID_ARG;
+    st = check_rest(c, L, b);
+    if (st != DMUON_OK) return st;
+
+    const Views v{static_cast<char*>(c.workspace), L};
+    st = gather_rows(c, v, losses, lse, student);
+    if (st != DMUON_OK) return st;
+    // read in place, the whole vocabulary is one launch
+    const int64_t step = L.pack_weight ? L.piece : round_up(L.vocab, kHeadTile);
+    for (int64_t v0 = 0; v0 < L.vocab; v0 += step) {
+        HeadGemmArgs a{};
+        st = weight_piece(c, v, v0, step, a);
+        if (st != DMUON_OK) return st;
+        logits_args(c, v, v0, step, a);
+        a.part = v.at<float2>(L.off_part);
+        a.target_logit = v.target_logit();
+        HEAD_TRY(launch_head_gemm(kHeadLse, L.tq, a, (int64_t)a.tiles_i * ceil_div(L.tokens, L.tq), c.stream));
+    }
+    HeadMergeArgs m{};
+    m.count = v.count();
+    m.src = v.src();
+    m.part = v.at<float2>(L.off_part);
+    m.t_pad = L.t_pad;
+    m.parts = (int32_t)ceil_div(L.vocab, kHeadTile) * head_wave_rows(L.tq);
+    m.tokens = L.tokens;
+    m.inv_temp = 1.f / c.temp;
+    m.target = distill ? nullptr : v.target();
+    m.target_logit = v.target_logit();
+    m.lse_c = v.lse();
+    m.losses = losses;
+    m.lse = lse;
+    HEAD_TRY(launch_head_merge(m, c.stream));
+    if (distill) {
+        HeadStudentArgs s{};
+        s.count = v.count();
+        s.src = v.src();
+        s.t = teacher_of(c);
+        s.q = v.q();
+        s.hidden = c.hidden;
+        s.weight = c.weight;
+        s.esize = L.esize;
+        s.cols = L.hidden;
+        s.lse_c = v.lse();
+        s.temp = c.temp;
+        s.student = student;
+        s.losses = losses;
+        s.tokens = L.tokens;
+        HEAD_TRY(launch_head_student(s, c.stream));
+    }
+    return DMUON_OK;
+}
+
+dmuon_status backward(const Call& c, bool distill, const float* lse, const float* student, const float* grad_losses,
+                      const float* grad_lse, void* grad_hidden, void* grad_weight) {
+    Buffers b;
+    dmuon_status st = check_call(c, distill, b);
+    if (st != DMUON_OK) return st;
+    const dmuon_head_desc& d = *c.desc;
+    const int64_t e = d.dtype == DMUON_BF16 ? 2 : 4;
+    if (grad_hidden == nullptr && grad_weight == nullptr && (d.tokens > 0)) return DMUON_ERR_INVALID_ARG;
+    b.add(lse, 4 * d.tokens, false);
+    b.add(grad_losses, 4 * d.tokens, false);
+    if (grad_lse != nullptr) b.add(grad_lse, 4 * d.tokens, false);
+    if (distill) b.add(student, 4 * d.tokens * d.top_k, false);
+    if (grad_hidden != nullptr) b.add(grad_hidden, d.tokens * d.hidden * e, true);
+    if (grad_weight != nullptr) b.add(grad_weight, d.vocab * d.hidden * e, true);
+    const HeadLayout L = layout_of(d, true);
+    if (d.tokens == 0) {
+        if (!b.good()) return DMUON_ERR_INVALID_ARG;
+        if (grad_weight != nullptr) HEAD_TRY(launch_head_zero(grad_weight, d.vocab * d.hidden * e, c.stream));
+        return DMUON_OK;
+    }
+    st = check_rest(c, L, b);
+    if (st != DMUON_OK) return st;
+
+    const Views v{static_cast<char*>(c.workspace), L};
+    st = gather_rows(c, v, nullptr, nullptr, nullptr);
+    if (st != DMUON_OK) return st;
+    HeadCoefArgs k{};
+    k.count = v.count();
+    k.src = v.src();
+    k.target = distill ? nullptr : v.target();
+    k.q = distill ? v.q() : nullptr;
+    k.lse = lse;
+    k.grad_losses = grad_losses;
+    k.grad_lse = grad_lse;
+    k.temp = c.temp;
+    k.lse_c = v.lse();
+    k.cp = v.cp();
+    k.ct = v.ct();
+    k.t_pad = L.t_pad;
+    HEAD_TRY(launch_head_coef(k, c.stream));
+    const int64_t t_tiles = ceil_div(L.tokens, L.tq);
+    const int32_t d_tiles = (int32_t)ceil_div(L.hidden, kHeadTile);
+    for (int64_t v0 = 0; v0 < L.vocab; v0 += L.piece) {
+        const int64_t left = std::min(L.piece, L.vocab - v0);
+        HeadGemmArgs w{};
+        st = weight_piece(c, v, v0, L.piece, w);
+        if (st != DMUON_OK) return st;
+        HeadGemmArgs a = w;
+        logits_args(c, v, v0, L.piece, a);
+        a.lse = v.lse();
+        a.cp = v.cp();
+        a.ct = v.ct();
+        a.g = v.ws + L.off_g;
+        a.g_plane = 2 * L.t_pad * L.piece;
+        a.g_ld = (int32_t)L.piece;
+        const int64_t g_tiles = ceil_div(std::max<int64_t>(L.tokens, kHeadMinK), L.tq);
+        HEAD_TRY(launch_head_gemm(kHeadGrad, L.tq, a, a.tiles_i * g_tiles, c.stream));
+        if (distill) {
+            HeadFixArgs f{};
+            f.count = v.count();
+            f.src = v.src();
+            f.t = teacher_of(c);
+            f.q = v.q();
+            f.student = student;
+            f.lse_c = v.lse();
+            f.cp = v.cp();
+            f.g = v.at<uint16_t>(L.off_g);
+            f.g_plane = L.t_pad * L.piece;
+            f.g_ld = L.piece;
+            f.planes = L.planes;
+            f.v0 = v0;
+            f.v1 = v0 + left;
+            f.tokens = L.tokens;
+            HEAD_TRY(launch_head_fix(f, c.stream));
+        }
+        if (grad_hidden != nullptr) {
+            HeadGemmArgs h = w;
+            h.count = v.count();
+            h.q = v.ws + L.off_g;
+            h.q_ld = (int32_t)L.piece;
+            h.q_plane = 2 * L.t_pad * L.piece;
+            h.parts = L.planes;
+            h.k = (int32_t)round_up(left, kHeadTile);
+            h.split_k = (int32_t)L.split_k;
+            h.splits = (int32_t)ceil_div(h.k, L.split_k);
+            h.tiles_i = d_tiles;
+            h.dh = v.at<float>(L.off_dh);
+            h.accumulate = v0 != 0;
+            HEAD_TRY(launch_head_gemm(kHeadDh, L.tq, h, h.splits * d_tiles * t_tiles, c.stream));
+        }
+        if (grad_weight != nullptr) {
+            HeadGemmArgs g{};
+            g.count = v.count();
+            g.p = v.ws + L.off_h;
+            g.p_ld = (int32_t)L.d_pad;
+            g.p_plane = 2 * L.t_pad * L.d_pad;
+            g.tail_row = INT_MAX;
+            g.q = v.ws + L.off_g;
+            g.q_ld = (int32_t)L.piece;
+            g.q_plane = 2 * L.t_pad * L.piece;
+            g.parts = L.planes;
+            g.tiles_i = d_tiles;
+            g.tiles_j = (int32_t)ceil_div(left, kHeadTile);
+            g.dw = static_cast<char*>(grad_weight) + v0 * L.hidden * L.esize;
+            g.dw_rows = left;
+            g.dw_ld = (int32_t)L.hidden;
+            HEAD_TRY(launch_head_gemm(kHeadDw, 256, g, (int64_t)g.tiles_i * g.tiles_j, c.stream));
+        }
+    }
+    if (grad_hidden != nullptr) {
+        HeadDhArgs h{};
+        h.count = v.count();
+        h.src = v.src();
+        h.dh = v.at<float>(L.off_dh);
+        h.splits = L.splits;
+        h.tiles_i = d_tiles;
+        h.tq = L.tq;
+        h.out = grad_hidden;
+        h.esize = L.esize;
+        h.tokens = L.tokens;
+        h.cols = L.hidden;
+        HEAD_TRY(launch_head_dh(h, c.stream));
+    }
+    return DMUON_OK;
+}
+
+}  // namespace
+
+extern "C" dmuon_status head_loss_workspace_bytes(const dmuon_head_desc* desc, int32_t backward, size_t* bytes) {
+    if (bytes == nullptr) return DMUON_ERR_INVALID_ARG;
+    const dmuon_status st = check_desc(desc);
+    if (st != DMUON_OK) return st;
+    // the cut depends on the number of tokens, so a shorter batch may need more:
+    // the largest over all of them, one per layout (tokens enter as 64 or fewer,
+    // then in whole tiles)
+    dmuon_head_desc d = *desc;
+    size_t most = 0;
+    for (int64_t t = std::min<int64_t>(64, desc->tokens);; t = std::min(round_up(t + 1, kHeadTile), desc->tokens)) {
+        d.tokens = t;
+        most = std::max(most, layout_of(d, backward != 0).bytes);
+        if (t == desc->tokens) break;
+    }
+    *bytes = most;
+    return DMUON_OK;
+}
+
+extern "C" dmuon_status head_cross_entropy_forward(const dmuon_head_desc* desc, const void* hidden, const void* weight,
+                                                   const int64_t* targets, int64_t ignore_index, float* losses,
+                                                   float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    try {
+        const Call c{desc, hidden, weight, targets, ignore_index, nullptr, nullptr, 1.f, workspace, workspace_bytes,
+                     static_cast<hipStream_t>(stream)};
+        return forward(c, false, losses, lse, nullptr);
+    } catch (...) {
+        return DMUON_ERR_ALLOC;
+    }
+}
+
+extern "C" dmuon_status head_cross_entropy_backward(const dmuon_head_desc* desc, const void* hidden,
+                                                    const void* weight, const int64_t* targets, int64_t ignore_index,
+                                                    const float* lse, const float* grad_losses, const float* grad_lse,
+                                                    void* grad_hidden, void* grad_weight, void* workspace,
+                                                    size_t workspace_bytes, void* stream) {
+    try {
+        const Call c{desc, hidden, weight, targets, ignore_index, nullptr, nullptr, 1.f, workspace, workspace_bytes,
+                     static_cast<hipStream_t>(stream)};
+        return backward(c, false, lse, nullptr, grad_losses, grad_lse, grad_hidden, grad_weight);
+    } catch (...) {
+        return DMUON_ERR_ALLOC;
+    }
+}
+
+extern "C" dmuon_status head_distill_forward(const dmuon_head_desc* desc, const void* hidden, const void* weight,
+                                             const int64_t* teacher_ids, const float* teacher_logits,
+                                             float temperature, float* losses, float* lse, float* student_logits,
+                                             void* workspace, size_t workspace_bytes, void* stream) {
+    try {
+        const Call c{desc, hidden, weight, nullptr, 0, teacher_ids, teacher_logits, temperature, workspace,
+                     workspace_bytes, static_cast<hipStream_t>(stream)};
+        return forward(c, true, losses, lse, student_logits);
+    } catch (...) {
+        return DMUON_ERR_ALLOC;
+    }
+}
+
+extern "C" dmuon_status head_distill_backward(const dmuon_head_desc* desc, const void* hidden, const void* weight,
+                                              const int64_t* teacher_ids, const float* teacher_logits,
+                                              float temperature, const float* lse, const float* student_logits,
+                                              const float* grad_losses, void* grad_hidden, void* grad_weight,
+                                              void* workspace, size_t workspace_bytes, void* stream) {
+    try {
+        const Call c{desc, hidden, weight, nullptr, 0, teacher_ids, teacher_logits, temperature, workspace,
+                     workspace_bytes, static_cast<hipStream_t>(stream)};
+        return backward(c, true, lse, student_logits, grad_losses, nullptr, grad_hidden, grad_weight);
+    } catch (...) {
+        return DMUON_ERR_ALLOC;
+    }
+}

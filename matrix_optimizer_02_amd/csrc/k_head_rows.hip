@@ -1,0 +1,434 @@
+// Row kernels of the output-head losses: which rows carry a loss, their hidden
+// states packed together, the join of the softmax statistics, the coefficients
+// of the gradient and the hidden states' gradient scattered back.
+#include "head_internal.h"
+#include "kcommon.h"
+
+namespace dmuon {
+namespace {
+
+constexpr int kRowThreads = 256;
+
+__device__ __forceinline__ float wave_sum(float v) {
+    #pragma unroll
+    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+    return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+    #pragma unroll
+    for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
+    return v;
+}
+
+__device__ __forceinline__ float nan_f() { return __uint_as_float(0x7fc00000u); }
+
+// One wave per token: the teacher's softmax over its K entries, as (max, log
+// of the sum) of z / T.  A row whose entries are all absent or -inf carries no
+// loss; an id past the vocabulary marks the row NaN.
+__global__ __launch_bounds__(kRowThreads) void head_teacher_kernel(HeadTeacher t, int64_t tokens, float2* q,
+                                                                   int32_t* flag, float* student) {
+    const int lane = threadIdx.x & 63;
+    const int64_t row = (int64_t)blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6);
+    if (row >= tokens) return;
+    const int64_t* ids = t.ids + row * t.k;
+    const float* z = t.logits + row * t.k;
+    float m = -INFINITY;
+    bool bad = false, held = false;
+    for (int k = lane; k < t.k; k += 64) {
+        const int64_t id = ids[k];
+        if (student != nullptr) student[row * t.k + k] = 0.f;
+        if (id < 0) continue;
+        const float y = z[k] * t.inv_temp;
+        if (y == -INFINITY) continue;  // no mass
+        held = true;
+        bad = bad || id >= t.vocab || y != y;
+        m = fmaxf(m, y);
+    }
+    held = __builtin_amdgcn_ballot_w64(held) != 0;
+    bad = __builtin_amdgcn_ballot_w64(bad) != 0;
+    m = wave_max(m);
+    float l = 0.f;
+    if (held && !bad)
+        for (int k = lane; k < t.k; k += 64)
+            if (ids[k] >= 0) l += expf(z[k] * t.inv_temp - m);
+    l = wave_sum(l);
+    if (lane == 0) {
+        flag[row] = held;
+        q[row] = bad ? make_float2(nan_f(), nan_f()) : make_float2(m, held ? logf(l) : 0.f);
+    }
+}
+
+// One block: the rows that carry a loss keep their order at the front of src,
+// the others fill it from the back.
+constexpr int kScanThreads = 1024;
+__global__ __launch_bounds__(kScanThreads) void head_rows_kernel(HeadRowsArgs a) {
+    __shared__ int wave_n[kScanThreads / 64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int n = 0;
+    for (int t0 = 0; t0 < a.tokens; t0 += kScanThreads) {
+        const int t = t0 + threadIdx.x;
+        const bool in = t < a.tokens;
+        const int64_t target = in && a.targets != nullptr ? a.targets[t] : 0;
+        const bool live = in && (a.targets != nullptr ? target != a.ignore_index : a.flag[t] != 0);
+        const uint64_t b = __builtin_amdgcn_ballot_w64(live);
+        if (lane == 0) wave_n[wave] = __popcll(b);
+        __syncthreads();
+        int before = __popcll(b & ((1ull << lane) - 1)), all = 0;
+        for (int w = 0; w < kScanThreads / 64; ++w) {
+            before += w < wave ? wave_n[w] : 0;
+            all += wave_n[w];
+        }
+        __syncthreads();
+        if (live) {
+            const int c = n + before;
+            a.src[c] = t;
+            if (a.targets != nullptr) a.target[c] = target >= 0 && target < a.vocab ? (int)target : -2;
+        } else if (in) {
+            a.src[a.tokens - 1 - (t - (n + before))] = t;
+            if (a.losses != nullptr) {
+                a.losses[t] = 0.f;
+                a.lse[t] = 0.f;
+            }
+        }
+        n += all;
+    }
+    if (a.targets != nullptr)
+        for (int c = n + threadIdx.x; c < a.t_pad; c += kScanThreads) a.target[c] = -1;
+    if (threadIdx.x == 0) *a.count = n;
+}
+
+// One block per output row (grid-stride), 8 columns per thread and step.
+template <int ESIZE, int PLANES>
+__global__ __launch_bounds__(kRowThreads) void head_pack_kernel(HeadPackArgs a) {
+    const int64_t limit = a.count != nullptr ? *a.count : a.rows;
+    // rows past the last one: zeros up to a whole tile
+    int64_t end = (limit + kHeadTile - 1) / kHeadTile * kHeadTile;
+    if (end == 0) end = kHeadTile;
+    if (end > a.out_rows) end = a.out_rows;
+    const bool vec = a.cols % 8 == 0;
+    for (int64_t r = blockIdx.x; r < end; r += gridDim.x) {
+        const int64_t from = r < limit ? (a.src != nullptr ? (int64_t)a.src[r] : r) : -1;
+        for (int64_t c = threadIdx.x * 8; c < a.ld; c += kRowThreads * 8) {
+            float x[8];
+            #pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = 0.f;
+            if (from >= 0) {
+                if (ESIZE == 2) {
+                    const uint16_t* p = static_cast<const uint16_t*>(a.in) + from * a.cols + c;
+                    if (vec && c < a.cols) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(p);
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                        #pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = bf16_to_f32((uint16_t)(w[e / 2] >> (16 * (e & 1))));
+                    } else {
+                        #pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (c + e < a.cols) x[e] = bf16_to_f32(p[e]);
+                    }
+                } else {
+                    const float* p = static_cast<const float*>(a.in) + from * a.cols + c;
+                    if (vec && c < a.cols) {
+                        const float4 u = reinterpret_cast<const float4*>(p)[0], v = reinterpret_cast<const float4*>(p)[1];
+                        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+                        x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+                    } else {
+                        #pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (c + e < a.cols) x[e] = p[e];
+                    }
+                }
+            }
+            #pragma unroll
+            for (int part = 0; part < PLANES; ++part) {
+                uint32_t w[4];
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint16_t b = f32_to_bf16(x[e]);
+                    x[e] -= bf16_to_f32(b);
+                    if (e & 1) w[e / 2] |= (uint32_t)b << 16; else w[e / 2] = b;
+                }
+                *reinterpret_cast<uint4*>(a.out + part * a.plane + r * a.ld + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    }
+}
+
+// 16 rows by 16 groups of tiles a block: each group joins its tiles' (max, sum)
+// pairs in order, then the groups join in order.
+constexpr int kMergeRows = 16, kMergeGroups = 16;
+__global__ __launch_bounds__(kMergeRows* kMergeGroups) void head_merge_kernel(HeadMergeArgs a) {
+    __shared__ float2 part[kMergeGroups][kMergeRows];
+    const int n = *a.count;
+    const int r = threadIdx.x % kMergeRows, g = threadIdx.x / kMergeRows;
+    const int64_t c = (int64_t)blockIdx.x * kMergeRows + r;
+    const float scale = a.inv_temp;
+    auto join = [&](float2 x, float2 y) {
+        // a NaN maximum does not survive fmaxf: it is in the sum too, and stays
+        const float m = fmaxf(x.x, y.x);
+        const float m0 = m == -INFINITY ? 0.f : m;
+        return make_float2(m, x.y * expf((x.x - m0) * scale) + y.y * expf((y.x - m0) * scale));
+    };
+    float2 s = make_float2(-INFINITY, 0.f);
+    if (c < n) {
+        const int per = (a.parts + kMergeGroups - 1) / kMergeGroups;
+        const int p1 = min(a.parts, (g + 1) * per);
+        #pragma unroll 8
+        for (int p = g * per; p < p1; ++p) s = join(s, a.part[(int64_t)p * a.t_pad + c]);
+    }
+    part[g][r] = s;
+    __syncthreads();
+    if (g != 0 || c >= n) return;
+    for (int k = 1; k < kMergeGroups; ++k) s = join(s, part[k][r]);
+    const float lse = fmaf(s.x, scale, logf(s.y));
+    a.lse_c[c] = lse;
+    const int t = a.src[c];
+    a.lse[t] = lse;
+    if (a.target != nullptr) a.losses[t] = a.target[c] < 0 ? nan_f() : lse - a.target_logit[c];
+}
+
+// One block per row with a loss: the student's logits at the teacher's ids, a
+// wave per id, and the loss.
+template <int ESIZE>
+__global__ __launch_bounds__(kRowThreads) void head_student_kernel(HeadStudentArgs a) {
+    __shared__ float sums[kRowThreads / 64];
+    const int n = *a.count;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const bool vec = a.cols % (16 / ESIZE) == 0;
+    for (int64_t c = blockIdx.x; c < n; c += gridDim.x) {
+        const int64_t row = a.src[c];
+        const float2 q = a.q[row];
+        const float lse = a.lse_c[c];
+        float loss = 0.f;
+        for (int k = wave; k < a.t.k; k += kRowThreads / 64) {
+            const int64_t id = a.t.ids[row * a.t.k + k];
+            if (id < 0 || id >= a.t.vocab) continue;
+            float s = 0.f;
+            if (ESIZE == 2) {
+                const uint16_t* h = static_cast<const uint16_t*>(a.hidden) + row * a.cols;
+                const uint16_t* w = static_cast<const uint16_t*>(a.weight) + id * a.cols;
+                if (vec) {
+                    #pragma unroll 4
+                    for (int64_t d = lane * 8; d < a.cols; d += 512) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(h + d), y = *reinterpret_cast<const uint4*>(w + d);
+                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+                        #pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
+                            s = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), s);
+                        }
+                    }
+                } else {
+                    for (int64_t d = lane; d < a.cols; d += 64) s = fmaf(bf16_to_f32(h[d]), bf16_to_f32(w[d]), s);
+                }
+            } else {
+                const float* h = static_cast<const float*>(a.hidden) + row * a.cols;
+                const float* w = static_cast<const float*>(a.weight) + id * a.cols;
+                if (vec) {
+                    #pragma unroll 4
+                    for (int64_t d = lane * 4; d < a.cols; d += 256) {
+                        const float4 x = *reinterpret_cast<const float4*>(h + d), y = *reinterpret_cast<const float4*>(w + d);
+                        s = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s))));
+                    }
+                } else {
+                    for (int64_t d = lane; d < a.cols; d += 64) s = fmaf(h[d], w[d], s);
+                }
+            }
+            s = wave_sum(s);
+            if (lane == 0) a.student[row * a.t.k + k] = s;
+            const float z = a.t.logits[row * a.t.k + k] * a.t.inv_temp;
+            if (z != -INFINITY) {
+                const float logq = z - q.x - q.y;
+                loss = fmaf(expf(logq), (logq + lse) - s * a.t.inv_temp, loss);
+            }
+        }
+        if (lane == 0) sums[wave] = loss;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            float total = 0.f;
+            for (int w = 0; w < kRowThreads / 64; ++w) total += sums[w];
+            // a row with an id past the vocabulary has q NaN; every other term may be absent
+            if (q.x != q.x) total = nan_f();
+            a.losses[row] = a.temp * a.temp * total;
+        }
+        __syncthreads();
+    }
+}
+
+__global__ __launch_bounds__(kRowThreads) void head_coef_kernel(HeadCoefArgs a) {
+    const int64_t c = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+    if (c >= a.t_pad) return;
+    float lse = 0.f, cp = 0.f, ct = 0.f;
+    if (c < *a.count) {
+        const int t = a.src[c];
+        lse = a.lse[t];
+        ct = a.temp * a.grad_losses[t];
+        cp = a.grad_lse != nullptr ? ct + a.grad_lse[t] : ct;
+        const bool bad = a.target != nullptr ? a.target[c] < 0 : a.q[t].x != a.q[t].x;
+        if (bad) cp = nan_f();
+    }
+    a.lse_c[c] = lse;
+    a.cp[c] = cp;
+    a.ct[c] = ct;
+}
+
+// One wave per row with a loss: ds at each teacher id of the piece, from the
+// exact student logit; an id held twice takes the sum of its entries' q, which
+// both of them write.
+__global__ __launch_bounds__(kRowThreads) void head_fix_kernel(HeadFixArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t c = (int64_t)blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6);
+    if (c >= *a.count) return;
+    const int64_t row = a.src[c];
+    const int64_t* ids = a.t.ids + row * a.t.k;
+    const float* z = a.t.logits + row * a.t.k;
+    const float2 qs = a.q[row];
+    const float cp = a.cp[c], lse = a.lse_c[c];
+    for (int k = lane; k < a.t.k; k += 64) {
+        const int64_t id = ids[k];
+        if (id < a.v0 || id >= a.v1) continue;
+        float q = 0.f;
+        for (int j = 0; j < a.t.k; ++j)
+            if (ids[j] == id) q += expf(z[j] * a.t.inv_temp - qs.x - qs.y);
+        const float p = expf(fmaf(a.student[row * a.t.k + k], a.t.inv_temp, -lse));
+        float g = cp * (p - q);
+        uint16_t* out = a.g + c * a.g_ld + (id - a.v0);
+        for (int part = 0; part < a.planes; ++part) {
+            const uint16_t b = f32_to_bf16(g);
+            out[part * a.g_plane] = b;
+            g -= bf16_to_f32(b);
+        }
+    }
+}
+
+// A block per tile quarter: the tile's sums in the product kernel's own order
+// (lane's four values are 4 consecutive columns of one row).
+template <int TQ>
+__global__ __launch_bounds__(kRowThreads) void head_dh_kernel(HeadDhArgs a) {
+    constexpr int WR = TQ == 256 ? 2 : 4, RW = kHeadTile / WR, CW = TQ / (8 / WR), FI = RW / 32, FJ = CW / 32;
+    constexpr int kGroups = 8 * FI * FJ * 4;  // of 64 float4
+    const int n = *a.count;
+    const int tiles_j = (n + TQ - 1) / TQ;
+    const int64_t per_split = (int64_t)tiles_j * a.tiles_i * (kHeadTile * TQ);
+    const int lane = threadIdx.x & 63;
+    const int64_t groups = (int64_t)tiles_j * a.tiles_i * kGroups;
+    const int64_t step = (int64_t)gridDim.x * (kRowThreads / 64);
+    for (int64_t w = (int64_t)blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6); w < groups; w += step) {
+        const int64_t tile = w / kGroups;
+        int g = (int)(w % kGroups);
+        const int v4 = g % 4; g /= 4;
+        const int j = g % FJ; g /= FJ;
+        const int i = g % FI; g /= FI;
+        const int wr = g % WR, wc = g / WR;
+        const int64_t J = tile / a.tiles_i, I = tile % a.tiles_i;
+        const int64_t c = J * TQ + wc * CW + 32 * j + (lane & 31);
+        const int64_t col = I * kHeadTile + wr * RW + 32 * i + 8 * v4 + 4 * (lane >> 5);
+        const float* p = a.dh + w * 256 + lane * 4;
+        float4 s = *reinterpret_cast<const float4*>(p);
+        for (int k = 1; k < a.splits; ++k) {
+            const float4 u = *reinterpret_cast<const float4*>(p + k * per_split);
+            s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
+        }
+        if (c >= n || col >= a.cols) continue;
+        const int64_t at = (int64_t)a.src[c] * a.cols + col;
+        const float x[4] = {s.x, s.y, s.z, s.w};
+        if (a.esize == 2) {
+            uint16_t* o = static_cast<uint16_t*>(a.out) + at;
+            if ((a.cols & 3) == 0) {
+                *reinterpret_cast<uint2*>(o) = make_uint2((uint32_t)f32_to_bf16(x[0]) | ((uint32_t)f32_to_bf16(x[1]) << 16),
+                                                          (uint32_t)f32_to_bf16(x[2]) | ((uint32_t)f32_to_bf16(x[3]) << 16));
+            } else {
+                for (int e = 0; e < 4; ++e)
+                    if (col + e < a.cols) o[e] = f32_to_bf16(x[e]);
+            }
+        } else {
+            float* o = static_cast<float*>(a.out) + at;
+            if ((a.cols & 3) == 0) {
+                *reinterpret_cast<float4*>(o) = s;
+            } else {
+                for (int e = 0; e < 4; ++e)
+                    if (col + e < a.cols) o[e] = x[e];
+            }
+        }
+    }
+    // rows without a loss
+    const int64_t idle = a.tokens - n;
+    for (int64_t w = (int64_t)blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6); w < idle; w += step) {
+        const int64_t at = (int64_t)a.src[n + w] * a.cols;
+        for (int64_t d = lane; d < a.cols; d += 64) {
+            if (a.esize == 2) static_cast<uint16_t*>(a.out)[at + d] = 0;
+            else static_cast<float*>(a.out)[at + d] = 0.f;
+        }
+    }
+}
+
+__global__ __launch_bounds__(kRowThreads) void head_zero_kernel(char* p, int64_t bytes) {
+    const int64_t step = (int64_t)gridDim.x * kRowThreads * 2;
+    for (int64_t i = ((int64_t)blockIdx.x * kRowThreads + threadIdx.x) * 2; i < bytes; i += step)
+        *reinterpret_cast<uint16_t*>(p + i) = 0;  // elements are 2 or 4 bytes
+}
+
+unsigned blocks_for(int64_t items, int64_t per_block, int64_t most) {
+    const int64_t b = (items + per_block - 1) / per_block;
+    return (unsigned)(b < 1 ? 1 : b > most ? most : b);
+}
+
+}  // namespace
+
+hipError_t launch_head_teacher(const HeadTeacher& t, int64_t tokens, float2* q, int32_t* flag, float* student,
+                               hipStream_t stream) {
+    const unsigned grid = blocks_for(tokens, kRowThreads / 64, INT32_MAX);
+    hipLaunchKernelGGL(head_teacher_kernel, dim3(grid), dim3(kRowThreads), 0, stream, t, tokens, q, flag, student);
+    return hipGetLastError();
+}
+
+hipError_t launch_head_rows(const HeadRowsArgs& a, hipStream_t stream) {
+    hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(kScanThreads), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_head_pack(const HeadPackArgs& a, hipStream_t stream) {
+    const dim3 grid(blocks_for(a.out_rows, 1, 16384)), block(kRowThreads);
+    if (a.esize == 2) hipLaunchKernelGGL((head_pack_kernel<2, 1>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((head_pack_kernel<4, kHeadMaxPlanes>), grid, block, 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_head_merge(const HeadMergeArgs& a, hipStream_t stream) {
+    const unsigned grid = blocks_for(a.tokens, kMergeRows, INT32_MAX);
+    hipLaunchKernelGGL(head_merge_kernel, dim3(grid), dim3(kMergeRows * kMergeGroups), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_head_student(const HeadStudentArgs& a, hipStream_t stream) {
+    const dim3 grid(blocks_for(a.tokens, 1, 1 << 20)), block(kRowThreads);
+    if (a.esize == 2) hipLaunchKernelGGL((head_student_kernel<2>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((head_student_kernel<4>), grid, block, 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_head_coef(const HeadCoefArgs& a, hipStream_t stream) {
+    const unsigned grid = blocks_for(a.t_pad, kRowThreads, INT32_MAX);
+    hipLaunchKernelGGL(head_coef_kernel, dim3(grid), dim3(kRowThreads), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_head_fix(const HeadFixArgs& a, hipStream_t stream) {
+    const unsigned grid = blocks_for(a.tokens, kRowThreads / 64, INT32_MAX);
+    hipLaunchKernelGGL(head_fix_kernel, dim3(grid), dim3(kRowThreads), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_head_dh(const HeadDhArgs& a, hipStream_t stream) {
+    const dim3 grid(blocks_for(a.tokens * ((a.cols + 255) / 256) * 64, kRowThreads, 8192)), block(kRowThreads);
+    if (a.tq == 256) hipLaunchKernelGGL((head_dh_kernel<256>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((head_dh_kernel<64>), grid, block, 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_head_zero(void* p, int64_t bytes, hipStream_t stream) {
+    const unsigned grid = blocks_for(bytes, kRowThreads * 2, 8192);
+    hipLaunchKernelGGL(head_zero_kernel, dim3(grid), dim3(kRowThreads), 0, stream, static_cast<char*>(p), bytes);
+    return hipGetLastError();
+}
+
+}  // namespace dmuon
