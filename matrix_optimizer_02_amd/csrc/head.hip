@@ -22,8 +22,6 @@ namespace {
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 int64_t ceil_div(int64_t x, int64_t a) { return (x + a - 1) / a; }
 
-// Workgroups that fill the chip.
-constexpr int64_t kFill = 256;
 // Bytes of ds a piece of the vocabulary may take (one part): it is written
 // once and read by two products, so it should stay in the 256 MB last-level
 // cache next to what those stream.
@@ -40,34 +38,102 @@ dmuon_status check_desc(const dmuon_head_desc* d) {
     return DMUON_OK;
 }
 
-HeadLayout layout_of(const dmuon_head_desc& d, bool backward) {
+// Tiles with the time a workgroup takes for 64 of K, in microseconds, when it has
+// the chip to itself (loads' latency) and when every slot is taken, and per tile.
+struct TileCost {
+    HeadTile tile;
+    double alone, full, fixed;
+};
+constexpr TileCost kTiles[] = {
+    {{256, 256}, 1.2, 1.9, 6.0}, {{256, 128}, 0.63, 1.09, 4.0}, {{256, 64}, 0.5, 1.05, 3.0}, {{64, 64}, 0.18, 0.54, 2.0}};
+
+// Estimated microseconds of `tiles` tiles of `slabs` slabs each: rounds of the
+// chip's slots.
+double rounds_cost(const TileCost& c, int64_t tiles, double slabs) {
+    const int64_t slots = head_slots(c.tile.tp);
+    const double busy = std::min(1.0, (double)tiles / slots);
+    return (double)ceil_div(tiles, slots) * (slabs * (c.alone + (c.full - c.alone) * busy) + c.fixed);
+}
+
+// The tile of a product with p rows of P, q of Q and K of `slabs` slabs.
+HeadTile pick_tile(int64_t p, int64_t q, double slabs, int max_tq) {
+    HeadTile best{256, max_tq};
+    double least = 1e300;
+    for (const TileCost& c : kTiles) {
+        if (c.tile.tq > max_tq) continue;
+        const double cost = rounds_cost(c, ceil_div(p, c.tile.tp) * ceil_div(q, c.tile.tq), slabs);
+        if (cost < least) {
+            least = cost;
+            best = c.tile;
+        }
+    }
+    return best;
+}
+
+// The same for dH, whose K axis, the vocabulary, is split until every slot of
+// the chip has a tile; the splits' fp32 sums are written and read once more.
+HeadTile pick_split_tile(int64_t p, int64_t q, double slabs, int max_tq, int64_t* splits) {
+    HeadTile best{256, max_tq};
+    double least = 1e300;
+    for (const TileCost& c : kTiles) {
+        if (c.tile.tq > max_tq) continue;
+        const int64_t tiles = ceil_div(p, c.tile.tp) * ceil_div(q, c.tile.tq);
+        const int64_t s = std::max<int64_t>(1, std::min<int64_t>(head_slots(c.tile.tp) / tiles, (int64_t)slabs));
+        const double sums = 8.0 * s * tiles * c.tile.tp * c.tile.tq / 4e6;  // at 4 TB/s
+        const double cost = rounds_cost(c, tiles * s, std::ceil(slabs / s)) + sums;
+        if (cost < least) {
+            least = cost;
+            best = c.tile;
+            *splits = s;
+        }
+    }
+    return best;
+}
+
+HeadLayout layout_of(dmuon_head_desc d, bool backward) {
     HeadLayout L{};
+    d.tokens = std::max<int64_t>(d.tokens, 1);
     L.tokens = d.tokens;
     L.hidden = d.hidden;
     L.vocab = d.vocab;
     L.top_k = d.top_k;
     L.planes = head_planes(d.dtype);
     L.esize = d.dtype == DMUON_BF16 ? 2 : 4;
-    L.tq = d.tokens <= 64 ? 64 : 256;
     L.t_pad = std::max<int64_t>(round_up(d.tokens, kHeadTile), kHeadTile);
-    L.d_pad = std::max<int64_t>(round_up(d.hidden, kHeadSlab), kHeadMinK);
+    L.d_pad = round_up(d.hidden, kHeadSlab);
     // bf16 rows of whole slabs are read in place; others go through a padded copy
     L.pack_weight = L.planes > 1 || d.hidden != L.d_pad;
+    // ... unless tokens are few: then the copy costs more than what the stream kernels
+    // lose per tile.  Measured (us, stream against copy): bf16 256 x 4090 x 50000
+    // forward 314 / 443, 512 tokens 573 / 534; backward without dW 128 tokens 360 / 502,
+    // 256 tokens 668 / 567; fp32 forward 256 tokens 883 / 1247, 512 x 1000 x 32000 219 /
+    // 153; backward without dW 512 x 1000 x 32000 426 / 429, 256 x 4090 x 50000 1531 / 2171.
+    const int64_t few = !backward ? 256 : L.planes > 1 ? 512 : 128;
+    L.stream_weight = L.pack_weight && d.tokens <= few;
+    if (L.stream_weight) L.pack_weight = 0;
     const int64_t v_pad = round_up(d.vocab, kHeadTile);
     const int64_t fit = kPieceBytes / (L.t_pad * 2 * L.planes) / kHeadTile * kHeadTile;
     int64_t piece = std::max(fit, kPieceMin);
-    if (L.pack_weight) {  // ... and the copy of W's piece
+    if (L.pack_weight) {  // ... and the copies of W's piece
         const int64_t w = (2 * kPieceBytes) / (L.d_pad * 2 * L.planes) / kHeadTile * kHeadTile;
         piece = std::min(piece, std::max(w, kPieceMin));
     }
     L.pieces = (int32_t)ceil_div(v_pad, piece);
     L.piece = round_up(ceil_div(v_pad, L.pieces), kHeadTile);
     L.pieces = (int32_t)ceil_div(v_pad, L.piece);
-    // dH has few tiles when tokens are few: its K axis, the vocabulary, is split
-    const int64_t dh_tiles = ceil_div(L.t_pad, L.tq) * ceil_div(L.hidden, kHeadTile);
-    int64_t splits = std::max<int64_t>(1, kFill / dh_tiles);
-    L.split_k = round_up(ceil_div(L.piece, splits), kHeadMinK);
-    L.splits = (int32_t)ceil_div(L.piece, L.split_k);
+    const bool f32 = L.planes > 1;
+    // one launch covers the vocabulary (forward, read in place) or a piece of it
+    const int64_t s_rows = backward || L.pack_weight ? L.piece : v_pad;
+    const int max_tq = L.stream_weight ? 128 : 256;
+    const double s_slabs = (double)(L.d_pad / kHeadSlab) * (!f32 ? 1 : L.stream_weight ? 6 : 3);
+    L.s_tile = pick_tile(std::min(s_rows, d.vocab), d.tokens, s_slabs, max_tq);
+    const double parts = f32 ? 6 : 1;
+    L.dw_tile = pick_tile(d.hidden, std::min(L.piece, d.vocab), (double)ceil_div(d.tokens, kHeadSlab) * parts, 256);
+    const int64_t k = round_up(std::min(L.piece, d.vocab), kHeadSlab);  // of the first, longest piece
+    int64_t splits = 1;
+    L.dh_tile = pick_split_tile(d.hidden, d.tokens, (double)(k / kHeadSlab) * parts, max_tq, &splits);
+    L.split_k = round_up(ceil_div(k, std::min(splits, k / kHeadSlab)), kHeadSlab);
+    L.splits = (int32_t)ceil_div(k, L.split_k);
 
     size_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -84,14 +150,21 @@ HeadLayout layout_of(const dmuon_head_desc& d, bool backward) {
     L.off_tl = take(4 * L.t_pad);
     L.off_q = take(8 * L.t_pad);
     L.off_flag = take(4 * L.t_pad);
-    L.off_h = take(2 * L.planes * L.t_pad * L.d_pad);
+    if (!f32 || backward || L.stream_weight) L.off_h = take(2 * L.planes * L.t_pad * L.d_pad);
     // a packed piece of W, or the copy of its last, partial tile
-    L.off_w = take(L.pack_weight ? 2 * L.planes * L.piece * L.d_pad : 2 * kHeadTile * L.d_pad);
+    if (!L.pack_weight && !L.stream_weight) L.off_w = take(2 * kHeadTile * L.d_pad);
+    else if (L.pack_weight && (!f32 || backward)) L.off_w = take(2 * L.planes * L.piece * L.d_pad);
+    if (f32 && L.pack_weight) {
+        L.off_h2 = take(4 * L.t_pad * L.d_pad);
+        L.off_hs = take(4 * L.t_pad);
+        L.off_w2 = take(4 * L.piece * L.d_pad);
+        L.off_ws = take(4 * L.piece);
+    }
     if (backward) {
         L.off_g = take(2 * L.planes * L.t_pad * L.piece);
-        L.off_dh = take(4 * L.splits * round_up(L.t_pad, L.tq) * round_up(L.hidden, kHeadTile));
+        L.off_dh = take(4 * L.splits * L.t_pad * round_up(L.hidden, kHeadTile));
     } else {
-        L.off_part = take(8 * (v_pad / kHeadTile) * head_wave_rows(L.tq) * L.t_pad);
+        L.off_part = take(8 * (v_pad / L.s_tile.tp) * head_wave_rows(L.s_tile.tp, L.s_tile.tq) * L.t_pad);
     }
     L.bytes = at;
     return L;
@@ -193,7 +266,7 @@ HeadTeacher teacher_of(const Call& c) {
 }
 
 // Which rows carry a loss, and their hidden states packed together.
-dmuon_status gather_rows(const Call& c, const Views& v, float* losses, float* lse, float* student) {
+dmuon_status gather_rows(const Call& c, const Views& v, bool backward, float* losses, float* lse, float* student) {
     const HeadLayout& L = v.L;
     if (c.ids != nullptr) HEAD_TRY(launch_head_teacher(teacher_of(c), L.tokens, v.q(), v.flag(), student, c.stream));
     HeadRowsArgs r{};
@@ -216,30 +289,38 @@ dmuon_status gather_rows(const Call& c, const Views& v, float* losses, float* ls
     p.src = v.src();
     p.count = v.count();
     p.rows = L.tokens;
-    p.out = v.at<uint16_t>(L.off_h);
+    p.out = L.planes == 1 || backward || L.stream_weight ? v.at<uint16_t>(L.off_h) : nullptr;
     p.out_rows = L.t_pad;
     p.ld = L.d_pad;
     p.plane = L.t_pad * L.d_pad;
-    p.planes = L.planes;
+    p.half2 = L.pack_weight ? v.at<uint16_t>(L.off_h2) : nullptr;
+    p.scale = v.at<float>(L.off_hs);
     HEAD_TRY(launch_head_pack(p, c.stream));
     return DMUON_OK;
 }
 
 // vocab rows [v0, v0 + rows) of W as the products' P operand: in place, with
 // the last partial tile copied, or packed.
-dmuon_status weight_piece(const Call& c, const Views& v, int64_t v0, int64_t rows, HeadGemmArgs& a) {
+dmuon_status weight_piece(const Call& c, const Views& v, bool backward, int64_t v0, int64_t rows, HeadGemmArgs& a) {
     const HeadLayout& L = v.L;
     const int64_t left = std::min(rows, L.vocab - v0);  // real rows
     const char* w = static_cast<const char*>(c.weight) + v0 * L.hidden * L.esize;
     HeadPackArgs p{};
     p.esize = L.esize;
     p.cols = L.hidden;
-    p.out = v.at<uint16_t>(L.off_w);
+    p.out = L.planes == 1 || backward ? v.at<uint16_t>(L.off_w) : nullptr;
     p.ld = L.d_pad;
-    p.planes = L.planes;
+    p.half2 = v.at<uint16_t>(L.off_w2);
+    p.scale = v.at<float>(L.off_ws);
     a.tail_row = INT_MAX;
     a.p_tail = nullptr;
     a.p_ld = (int32_t)L.d_pad;
+    if (L.stream_weight) {
+        a.p = w;
+        a.p_ld = (int32_t)L.hidden;
+        a.p_rows = left;
+        return DMUON_OK;
+    }
     if (L.pack_weight) {
         p.in = w;
         p.rows = left;
@@ -273,13 +354,27 @@ void logits_args(const Call& c, const Views& v, int64_t v0, int64_t rows, HeadGe
     a.q_plane = 2 * L.t_pad * L.d_pad;
     a.parts = L.planes;
     a.k = (int32_t)L.d_pad;
-    a.tiles_i = (int32_t)ceil_div(std::min(rows, L.vocab - v0), kHeadTile);
+    if (L.planes > 1 && !L.stream_weight) {
+        a.p = v.ws + L.off_w2;
+        a.q = v.ws + L.off_h2;
+        a.p_ld = a.q_ld = a.k = (int32_t)(2 * L.d_pad);
+        a.p_scale = v.at<float>(L.off_ws);
+        a.q_scale = v.at<float>(L.off_hs);
+    }
+    a.tiles_i = (int32_t)ceil_div(std::min(rows, L.vocab - v0), L.s_tile.tp);
     a.v0 = v0;
     a.vocab = L.vocab;
     a.inv_temp = 1.f / c.temp;
     a.target = c.ids != nullptr ? nullptr : v.target();
     a.t_pad = L.t_pad;
-    a.first_tile = (int32_t)(v0 / kHeadTile);
+    a.first_tile = (int32_t)(v0 / L.s_tile.tp);
+}
+
+// A product with W as its P operand.
+hipError_t launch_w(int mode, const HeadLayout& L, HeadTile tile, const HeadGemmArgs& a, int64_t max_tiles,
+                    hipStream_t stream) {
+    return L.stream_weight ? launch_head_stream(mode, tile, a, max_tiles, stream)
+                           : launch_head_gemm(mode, tile, a, max_tiles, stream);
 }
 
 dmuon_status forward(const Call& c, bool distill, float* losses, float* lse, float* student) {
@@ -296,25 +391,25 @@ dmuon_status forward(const Call& c, bool distill, float* losses, float* lse, flo
     if (st != DMUON_OK) return st;
 
     const Views v{static_cast<char*>(c.workspace), L};
-    st = gather_rows(c, v, losses, lse, student);
+    st = gather_rows(c, v, false, losses, lse, student);
     if (st != DMUON_OK) return st;
     // read in place, the whole vocabulary is one launch
     const int64_t step = L.pack_weight ? L.piece : round_up(L.vocab, kHeadTile);
     for (int64_t v0 = 0; v0 < L.vocab; v0 += step) {
         HeadGemmArgs a{};
-        st = weight_piece(c, v, v0, step, a);
+        st = weight_piece(c, v, false, v0, step, a);
         if (st != DMUON_OK) return st;
         logits_args(c, v, v0, step, a);
         a.part = v.at<float2>(L.off_part);
         a.target_logit = v.target_logit();
-        HEAD_TRY(launch_head_gemm(kHeadLse, L.tq, a, (int64_t)a.tiles_i * ceil_div(L.tokens, L.tq), c.stream));
+        HEAD_TRY(launch_w(kHeadLse, L, L.s_tile, a, (int64_t)a.tiles_i * ceil_div(L.tokens, L.s_tile.tq), c.stream));
     }
     HeadMergeArgs m{};
     m.count = v.count();
     m.src = v.src();
     m.part = v.at<float2>(L.off_part);
     m.t_pad = L.t_pad;
-    m.parts = (int32_t)ceil_div(L.vocab, kHeadTile) * head_wave_rows(L.tq);
+    m.parts = (int32_t)ceil_div(L.vocab, L.s_tile.tp) * head_wave_rows(L.s_tile.tp, L.s_tile.tq);
     m.tokens = L.tokens;
     m.inv_temp = 1.f / c.temp;
     m.target = distill ? nullptr : v.target();
@@ -367,7 +462,7 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
     if (st != DMUON_OK) return st;
 
     const Views v{static_cast<char*>(c.workspace), L};
-    st = gather_rows(c, v, nullptr, nullptr, nullptr);
+    st = gather_rows(c, v, true, nullptr, nullptr, nullptr);
     if (st != DMUON_OK) return st;
     HeadCoefArgs k{};
     k.count = v.count();
@@ -383,12 +478,12 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
     k.ct = v.ct();
     k.t_pad = L.t_pad;
     HEAD_TRY(launch_head_coef(k, c.stream));
-    const int64_t t_tiles = ceil_div(L.tokens, L.tq);
-    const int32_t d_tiles = (int32_t)ceil_div(L.hidden, kHeadTile);
+    const int64_t dh_tiles_j = ceil_div(L.tokens, L.dh_tile.tq);
+    const int32_t dh_tiles_i = (int32_t)ceil_div(L.hidden, L.dh_tile.tp);
     for (int64_t v0 = 0; v0 < L.vocab; v0 += L.piece) {
         const int64_t left = std::min(L.piece, L.vocab - v0);
         HeadGemmArgs w{};
-        st = weight_piece(c, v, v0, L.piece, w);
+        st = weight_piece(c, v, true, v0, L.piece, w);
         if (st != DMUON_OK) return st;
         HeadGemmArgs a = w;
         logits_args(c, v, v0, L.piece, a);
@@ -398,8 +493,8 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
         a.g = v.ws + L.off_g;
         a.g_plane = 2 * L.t_pad * L.piece;
         a.g_ld = (int32_t)L.piece;
-        const int64_t g_tiles = ceil_div(std::max<int64_t>(L.tokens, kHeadMinK), L.tq);
-        HEAD_TRY(launch_head_gemm(kHeadGrad, L.tq, a, a.tiles_i * g_tiles, c.stream));
+        const int64_t g_tiles = ceil_div(round_up(L.tokens, kHeadSlab), L.s_tile.tq);
+        HEAD_TRY(launch_w(kHeadGrad, L, L.s_tile, a, a.tiles_i * g_tiles, c.stream));
         if (distill) {
             HeadFixArgs f{};
             f.count = v.count();
@@ -425,13 +520,13 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
             h.q_ld = (int32_t)L.piece;
             h.q_plane = 2 * L.t_pad * L.piece;
             h.parts = L.planes;
-            h.k = (int32_t)round_up(left, kHeadTile);
+            h.k = (int32_t)round_up(left, kHeadSlab);
             h.split_k = (int32_t)L.split_k;
             h.splits = (int32_t)ceil_div(h.k, L.split_k);
-            h.tiles_i = d_tiles;
+            h.tiles_i = dh_tiles_i;
             h.dh = v.at<float>(L.off_dh);
             h.accumulate = v0 != 0;
-            HEAD_TRY(launch_head_gemm(kHeadDh, L.tq, h, h.splits * d_tiles * t_tiles, c.stream));
+            HEAD_TRY(launch_w(kHeadDh, L, L.dh_tile, h, h.splits * dh_tiles_i * dh_tiles_j, c.stream));
         }
         if (grad_weight != nullptr) {
             HeadGemmArgs g{};
@@ -444,12 +539,12 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
             g.q_ld = (int32_t)L.piece;
             g.q_plane = 2 * L.t_pad * L.piece;
             g.parts = L.planes;
-            g.tiles_i = d_tiles;
-            g.tiles_j = (int32_t)ceil_div(left, kHeadTile);
+            g.tiles_i = (int32_t)ceil_div(L.hidden, L.dw_tile.tp);
+            g.tiles_j = (int32_t)ceil_div(left, L.dw_tile.tq);
             g.dw = static_cast<char*>(grad_weight) + v0 * L.hidden * L.esize;
             g.dw_rows = left;
             g.dw_ld = (int32_t)L.hidden;
-            HEAD_TRY(launch_head_gemm(kHeadDw, 256, g, (int64_t)g.tiles_i * g.tiles_j, c.stream));
+            HEAD_TRY(launch_head_gemm(kHeadDw, L.dw_tile, g, (int64_t)g.tiles_i * g.tiles_j, c.stream));
         }
     }
     if (grad_hidden != nullptr) {
@@ -458,8 +553,8 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
         h.src = v.src();
         h.dh = v.at<float>(L.off_dh);
         h.splits = L.splits;
-        h.tiles_i = d_tiles;
-        h.tq = L.tq;
+        h.tiles_i = dh_tiles_i;
+        h.tile = L.dh_tile;
         h.out = grad_hidden;
         h.esize = L.esize;
         h.tokens = L.tokens;
@@ -476,11 +571,11 @@ extern "C" dmuon_status head_loss_workspace_bytes(const dmuon_head_desc* desc, i
     const dmuon_status st = check_desc(desc);
     if (st != DMUON_OK) return st;
     // the cut depends on the number of tokens, so a shorter batch may need more:
-    // the largest over all of them, one per layout (tokens enter as 64 or fewer,
-    // then in whole tiles)
+    // the largest over all of them (tokens enter a layout in steps of the smallest
+    // tile edge)
     dmuon_head_desc d = *desc;
     size_t most = 0;
-    for (int64_t t = std::min<int64_t>(64, desc->tokens);; t = std::min(round_up(t + 1, kHeadTile), desc->tokens)) {
+    for (int64_t t = std::min<int64_t>(64, desc->tokens);; t = std::min(round_up(t + 1, 64), desc->tokens)) {
         d.tokens = t;
         most = std::max(most, layout_of(d, backward != 0).bytes);
         if (t == desc->tokens) break;

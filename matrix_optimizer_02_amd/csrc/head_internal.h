@@ -18,29 +18,46 @@ constexpr int64_t kHeadMaxVocab = (int64_t(1) << 27) - 1;
 constexpr int32_t kHeadMaxTopK = 1024;
 constexpr int64_t kHeadMaxLogits = int64_t(1) << 42;  // tokens x vocab: keeps every launch's tile count in 31 bits
 
-constexpr int kHeadTile = 256;  // rows of the P operand a tile covers (vocab, or hidden columns)
+constexpr int kHeadTile = 256;  // every tile edge divides it: arrays are padded to it
 constexpr int kHeadSlab = 64;   // K slab
-constexpr int kHeadMinK = 128;  // K extents are padded to at least two slabs
 constexpr int kHeadMaxPlanes = 3;
 
-// bf16 parts of an operand element: 1 (bf16) or 3 (fp32).
+// Parts of an operand element.
+enum HeadKind : int32_t {
+    kHeadBf16 = 0,    // as it is
+    kHeadHalf2 = 1,   // fp32 as two fp16 parts, rows scaled (logits)
+    kHeadBf16x3 = 2   // fp32 as three bf16 parts (gradients)
+};
+// bf16 parts of the gradients' operands: 1 (bf16) or 3 (fp32).
 inline int head_planes(int32_t dtype) { return dtype == DMUON_BF16 ? 1 : kHeadMaxPlanes; }
+
+// An output tile: tp rows of P by tq rows of Q.
+struct HeadTile {
+    int32_t tp, tq;
+};
+constexpr int head_waves(int tp) { return tp == 64 ? 4 : 8; }
+// Waves along a tile's P rows: rows of statistics written per vocab tile.
+constexpr int head_wave_rows(int tp, int tq) { return tp == 64 || tq == 256 ? 2 : 4; }
+// Workgroups the chip holds at once (two of the 64 x 64 tiles' to a CU).
+constexpr int head_slots(int tp) { return tp == 64 ? 512 : 256; }
 
 // Where everything lies in the workspace, and how the work is cut.
 struct HeadLayout {
     int64_t tokens, hidden, vocab;
     int32_t top_k, planes, esize;
-    int32_t tq;             // token rows a tile of the logits covers (64 or 256)
+    HeadTile s_tile, dh_tile, dw_tile;  // of the logits, dH and dW
     int64_t t_pad;          // token rows of the padded arrays (multiple of 256)
-    int64_t d_pad;          // K extent of packed rows (multiple of 64, >= 128)
+    int64_t d_pad;          // K extent of packed rows (multiple of 64)
     int32_t pack_weight;    // 1: pieces of W are copied (split) into the workspace
+    int32_t stream_weight;  // 1: the stream kernels read W in place
     int64_t piece;          // vocab rows of a piece (multiple of 256)
     int32_t pieces;
-    int64_t split_k;        // dH: vocab rows of a split (multiple of 128)
+    int64_t split_k;        // dH: vocab rows of a split (multiple of 64)
     int32_t splits;         // ... splits of a full piece
     // byte offsets
     size_t off_count, off_src, off_tgt, off_lse, off_cp, off_ct, off_tl, off_q, off_flag;
     size_t off_h, off_w, off_part, off_g, off_dh;
+    size_t off_h2, off_w2, off_hs, off_ws;  // fp32: the logits' operands and their row scales
     size_t bytes;
 };
 
@@ -59,8 +76,10 @@ struct HeadGemmArgs {
     int32_t tail_row;            // ... which stands for P rows >= tail_row of this piece (INT32_MAX: none)
     const char* q;
     int64_t p_plane, q_plane;    // bytes between the parts of an operand
+    const float *p_scale, *q_scale;  // fp32 logits: what the rows' products are multiplied by
     int32_t p_ld, q_ld;          // elements between rows
-    int32_t parts;               // bf16 parts of the operands: 1, or 3 (six products)
+    int64_t p_rows;              // rows of W left from the piece's first (stream kernels)
+    int32_t parts;               // 1: bf16; 3: fp32
     int32_t k;                   // K extent (dH: of the piece; dW: taken from count)
     int32_t split_k, splits;     // dH
     int32_t tiles_i;             // tiles along P's rows (or columns)
@@ -87,9 +106,10 @@ struct HeadGemmArgs {
     int32_t dw_ld;               // hidden
 };
 
-hipError_t launch_head_gemm(int mode, int tq, const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream);
-// Waves along a tile's P rows: statistics rows written per vocab tile.
-inline int head_wave_rows(int tq) { return tq == 256 ? 2 : 4; }
+hipError_t launch_head_gemm(int mode, HeadTile tile, const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream);
+// The same with W read in place whatever its width and type (Lse, Grad, dH;
+// tiles 256 x 128, 256 x 64 and 64 x 64).
+hipError_t launch_head_stream(int mode, HeadTile tile, const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream);
 
 // ---- row kernels (k_head_rows.hip) ---------------------------------------------
 
@@ -129,9 +149,10 @@ struct HeadPackArgs {
     const int32_t* src;
     const int32_t* count;  // device row count, or null:
     int64_t rows;          // rows of the input
-    uint16_t* out;
+    uint16_t* out;         // bf16: the rows; fp32: three bf16 parts (null: not)
     int64_t out_rows, ld, plane;  // plane in elements
-    int32_t planes;
+    uint16_t* half2;       // fp32: 32 hi, 32 lo fp16 values of every 32 columns, rows of 2 ld
+    float* scale;          // ... and the factor that restores a row's scale
 };
 hipError_t launch_head_pack(const HeadPackArgs& a, hipStream_t stream);
 // Joins the tiles' softmax statistics: lse (compact, natural units) and, for
@@ -207,7 +228,7 @@ struct HeadDhArgs {
     const float* dh;
     int32_t splits;
     int32_t tiles_i;
-    int32_t tq;
+    HeadTile tile;
     void* out;
     int32_t esize;
     int64_t tokens, cols;

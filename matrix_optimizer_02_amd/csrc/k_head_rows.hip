@@ -97,8 +97,46 @@ __global__ __launch_bounds__(kScanThreads) void head_rows_kernel(HeadRowsArgs a)
     if (threadIdx.x == 0) *a.count = n;
 }
 
-// One block per output row (grid-stride), 8 columns per thread and step.
-template <int ESIZE, int PLANES>
+// Eight columns c .. c + 7 of a row, zeros past its end.
+template <int ESIZE>
+__device__ __forceinline__ void load_cols(const void* in, int64_t row, int64_t cols, int64_t c, bool vec, float (&x)[8]) {
+    #pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    if (ESIZE == 2) {
+        const uint16_t* p = static_cast<const uint16_t*>(in) + row * cols + c;
+        if (vec && c < cols) {
+            const uint4 u = *reinterpret_cast<const uint4*>(p);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            #pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = bf16_to_f32((uint16_t)(w[e / 2] >> (16 * (e & 1))));
+        } else {
+            #pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < cols) x[e] = bf16_to_f32(p[e]);
+        }
+    } else {
+        const float* p = static_cast<const float*>(in) + row * cols + c;
+        if (vec && c < cols) {
+            const float4 u = reinterpret_cast<const float4*>(p)[0], v = reinterpret_cast<const float4*>(p)[1];
+            x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+            x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+        } else {
+            #pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < cols) x[e] = p[e];
+        }
+    }
+}
+
+__device__ __forceinline__ uint4 pack_bf16(const float (&x)[8]) {
+    uint32_t w[4];
+    #pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = (uint32_t)f32_to_bf16(x[2 * e]) | ((uint32_t)f32_to_bf16(x[2 * e + 1]) << 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One wave per output row, 8 columns a lane and step.
+template <int ESIZE>
 __global__ __launch_bounds__(kRowThreads) void head_pack_kernel(HeadPackArgs a) {
     const int64_t limit = a.count != nullptr ? *a.count : a.rows;
     // rows past the last one: zeros up to a whole tile
@@ -106,48 +144,65 @@ __global__ __launch_bounds__(kRowThreads) void head_pack_kernel(HeadPackArgs a) 
     if (end == 0) end = kHeadTile;
     if (end > a.out_rows) end = a.out_rows;
     const bool vec = a.cols % 8 == 0;
-    for (int64_t r = blockIdx.x; r < end; r += gridDim.x) {
+    const int lane = threadIdx.x & 63;
+    constexpr int kWavesBlock = kRowThreads / 64;
+    for (int64_t r = (int64_t)blockIdx.x * kWavesBlock + (threadIdx.x >> 6); r < end; r += (int64_t)gridDim.x * kWavesBlock) {
         const int64_t from = r < limit ? (a.src != nullptr ? (int64_t)a.src[r] : r) : -1;
-        for (int64_t c = threadIdx.x * 8; c < a.ld; c += kRowThreads * 8) {
-            float x[8];
-            #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = 0.f;
-            if (from >= 0) {
-                if (ESIZE == 2) {
-                    const uint16_t* p = static_cast<const uint16_t*>(a.in) + from * a.cols + c;
-                    if (vec && c < a.cols) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(p);
-                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-                        #pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = bf16_to_f32((uint16_t)(w[e / 2] >> (16 * (e & 1))));
-                    } else {
-                        #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (c + e < a.cols) x[e] = bf16_to_f32(p[e]);
-                    }
-                } else {
-                    const float* p = static_cast<const float*>(a.in) + from * a.cols + c;
-                    if (vec && c < a.cols) {
-                        const float4 u = reinterpret_cast<const float4*>(p)[0], v = reinterpret_cast<const float4*>(p)[1];
-                        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
-                        x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
-                    } else {
-                        #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (c + e < a.cols) x[e] = p[e];
-                    }
+        float scale = 1.f;
+        if (ESIZE == 4 && a.half2 != nullptr) {
+            // a power of two that puts the row's largest element in [2^14, 2^15)
+            float m = 0.f;
+            if (from >= 0)
+                for (int64_t c = lane * 8; c < a.cols; c += 512) {
+                    float x[8];
+                    load_cols<ESIZE>(a.in, from, a.cols, c, vec, x);
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
                 }
+            m = wave_max(m);
+            // exponents below 2^-100 would need a scale past fp32's range
+            const int e = min(max((int)(__float_as_uint(m) >> 23), 27), 254);
+            scale = __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
+            if (lane == 0) a.scale[r] = 1.f / scale;
+        }
+        #pragma unroll 2
+        for (int64_t c = lane * 8; c < a.ld; c += 512) {
+            float x[8];
+            if (from >= 0) {
+                load_cols<ESIZE>(a.in, from, a.cols, c, vec, x);
+            } else {
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = 0.f;
             }
+            if (ESIZE == 2) {
+                *reinterpret_cast<uint4*>(a.out + r * a.ld + c) = pack_bf16(x);
+                continue;
+            }
+            if (a.half2 != nullptr) {
+            uint16_t h[2][8];
             #pragma unroll
-            for (int part = 0; part < PLANES; ++part) {
+            for (int e = 0; e < 8; ++e) {
+                const float y = x[e] * scale;
+                const _Float16 hi = (_Float16)y;
+                h[0][e] = __builtin_bit_cast(uint16_t, hi);
+                h[1][e] = __builtin_bit_cast(uint16_t, (_Float16)(y - (float)hi));
+            }
+            uint16_t* o = a.half2 + r * 2 * a.ld + (c / 32) * 64 + c % 32;
+            #pragma unroll
+            for (int part = 0; part < 2; ++part) {
                 uint32_t w[4];
                 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint16_t b = f32_to_bf16(x[e]);
-                    x[e] -= bf16_to_f32(b);
-                    if (e & 1) w[e / 2] |= (uint32_t)b << 16; else w[e / 2] = b;
+                for (int e = 0; e < 4; ++e) w[e] = (uint32_t)h[part][2 * e] | ((uint32_t)h[part][2 * e + 1] << 16);
+                *reinterpret_cast<uint4*>(o + 32 * part) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            }
+            if (a.out != nullptr) {
+                #pragma unroll
+                for (int part = 0; part < kHeadMaxPlanes; ++part) {
+                    *reinterpret_cast<uint4*>(a.out + part * a.plane + r * a.ld + c) = pack_bf16(x);
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] -= bf16_to_f32(f32_to_bf16(x[e]));
                 }
-                *reinterpret_cast<uint4*>(a.out + part * a.plane + r * a.ld + c) = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
     }
@@ -300,15 +355,16 @@ __global__ __launch_bounds__(kRowThreads) void head_fix_kernel(HeadFixArgs a) {
     }
 }
 
-// A block per tile quarter: the tile's sums in the product kernel's own order
-// (lane's four values are 4 consecutive columns of one row).
-template <int TQ>
+// A wave per 64 float4 of a tile's sums, in the product kernel's own order (a
+// lane's four values are 4 consecutive columns of one row).
 __global__ __launch_bounds__(kRowThreads) void head_dh_kernel(HeadDhArgs a) {
-    constexpr int WR = TQ == 256 ? 2 : 4, RW = kHeadTile / WR, CW = TQ / (8 / WR), FI = RW / 32, FJ = CW / 32;
-    constexpr int kGroups = 8 * FI * FJ * 4;  // of 64 float4
+    const int TP = a.tile.tp, TQ = a.tile.tq;
+    const int WR = head_wave_rows(TP, TQ), NW = head_waves(TP), RW = TP / WR, CW = TQ / (NW / WR);
+    const int FI = RW / 32, FJ = CW / 32;
+    const int kGroups = NW * FI * FJ * 4;
     const int n = *a.count;
     const int tiles_j = (n + TQ - 1) / TQ;
-    const int64_t per_split = (int64_t)tiles_j * a.tiles_i * (kHeadTile * TQ);
+    const int64_t per_split = (int64_t)tiles_j * a.tiles_i * (TP * TQ);
     const int lane = threadIdx.x & 63;
     const int64_t groups = (int64_t)tiles_j * a.tiles_i * kGroups;
     const int64_t step = (int64_t)gridDim.x * (kRowThreads / 64);
@@ -321,7 +377,7 @@ __global__ __launch_bounds__(kRowThreads) void head_dh_kernel(HeadDhArgs a) {
         const int wr = g % WR, wc = g / WR;
         const int64_t J = tile / a.tiles_i, I = tile % a.tiles_i;
         const int64_t c = J * TQ + wc * CW + 32 * j + (lane & 31);
-        const int64_t col = I * kHeadTile + wr * RW + 32 * i + 8 * v4 + 4 * (lane >> 5);
+        const int64_t col = I * TP + wr * RW + 32 * i + 8 * v4 + 4 * (lane >> 5);
         const float* p = a.dh + w * 256 + lane * 4;
         float4 s = *reinterpret_cast<const float4*>(p);
         for (int k = 1; k < a.splits; ++k) {
@@ -387,9 +443,9 @@ hipError_t launch_head_rows(const HeadRowsArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_head_pack(const HeadPackArgs& a, hipStream_t stream) {
-    const dim3 grid(blocks_for(a.out_rows, 1, 16384)), block(kRowThreads);
-    if (a.esize == 2) hipLaunchKernelGGL((head_pack_kernel<2, 1>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((head_pack_kernel<4, kHeadMaxPlanes>), grid, block, 0, stream, a);
+    const dim3 grid(blocks_for(a.out_rows, kRowThreads / 64, 8192)), block(kRowThreads);
+    if (a.esize == 2) hipLaunchKernelGGL((head_pack_kernel<2>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((head_pack_kernel<4>), grid, block, 0, stream, a);
     return hipGetLastError();
 }
 
@@ -420,8 +476,7 @@ hipError_t launch_head_fix(const HeadFixArgs& a, hipStream_t stream) {
 
 hipError_t launch_head_dh(const HeadDhArgs& a, hipStream_t stream) {
     const dim3 grid(blocks_for(a.tokens * ((a.cols + 255) / 256) * 64, kRowThreads, 8192)), block(kRowThreads);
-    if (a.tq == 256) hipLaunchKernelGGL((head_dh_kernel<256>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((head_dh_kernel<64>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL(head_dh_kernel, grid, block, 0, stream, a);
     return hipGetLastError();
 }
 
