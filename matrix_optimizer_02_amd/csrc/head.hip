@@ -26,6 +26,7 @@ int64_t ceil_div(int64_t x, int64_t a) { return (x + a - 1) / a; }
 // once and read by two products, so it should stay in the 256 MB last-level
 // cache next to what those stream.
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
+constexpr int64_t kLowTokens = 128;
 constexpr int64_t kPieceMin = 8192;  // vocab rows: fewer would leave dW's launch short of tiles
 
 dmuon_status check_desc(const dmuon_head_desc* d) {
@@ -124,14 +125,19 @@ HeadLayout layout_of(dmuon_head_desc d, bool backward) {
     const bool f32 = L.planes > 1;
     // one launch covers the vocabulary (forward, read in place) or a piece of it
     const int64_t s_rows = backward || L.pack_weight ? L.piece : v_pad;
-    const int max_tq = L.stream_weight ? 128 : 256;
+    // bf16 batches of few tokens hold ds in two bf16 parts: a few entries' roundings
+    // would not average out, and while W's bytes bound the call the further rows are
+    // next to free
+    L.low = backward && !f32 && d.tokens <= kLowTokens;
+    const int64_t ds_rows = L.low ? 2 * head_low_row((int)d.tokens) : d.tokens;
+    const int max_tq = L.stream_weight || L.low ? 128 : 256;
     const double s_slabs = (double)(L.d_pad / kHeadSlab) * (!f32 ? 1 : L.stream_weight ? 6 : 3);
     L.s_tile = pick_tile(std::min(s_rows, d.vocab), d.tokens, s_slabs, max_tq);
     const double parts = f32 ? 6 : 1;
-    L.dw_tile = pick_tile(d.hidden, std::min(L.piece, d.vocab), (double)ceil_div(d.tokens, kHeadSlab) * parts, 256);
+    L.dw_tile = pick_tile(d.hidden, std::min(L.piece, d.vocab), (double)ceil_div(ds_rows, kHeadSlab) * parts, 256);
     const int64_t k = round_up(std::min(L.piece, d.vocab), kHeadSlab);  // of the first, longest piece
     int64_t splits = 1;
-    L.dh_tile = pick_split_tile(d.hidden, d.tokens, (double)(k / kHeadSlab) * parts, max_tq, &splits);
+    L.dh_tile = pick_split_tile(d.hidden, ds_rows, (double)(k / kHeadSlab) * parts, max_tq, &splits);
     L.split_k = round_up(ceil_div(k, std::min(splits, k / kHeadSlab)), kHeadSlab);
     L.splits = (int32_t)ceil_div(k, L.split_k);
 
@@ -141,7 +147,8 @@ HeadLayout layout_of(dmuon_head_desc d, bool backward) {
         at += align_up((size_t)bytes);
         return o;
     };
-    L.off_count = take(4);
+    L.off_count = take(8);
+    L.off_norm = take(4);
     L.off_src = take(4 * L.t_pad);
     L.off_tgt = take(4 * L.t_pad);
     L.off_lse = take(4 * L.t_pad);
@@ -251,6 +258,7 @@ struct Views {
         return reinterpret_cast<T*>(ws + off);
     }
     int32_t* count() const { return at<int32_t>(L.off_count); }
+    float* norm() const { return at<float>(L.off_norm); }
     int32_t* src() const { return at<int32_t>(L.off_src); }
     int32_t* target() const { return at<int32_t>(L.off_tgt); }
     float* lse() const { return at<float>(L.off_lse); }
@@ -277,6 +285,8 @@ dmuon_status gather_rows(const Call& c, const Views& v, bool backward, float* lo
     r.tokens = (int32_t)L.tokens;
     r.t_pad = (int32_t)L.t_pad;
     r.count = v.count();
+    r.low = L.low;
+    r.norm = v.norm();
     r.src = v.src();
     r.target = v.target();
     r.losses = losses;
@@ -290,6 +300,7 @@ dmuon_status gather_rows(const Call& c, const Views& v, bool backward, float* lo
     p.count = v.count();
     p.rows = L.tokens;
     p.out = L.planes == 1 || backward || L.stream_weight ? v.at<uint16_t>(L.off_h) : nullptr;
+    p.low = L.low;
     p.out_rows = L.t_pad;
     p.ld = L.d_pad;
     p.plane = L.t_pad * L.d_pad;
@@ -476,9 +487,10 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
     k.lse_c = v.lse();
     k.cp = v.cp();
     k.ct = v.ct();
+    k.norm = v.norm();
     k.t_pad = L.t_pad;
     HEAD_TRY(launch_head_coef(k, c.stream));
-    const int64_t dh_tiles_j = ceil_div(L.tokens, L.dh_tile.tq);
+    const int64_t dh_tiles_j = ceil_div(L.low ? 2 * head_low_row((int)L.tokens) : L.tokens, L.dh_tile.tq);
     const int32_t dh_tiles_i = (int32_t)ceil_div(L.hidden, L.dh_tile.tp);
     for (int64_t v0 = 0; v0 < L.vocab; v0 += L.piece) {
         const int64_t left = std::min(L.piece, L.vocab - v0);
@@ -490,6 +502,8 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
         a.lse = v.lse();
         a.cp = v.cp();
         a.ct = v.ct();
+        a.norm = v.norm();
+        a.low = L.low;
         a.g = v.ws + L.off_g;
         a.g_plane = 2 * L.t_pad * L.piece;
         a.g_ld = (int32_t)L.piece;
@@ -504,6 +518,8 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
             f.student = student;
             f.lse_c = v.lse();
             f.cp = v.cp();
+            f.norm = v.norm();
+            f.low = L.low;
             f.g = v.at<uint16_t>(L.off_g);
             f.g_plane = L.t_pad * L.piece;
             f.g_ld = L.piece;
@@ -515,7 +531,7 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
         }
         if (grad_hidden != nullptr) {
             HeadGemmArgs h = w;
-            h.count = v.count();
+            h.count = v.count() + 1;
             h.q = v.ws + L.off_g;
             h.q_ld = (int32_t)L.piece;
             h.q_plane = 2 * L.t_pad * L.piece;
@@ -530,7 +546,8 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
         }
         if (grad_weight != nullptr) {
             HeadGemmArgs g{};
-            g.count = v.count();
+            g.count = v.count() + 1;
+            g.norm = v.norm();
             g.p = v.ws + L.off_h;
             g.p_ld = (int32_t)L.d_pad;
             g.p_plane = 2 * L.t_pad * L.d_pad;
@@ -551,6 +568,8 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
         HeadDhArgs h{};
         h.count = v.count();
         h.src = v.src();
+        h.norm = v.norm();
+        h.low = L.low;
         h.dh = v.at<float>(L.off_dh);
         h.splits = L.splits;
         h.tiles_i = dh_tiles_i;

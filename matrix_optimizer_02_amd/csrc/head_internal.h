@@ -31,6 +31,12 @@ enum HeadKind : int32_t {
 // bf16 parts of the gradients' operands: 1 (bf16) or 3 (fp32).
 inline int head_planes(int32_t dtype) { return dtype == DMUON_BF16 ? 1 : kHeadMaxPlanes; }
 
+// First row of the low parts of ds behind n token rows.
+#if defined(__HIPCC__)
+__host__ __device__
+#endif
+inline int head_low_row(int n) { return n <= kHeadSlab ? kHeadSlab : (n + kHeadSlab - 1) / kHeadSlab * kHeadSlab; }
+
 // An output tile: tp rows of P by tq rows of Q.
 struct HeadTile {
     int32_t tp, tq;
@@ -50,12 +56,13 @@ struct HeadLayout {
     int64_t d_pad;          // K extent of packed rows (multiple of 64)
     int32_t pack_weight;    // 1: pieces of W are copied (split) into the workspace
     int32_t stream_weight;  // 1: the stream kernels read W in place
+    int32_t low;            // 1: ds in two bf16 parts, the low ones as further token rows
     int64_t piece;          // vocab rows of a piece (multiple of 256)
     int32_t pieces;
     int64_t split_k;        // dH: vocab rows of a split (multiple of 64)
     int32_t splits;         // ... splits of a full piece
     // byte offsets
-    size_t off_count, off_src, off_tgt, off_lse, off_cp, off_ct, off_tl, off_q, off_flag;
+    size_t off_count, off_norm, off_src, off_tgt, off_lse, off_cp, off_ct, off_tl, off_q, off_flag;
     size_t off_h, off_w, off_part, off_g, off_dh;
     size_t off_h2, off_w2, off_hs, off_ws;  // fp32: the logits' operands and their row scales
     size_t bytes;
@@ -70,7 +77,7 @@ enum HeadMode : int32_t {
 };
 
 struct HeadGemmArgs {
-    const int32_t* count;        // token rows that carry a loss
+    const int32_t* count;        // token rows that carry a loss (dH, dW: rows of ds)
     const char* p;               // P operand of this piece
     const char* p_tail;          // a zero-padded copy of the last, partial vocab tile ...
     int32_t tail_row;            // ... which stands for P rows >= tail_row of this piece (INT32_MAX: none)
@@ -96,6 +103,8 @@ struct HeadGemmArgs {
     const float* lse;            // per compact row
     const float* cp;             // coefficient of p
     const float* ct;             // coefficient at the target
+    const float* norm;           // the largest coefficient: ds is held as multiples of it
+    int32_t low;                 // Grad: the rows' low parts go to head_low_row(n) rows further
     char* g;                     // ds out
     int64_t g_plane;             // bytes
     int32_t g_ld;
@@ -132,7 +141,9 @@ struct HeadRowsArgs {
     const int32_t* flag;
     int64_t ignore_index, vocab;
     int32_t tokens, t_pad;
-    int32_t* count;
+    int32_t* count;          // the rows, then the rows of ds
+    int32_t low;
+    float* norm;             // zeroed
     int32_t* src;
     int32_t* target;
     float* losses;
@@ -151,6 +162,7 @@ struct HeadPackArgs {
     int64_t rows;          // rows of the input
     uint16_t* out;         // bf16: the rows; fp32: three bf16 parts (null: not)
     int64_t out_rows, ld, plane;  // plane in elements
+    int32_t low;           // 1: every row again, head_low_row(count) rows further
     uint16_t* half2;       // fp32: 32 hi, 32 lo fp16 values of every 32 columns, rows of 2 ld
     float* scale;          // ... and the factor that restores a row's scale
 };
@@ -200,6 +212,7 @@ struct HeadCoefArgs {
     const float* grad_lse;  // or null
     float temp;
     float *lse_c, *cp, *ct;
+    float* norm;            // the largest |cp|, |ct|
     int64_t t_pad;
 };
 hipError_t launch_head_coef(const HeadCoefArgs& a, hipStream_t stream);
@@ -212,6 +225,8 @@ struct HeadFixArgs {
     const float* student;
     const float* lse_c;
     const float* cp;
+    const float* norm;
+    int32_t low;
     uint16_t* g;
     int64_t g_plane;  // elements
     int64_t g_ld;
@@ -225,6 +240,8 @@ hipError_t launch_head_fix(const HeadFixArgs& a, hipStream_t stream);
 struct HeadDhArgs {
     const int32_t* count;
     const int32_t* src;
+    const float* norm;
+    int32_t low;
     const float* dh;
     int32_t splits;
     int32_t tiles_i;

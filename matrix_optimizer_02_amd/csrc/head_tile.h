@@ -114,6 +114,14 @@ __device__ __forceinline__ Tile tile_at(const HeadGemmArgs& args, const Share& s
     return t;
 }
 
+// What ds is divided by before it is rounded: the largest coefficient, so that
+// equal weights of all tokens, the usual case, round no target's entry (1 - p
+// instead of w (1 - p), whose rounding all tokens would share).
+__device__ __forceinline__ float norm_of(const float* norm) {
+    const float x = *norm;
+    return x > 0.f ? x : 1.f;
+}
+
 // Writes a finished tile.  acc[i][j][v]: P row wr RW + 32 i + 8 (v / 4) + 4 khalf
 // + v % 4, Q row wc CW + 32 j + lrow.  SCALED: fp32 logits of scaled rows.  PARTS:
 // bf16 parts of the outputs (Grad) or an fp32 output (dW) where 3.
@@ -212,13 +220,14 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
                 }
     } else {
         if constexpr (MODE == kHeadGrad) {
+            const float inv_norm = 1.f / norm_of(args.norm);
             const int64_t v_base = args.v0 + (int64_t)t.I * TP + wr * C::RW;
             const int64_t left = args.vocab - v_base;
             const int limit = left < C::RW ? (int)(left < 0 ? 0 : left) : C::RW;
             #pragma unroll
             for (int j = 0; j < C::FJ; ++j) {
                 const int row = t.J * TQ + wc * C::CW + 32 * j + lrow;
-                const float lse = args.lse[row], cp = args.cp[row], ct = args.ct[row];
+                const float lse = args.lse[row], cp = args.cp[row] * inv_norm, ct = args.ct[row] * inv_norm;
                 const int64_t off = args.target != nullptr ? args.target[row] - v_base : -1;
                 const int at = off >= 0 && off < limit ? (int)off : -1;
                 #pragma unroll
@@ -231,6 +240,15 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
                         acc[i][j][v] = r < limit ? g : 0.f;
                     }
             }
+        }
+        if constexpr (MODE == kHeadDw) {
+            const float norm = norm_of(args.norm);
+            #pragma unroll
+            for (int i = 0; i < C::FI; ++i)
+                #pragma unroll
+                for (int j = 0; j < C::FJ; ++j)
+                    #pragma unroll
+                    for (int v = 0; v < 16; ++v) acc[i][j][v] *= norm;
         }
         if constexpr (MODE == kHeadDw && PARTS > 1) {
             float* dw = static_cast<float*>(args.dw);
@@ -259,8 +277,11 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
             }
         } else {
             // bf16 rows: staged through LDS as E[c][r], stored in whole 16-byte chunks
-            constexpr int kOut = MODE == kHeadGrad ? PARTS : 1;
+            // (256 token rows: never in two parts)
+            constexpr bool kSplit = MODE == kHeadGrad && (PARTS > 1 || TQ <= 128);
+            const int kOut = !kSplit ? 1 : PARTS > 1 ? PARTS : args.low + 1;
             constexpr int kEBytes = 2 * TP, kEChunks = TP / 8;
+            const int low_row = kSplit && PARTS == 1 && args.low ? head_low_row(*args.count) : 0;
             #pragma unroll 1
             for (int part = 0; part < kOut; ++part) {
                 __syncthreads();
@@ -276,7 +297,7 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
                             #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 b[e] = f32_to_bf16(acc[i][j][4 * v4 + e]);
-                                if (kOut > 1) acc[i][j][4 * v4 + e] -= bf16_to_f32(b[e]);
+                                if (kSplit) acc[i][j][4 * v4 + e] -= bf16_to_f32(b[e]);
                             }
                             uint2 o;
                             o.x = (uint32_t)b[0] | ((uint32_t)b[1] << 16);
@@ -290,8 +311,11 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
                     const uint4 v = *reinterpret_cast<const uint4*>(smem + c * kEBytes +
                                                                     ((ch ^ (c & (kEChunks - 1))) << 4));
                     if (MODE == kHeadGrad) {
-                        char* g = args.g + part * args.g_plane +
-                                  2 * ((int64_t)(t.J * TQ + c) * args.g_ld + t.I * TP + ch * 8);
+                        // the low parts' rows begin where this tile's padding may reach
+                        if (low_row != 0 && t.J * TQ + c >= low_row) continue;
+                        const int64_t row = t.J * TQ + c + part * low_row;
+                        char* g = args.g + (PARTS > 1 ? part * args.g_plane : 0) +
+                                  2 * (row * args.g_ld + t.I * TP + ch * 8);
                         *reinterpret_cast<uint4*>(g) = v;
                     } else {
                         const int64_t row = (int64_t)t.J * TQ + c;

@@ -94,7 +94,11 @@ __global__ __launch_bounds__(kScanThreads) void head_rows_kernel(HeadRowsArgs a)
     }
     if (a.targets != nullptr)
         for (int c = n + threadIdx.x; c < a.t_pad; c += kScanThreads) a.target[c] = -1;
-    if (threadIdx.x == 0) *a.count = n;
+    if (threadIdx.x == 0) {
+        a.count[0] = n;
+        a.count[1] = a.low ? 2 * head_low_row(n) : n;
+        *a.norm = 0.f;
+    }
 }
 
 // Eight columns c .. c + 7 of a row, zeros past its end.
@@ -144,10 +148,12 @@ __global__ __launch_bounds__(kRowThreads) void head_pack_kernel(HeadPackArgs a) 
     if (end == 0) end = kHeadTile;
     if (end > a.out_rows) end = a.out_rows;
     const bool vec = a.cols % 8 == 0;
+    const int64_t low_row = a.low ? head_low_row((int)limit) : end;
     const int lane = threadIdx.x & 63;
     constexpr int kWavesBlock = kRowThreads / 64;
     for (int64_t r = (int64_t)blockIdx.x * kWavesBlock + (threadIdx.x >> 6); r < end; r += (int64_t)gridDim.x * kWavesBlock) {
-        const int64_t from = r < limit ? (a.src != nullptr ? (int64_t)a.src[r] : r) : -1;
+        const int64_t of = r < low_row ? r : r - low_row;
+        const int64_t from = of < limit ? (a.src != nullptr ? (int64_t)a.src[of] : of) : -1;
         float scale = 1.f;
         if (ESIZE == 4 && a.half2 != nullptr) {
             // a power of two that puts the row's largest element in [2^14, 2^15)
@@ -319,6 +325,9 @@ __global__ __launch_bounds__(kRowThreads) void head_coef_kernel(HeadCoefArgs a) 
         ct = a.temp * a.grad_losses[t];
         cp = a.grad_lse != nullptr ? ct + a.grad_lse[t] : ct;
         const bool bad = a.target != nullptr ? a.target[c] < 0 : a.q[t].x != a.q[t].x;
+        // (integer order is float order for these bits; the maximum does not depend on the order)
+        const float m = fmaxf(fabsf(cp), fabsf(ct));
+        if (m < INFINITY) atomicMax(reinterpret_cast<unsigned int*>(a.norm), __float_as_uint(m));
         if (bad) cp = nan_f();
     }
     a.lse_c[c] = lse;
@@ -337,7 +346,9 @@ __global__ __launch_bounds__(kRowThreads) void head_fix_kernel(HeadFixArgs a) {
     const int64_t* ids = a.t.ids + row * a.t.k;
     const float* z = a.t.logits + row * a.t.k;
     const float2 qs = a.q[row];
-    const float cp = a.cp[c], lse = a.lse_c[c];
+    const float norm = *a.norm;
+    const float cp = a.cp[c] * (1.f / (norm > 0.f ? norm : 1.f)), lse = a.lse_c[c];
+    const int64_t low_step = a.low ? (int64_t)head_low_row(*a.count) * a.g_ld : a.g_plane;
     for (int k = lane; k < a.t.k; k += 64) {
         const int64_t id = ids[k];
         if (id < a.v0 || id >= a.v1) continue;
@@ -347,9 +358,9 @@ __global__ __launch_bounds__(kRowThreads) void head_fix_kernel(HeadFixArgs a) {
         const float p = expf(fmaf(a.student[row * a.t.k + k], a.t.inv_temp, -lse));
         float g = cp * (p - q);
         uint16_t* out = a.g + c * a.g_ld + (id - a.v0);
-        for (int part = 0; part < a.planes; ++part) {
+        for (int part = 0; part < (a.low ? 2 : a.planes); ++part) {
             const uint16_t b = f32_to_bf16(g);
-            out[part * a.g_plane] = b;
+            out[part * low_step] = b;
             g -= bf16_to_f32(b);
         }
     }
@@ -363,9 +374,11 @@ __global__ __launch_bounds__(kRowThreads) void head_dh_kernel(HeadDhArgs a) {
     const int FI = RW / 32, FJ = CW / 32;
     const int kGroups = NW * FI * FJ * 4;
     const int n = *a.count;
-    const int tiles_j = (n + TQ - 1) / TQ;
-    const int64_t per_split = (int64_t)tiles_j * a.tiles_i * (TP * TQ);
+    const int low_row = a.low ? head_low_row(n) : 0;
+    const int tiles_j = (n + TQ - 1) / TQ;  // of the rows themselves
+    const int64_t per_split = (int64_t)((a.low ? 2 * low_row : n) + TQ - 1) / TQ * a.tiles_i * (TP * TQ);
     const int lane = threadIdx.x & 63;
+    const float norm = *a.norm > 0.f ? *a.norm : 1.f;
     const int64_t groups = (int64_t)tiles_j * a.tiles_i * kGroups;
     const int64_t step = (int64_t)gridDim.x * (kRowThreads / 64);
     for (int64_t w = (int64_t)blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6); w < groups; w += step) {
@@ -376,14 +389,23 @@ __global__ __launch_bounds__(kRowThreads) void head_dh_kernel(HeadDhArgs a) {
         const int i = g % FI; g /= FI;
         const int wr = g % WR, wc = g / WR;
         const int64_t J = tile / a.tiles_i, I = tile % a.tiles_i;
-        const int64_t c = J * TQ + wc * CW + 32 * j + (lane & 31);
+        const int64_t c0 = J * TQ + wc * CW + 32 * j, c = c0 + (lane & 31);
         const int64_t col = I * TP + wr * RW + 32 * i + 8 * v4 + 4 * (lane >> 5);
-        const float* p = a.dh + w * 256 + lane * 4;
-        float4 s = *reinterpret_cast<const float4*>(p);
-        for (int k = 1; k < a.splits; ++k) {
-            const float4 u = *reinterpret_cast<const float4*>(p + k * per_split);
-            s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](int64_t group) {
+            const float* p = a.dh + group * 256 + lane * 4;
+            for (int k = 0; k < a.splits; ++k) {
+                const float4 u = *reinterpret_cast<const float4*>(p + k * per_split);
+                s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
+            }
+        };
+        if (low_row != 0 && c0 < low_row) {  // the 32 rows of the low parts first
+            const int64_t cl = c0 + low_row, Jl = cl / TQ;
+            const int in = (int)(cl - Jl * TQ), wl = in / CW * WR + wr, jl = in % CW / 32;
+            add((Jl * a.tiles_i + I) * kGroups + ((wl * FI + i) * FJ + jl) * 4 + v4);
         }
+        add(w);
+        s.x *= norm, s.y *= norm, s.z *= norm, s.w *= norm;
         if (c >= n || col >= a.cols) continue;
         const int64_t at = (int64_t)a.src[c] * a.cols + col;
         const float x[4] = {s.x, s.y, s.z, s.w};

@@ -12,7 +12,8 @@ With A = |H| |W|^T and u32 = 2^-24, u16 = 2^-8 (half a step of bf16):
         el = max es / T + (chain + 8) 2 u32 + 4 u32 xmax + 2 u32 |lse|
   * p = exp(s / T - lse): ep = p (es / T + el + 8 u32 (1 + |x|)), ds = cp p - ct q:
         ed = cp ep + 8 u32 (cp p + ct q) + ur |ds|,
-    ur the rounding of ds as an operand: u16 (bf16), 2^-22 (fp32, three parts);
+    ur the rounding of ds as an operand: u16 (bf16), 2^-15 (bf16 of at most 128
+    tokens: two parts leave u16^2), 2^-22 (fp32, three parts);
     below 2^-126 the device's exponentials and products may be 0, so p, cp p and
     ds are each also off by up to 2^-126: (cp + 2) 2^-126 more
   * dH = ds W:  ed |W| + (2 V' + 64) u32 |ds| |W| + out |dH|,  V' terms as D';
@@ -89,7 +90,7 @@ def bounds(o, h, w, tau, dtype, losses_extra=0.0):
     el = np.where(live, el, 0.0)
     b = {"es": es, "lse": el}
     if "ds" in o:
-        ur = U16 if dtype == BF16 else 2.0 ** -22
+        ur = 2.0 ** -22 if dtype == F32 else U16 if len(h) > 128 else 2.0 ** -15
         ep = o["p"] * (es / tau + el[:, None] + 8 * U32 * (1 + np.abs(x)))
         # a temperature scales s inside p only: ds carries it in cp and ct already
         ed = o["cp"] * ep + 8 * U32 * (o["cp"] * o["p"] + o["ct"] * o["hot"])
