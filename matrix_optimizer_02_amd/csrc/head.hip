@@ -71,16 +71,18 @@ HeadTile pick_tile(int64_t p, int64_t q, double slabs, int max_tq) {
     return best;
 }
 
-// The same for dH, whose K axis, the vocabulary, is split until every slot of
-// the chip has a tile; the splits' fp32 sums are written and read once more.
-HeadTile pick_split_tile(int64_t p, int64_t q, double slabs, int max_tq, int64_t* splits) {
+// The same for the gradients: the K axis (dH: the vocabulary, dW: the tokens) is
+// split until every slot of the chip has a tile; the splits' fp32 sums are written
+// and read once more (dH's always are: they add up over the pieces).
+HeadTile pick_split_tile(int64_t p, int64_t q, double slabs, int max_tq, bool sums_anyway, int64_t* splits) {
     HeadTile best{256, max_tq};
     double least = 1e300;
     for (const TileCost& c : kTiles) {
         if (c.tile.tq > max_tq) continue;
         const int64_t tiles = ceil_div(p, c.tile.tp) * ceil_div(q, c.tile.tq);
         const int64_t s = std::max<int64_t>(1, std::min<int64_t>(head_slots(c.tile.tp) / tiles, (int64_t)slabs));
-        const double sums = 8.0 * s * tiles * c.tile.tp * c.tile.tq / 4e6;  // at 4 TB/s
+        // at 4 TB/s, and a launch for dW
+        const double sums = s > 1 || sums_anyway ? 8.0 * s * tiles * c.tile.tp * c.tile.tq / 4e6 + (sums_anyway ? 0 : 8) : 0;
         const double cost = rounds_cost(c, tiles * s, std::ceil(slabs / s)) + sums;
         if (cost < least) {
             least = cost;
@@ -109,7 +111,7 @@ HeadLayout layout_of(dmuon_head_desc d, bool backward) {
     // forward 314 / 443, 512 tokens 573 / 534; backward without dW 128 tokens 360 / 502,
     // 256 tokens 668 / 567; fp32 forward 256 tokens 883 / 1247, 512 x 1000 x 32000 219 /
     // 153; backward without dW 512 x 1000 x 32000 426 / 429, 256 x 4090 x 50000 1531 / 2171.
-    const int64_t few = !backward ? 256 : L.planes > 1 ? 512 : 128;
+    const int64_t few = !backward ? 256 : L.planes > 1 ? 384 : 128;
     L.stream_weight = L.pack_weight && d.tokens <= few;
     if (L.stream_weight) L.pack_weight = 0;
     const int64_t v_pad = round_up(d.vocab, kHeadTile);
@@ -134,10 +136,13 @@ HeadLayout layout_of(dmuon_head_desc d, bool backward) {
     const double s_slabs = (double)(L.d_pad / kHeadSlab) * (!f32 ? 1 : L.stream_weight ? 6 : 3);
     L.s_tile = pick_tile(std::min(s_rows, d.vocab), d.tokens, s_slabs, max_tq);
     const double parts = f32 ? 6 : 1;
-    L.dw_tile = pick_tile(d.hidden, std::min(L.piece, d.vocab), (double)ceil_div(ds_rows, kHeadSlab) * parts, 256);
+    int64_t dw_splits = 1;
+    L.dw_tile = pick_split_tile(d.hidden, std::min(L.piece, d.vocab), (double)ceil_div(ds_rows, kHeadSlab) * parts, 256,
+                                false, &dw_splits);
+    L.dw_splits = (int32_t)std::min(dw_splits, ceil_div(ds_rows, kHeadSlab));
     const int64_t k = round_up(std::min(L.piece, d.vocab), kHeadSlab);  // of the first, longest piece
     int64_t splits = 1;
-    L.dh_tile = pick_split_tile(d.hidden, ds_rows, (double)(k / kHeadSlab) * parts, max_tq, &splits);
+    L.dh_tile = pick_split_tile(d.hidden, ds_rows, (double)(k / kHeadSlab) * parts, max_tq, true, &splits);
     L.split_k = round_up(ceil_div(k, std::min(splits, k / kHeadSlab)), kHeadSlab);
     L.splits = (int32_t)ceil_div(k, L.split_k);
 
@@ -170,7 +175,14 @@ HeadLayout layout_of(dmuon_head_desc d, bool backward) {
     if (backward) {
         L.off_g = take(2 * L.planes * L.t_pad * L.piece);
         L.off_dh = take(4 * L.splits * L.t_pad * round_up(L.hidden, kHeadTile));
+        if (L.dw_splits > 1) L.off_dw = take(4 * L.dw_splits * L.piece * round_up(L.hidden, kHeadTile));
     } else {
+        // Distillation needs K logits a token.  Dots of H's rows with the gathered rows of W
+        // read K hidden elements of W a token; written out and gathered, the logits cost 4
+        // bytes each and some: the cheaper one, as long as they stay a small buffer.
+        const int64_t kept = 4 * L.t_pad * v_pad;
+        L.keep_logits = L.top_k > 0 && kept <= kPieceBytes && (int64_t)L.top_k * L.hidden * L.esize > 5 * v_pad;
+        if (L.keep_logits) L.off_logits = take(kept);
         L.off_part = take(8 * (v_pad / L.s_tile.tp) * head_wave_rows(L.s_tile.tp, L.s_tile.tq) * L.t_pad);
     }
     L.bytes = at;
@@ -273,9 +285,29 @@ HeadTeacher teacher_of(const Call& c) {
     return HeadTeacher{c.ids, c.teacher, c.desc->top_k, c.desc->vocab, 1.f / c.temp};
 }
 
-// Which rows carry a loss, and their hidden states packed together.
-dmuon_status gather_rows(const Call& c, const Views& v, bool backward, float* losses, float* lse, float* student) {
+// W's rows v0 .. v0 + rows - 1 to be packed (all parts a backward call needs).
+HeadPackArgs pack_weight(const Call& c, const Views& v, bool backward, int64_t v0, int64_t rows) {
     const HeadLayout& L = v.L;
+    HeadPackArgs p{};
+    p.in = static_cast<const char*>(c.weight) + v0 * L.hidden * L.esize;
+    p.cols = L.hidden;
+    p.rows = rows;
+    p.out_rows = round_up(rows, kHeadTile);
+    p.out = L.planes == 1 || backward ? v.at<uint16_t>(L.off_w) : nullptr;
+    p.ld = L.d_pad;
+    p.plane = L.piece * L.d_pad;
+    p.half2 = v.at<uint16_t>(L.off_w2);
+    p.scale = v.at<float>(L.off_ws);
+    return p;
+}
+
+// Which rows carry a loss; then their hidden states packed together, the first
+// piece of W (or its last, partial tile, where it is read in place) and, where
+// given, the coefficients of the gradient.
+dmuon_status gather_rows(const Call& c, const Views& v, float* losses, float* lse, float* student,
+                         const HeadCoefArgs* coef) {
+    const HeadLayout& L = v.L;
+    const bool backward = coef != nullptr;
     if (c.ids != nullptr) HEAD_TRY(launch_head_teacher(teacher_of(c), L.tokens, v.q(), v.flag(), student, c.stream));
     HeadRowsArgs r{};
     r.targets = c.ids != nullptr ? nullptr : c.targets;
@@ -292,67 +324,52 @@ dmuon_status gather_rows(const Call& c, const Views& v, bool backward, float* lo
     r.losses = losses;
     r.lse = lse;
     HEAD_TRY(launch_head_rows(r, c.stream));
-    HeadPackArgs p{};
-    p.in = c.hidden;
-    p.esize = L.esize;
-    p.cols = L.hidden;
-    p.src = v.src();
-    p.count = v.count();
-    p.rows = L.tokens;
-    p.out = L.planes == 1 || backward || L.stream_weight ? v.at<uint16_t>(L.off_h) : nullptr;
-    p.low = L.low;
-    p.out_rows = L.t_pad;
-    p.ld = L.d_pad;
-    p.plane = L.t_pad * L.d_pad;
-    p.half2 = L.pack_weight ? v.at<uint16_t>(L.off_h2) : nullptr;
-    p.scale = v.at<float>(L.off_hs);
-    HEAD_TRY(launch_head_pack(p, c.stream));
+    HeadPrepareArgs a{};
+    a.esize = L.esize;
+    a.h.in = c.hidden;
+    a.h.cols = L.hidden;
+    a.h.src = v.src();
+    a.h.count = v.count();
+    a.h.rows = L.tokens;
+    a.h.out = L.planes == 1 || backward || L.stream_weight ? v.at<uint16_t>(L.off_h) : nullptr;
+    a.h.low = L.low;
+    a.h.out_rows = L.t_pad;
+    a.h.ld = L.d_pad;
+    a.h.plane = L.t_pad * L.d_pad;
+    a.h.half2 = L.pack_weight ? v.at<uint16_t>(L.off_h2) : nullptr;
+    a.h.scale = v.at<float>(L.off_hs);
+    const int64_t tail = L.vocab % kHeadTile;
+    if (L.pack_weight) a.w = pack_weight(c, v, backward, 0, std::min(L.piece, L.vocab));
+    else if (!L.stream_weight && tail != 0) a.w = pack_weight(c, v, backward, L.vocab - tail, tail);
+    if (coef != nullptr) a.coef = *coef;
+    HEAD_TRY(launch_head_prepare(a, c.stream));
     return DMUON_OK;
 }
 
 // vocab rows [v0, v0 + rows) of W as the products' P operand: in place, with
-// the last partial tile copied, or packed.
+// the last partial tile copied, or packed (the first piece by gather_rows).
 dmuon_status weight_piece(const Call& c, const Views& v, bool backward, int64_t v0, int64_t rows, HeadGemmArgs& a) {
     const HeadLayout& L = v.L;
     const int64_t left = std::min(rows, L.vocab - v0);  // real rows
-    const char* w = static_cast<const char*>(c.weight) + v0 * L.hidden * L.esize;
-    HeadPackArgs p{};
-    p.esize = L.esize;
-    p.cols = L.hidden;
-    p.out = L.planes == 1 || backward ? v.at<uint16_t>(L.off_w) : nullptr;
-    p.ld = L.d_pad;
-    p.half2 = v.at<uint16_t>(L.off_w2);
-    p.scale = v.at<float>(L.off_ws);
     a.tail_row = INT_MAX;
-    a.p_tail = nullptr;
-    a.p_ld = (int32_t)L.d_pad;
-    if (L.stream_weight) {
-        a.p = w;
-        a.p_ld = (int32_t)L.hidden;
-        a.p_rows = left;
-        return DMUON_OK;
-    }
+    a.p_rows = left;
     if (L.pack_weight) {
-        p.in = w;
-        p.rows = left;
-        p.out_rows = round_up(left, kHeadTile);
-        p.plane = L.piece * L.d_pad;
+        if (v0 > 0) {
+            HeadPrepareArgs p{};
+            p.esize = L.esize;
+            p.w = pack_weight(c, v, backward, v0, left);
+            HEAD_TRY(launch_head_prepare(p, c.stream));
+        }
         a.p = v.ws + L.off_w;
-        a.p_plane = 2 * p.plane;
-        HEAD_TRY(launch_head_pack(p, c.stream));
+        a.p_plane = 2 * L.piece * L.d_pad;
+        a.p_ld = (int32_t)L.d_pad;
         return DMUON_OK;
     }
-    a.p = w;
-    a.p_plane = 0;
-    if (left % kHeadTile != 0) {
-        const int64_t whole = left / kHeadTile * kHeadTile;
-        p.in = w + whole * L.hidden * L.esize;
-        p.rows = left - whole;
-        p.out_rows = kHeadTile;
-        p.plane = 0;
-        a.tail_row = (int32_t)whole;
+    a.p = static_cast<const char*>(c.weight) + v0 * L.hidden * L.esize;
+    a.p_ld = (int32_t)L.hidden;
+    if (!L.stream_weight && left % kHeadTile != 0) {
+        a.tail_row = (int32_t)(left / kHeadTile * kHeadTile);
         a.p_tail = v.ws + L.off_w;
-        HEAD_TRY(launch_head_pack(p, c.stream));
     }
     return DMUON_OK;
 }
@@ -402,8 +419,21 @@ dmuon_status forward(const Call& c, bool distill, float* losses, float* lse, flo
     if (st != DMUON_OK) return st;
 
     const Views v{static_cast<char*>(c.workspace), L};
-    st = gather_rows(c, v, false, losses, lse, student);
+    st = gather_rows(c, v, losses, lse, student, nullptr);
     if (st != DMUON_OK) return st;
+    if (distill && !L.keep_logits) {
+        HeadStudentArgs t{};
+        t.count = v.count();
+        t.src = v.src();
+        t.t = teacher_of(c);
+        t.hidden = c.hidden;
+        t.weight = c.weight;
+        t.esize = L.esize;
+        t.cols = L.hidden;
+        t.student = student;
+        t.tokens = L.tokens;
+        HEAD_TRY(launch_head_student(t, c.stream));
+    }
     // read in place, the whole vocabulary is one launch
     const int64_t step = L.pack_weight ? L.piece : round_up(L.vocab, kHeadTile);
     for (int64_t v0 = 0; v0 < L.vocab; v0 += step) {
@@ -413,6 +443,8 @@ dmuon_status forward(const Call& c, bool distill, float* losses, float* lse, flo
         logits_args(c, v, v0, step, a);
         a.part = v.at<float2>(L.off_part);
         a.target_logit = v.target_logit();
+        if (L.keep_logits) a.logits = v.at<float>(L.off_logits);
+        a.logits_ld = (int32_t)round_up(L.vocab, kHeadTile);
         HEAD_TRY(launch_w(kHeadLse, L, L.s_tile, a, (int64_t)a.tiles_i * ceil_div(L.tokens, L.s_tile.tq), c.stream));
     }
     HeadMergeArgs m{};
@@ -423,29 +455,17 @@ dmuon_status forward(const Call& c, bool distill, float* losses, float* lse, flo
     m.parts = (int32_t)ceil_div(L.vocab, L.s_tile.tp) * head_wave_rows(L.s_tile.tp, L.s_tile.tq);
     m.tokens = L.tokens;
     m.inv_temp = 1.f / c.temp;
+    m.temp = c.temp;
     m.target = distill ? nullptr : v.target();
     m.target_logit = v.target_logit();
-    m.lse_c = v.lse();
+    m.t = teacher_of(c);
+    m.q = v.q();
+    m.student = student;
+    if (L.keep_logits) m.logits = v.at<float>(L.off_logits);
+    m.logits_ld = round_up(L.vocab, kHeadTile);
     m.losses = losses;
     m.lse = lse;
     HEAD_TRY(launch_head_merge(m, c.stream));
-    if (distill) {
-        HeadStudentArgs s{};
-        s.count = v.count();
-        s.src = v.src();
-        s.t = teacher_of(c);
-        s.q = v.q();
-        s.hidden = c.hidden;
-        s.weight = c.weight;
-        s.esize = L.esize;
-        s.cols = L.hidden;
-        s.lse_c = v.lse();
-        s.temp = c.temp;
-        s.student = student;
-        s.losses = losses;
-        s.tokens = L.tokens;
-        HEAD_TRY(launch_head_student(s, c.stream));
-    }
     return DMUON_OK;
 }
 
@@ -473,8 +493,6 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
     if (st != DMUON_OK) return st;
 
     const Views v{static_cast<char*>(c.workspace), L};
-    st = gather_rows(c, v, true, nullptr, nullptr, nullptr);
-    if (st != DMUON_OK) return st;
     HeadCoefArgs k{};
     k.count = v.count();
     k.src = v.src();
@@ -489,7 +507,8 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
     k.ct = v.ct();
     k.norm = v.norm();
     k.t_pad = L.t_pad;
-    HEAD_TRY(launch_head_coef(k, c.stream));
+    st = gather_rows(c, v, nullptr, nullptr, nullptr, &k);
+    if (st != DMUON_OK) return st;
     const int64_t dh_tiles_j = ceil_div(L.low ? 2 * head_low_row((int)L.tokens) : L.tokens, L.dh_tile.tq);
     const int32_t dh_tiles_i = (int32_t)ceil_div(L.hidden, L.dh_tile.tp);
     for (int64_t v0 = 0; v0 < L.vocab; v0 += L.piece) {
@@ -540,7 +559,7 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
             h.split_k = (int32_t)L.split_k;
             h.splits = (int32_t)ceil_div(h.k, L.split_k);
             h.tiles_i = dh_tiles_i;
-            h.dh = v.at<float>(L.off_dh);
+            h.sums = v.at<float>(L.off_dh);
             h.accumulate = v0 != 0;
             HEAD_TRY(launch_w(kHeadDh, L, L.dh_tile, h, h.splits * dh_tiles_i * dh_tiles_j, c.stream));
         }
@@ -561,24 +580,39 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
             g.dw = static_cast<char*>(grad_weight) + v0 * L.hidden * L.esize;
             g.dw_rows = left;
             g.dw_ld = (int32_t)L.hidden;
-            HEAD_TRY(launch_head_gemm(kHeadDw, L.dw_tile, g, (int64_t)g.tiles_i * g.tiles_j, c.stream));
+            g.splits = L.dw_splits;
+            g.sums = v.at<float>(L.off_dw);
+            HEAD_TRY(launch_head_gemm(g.splits > 1 ? kHeadDwSum : kHeadDw, L.dw_tile, g, (int64_t)g.tiles_i * g.tiles_j * g.splits, c.stream));
+            if (g.splits > 1) {
+                HeadSumArgs d{};
+                d.rows = left;
+                d.norm = v.norm();
+                d.sums = g.sums;
+                d.splits = g.splits;
+                d.tiles_i = g.tiles_i;
+                d.tile = L.dw_tile;
+                d.out = g.dw;
+                d.esize = L.esize;
+                d.cols = L.hidden;
+                HEAD_TRY(launch_head_sum(d, c.stream));
+            }
         }
     }
     if (grad_hidden != nullptr) {
-        HeadDhArgs h{};
+        HeadSumArgs h{};
         h.count = v.count();
+        h.rows = L.tokens;
         h.src = v.src();
         h.norm = v.norm();
         h.low = L.low;
-        h.dh = v.at<float>(L.off_dh);
+        h.sums = v.at<float>(L.off_dh);
         h.splits = L.splits;
         h.tiles_i = dh_tiles_i;
         h.tile = L.dh_tile;
         h.out = grad_hidden;
         h.esize = L.esize;
-        h.tokens = L.tokens;
         h.cols = L.hidden;
-        HEAD_TRY(launch_head_dh(h, c.stream));
+        HEAD_TRY(launch_head_sum(h, c.stream));
     }
     return DMUON_OK;
 }

@@ -61,9 +61,11 @@ struct HeadLayout {
     int32_t pieces;
     int64_t split_k;        // dH: vocab rows of a split (multiple of 64)
     int32_t splits;         // ... splits of a full piece
+    int32_t dw_splits;      // dW: splits of the tokens
+    int32_t keep_logits;    // distillation, small vocabularies: see layout_of
     // byte offsets
     size_t off_count, off_norm, off_src, off_tgt, off_lse, off_cp, off_ct, off_tl, off_q, off_flag;
-    size_t off_h, off_w, off_part, off_g, off_dh;
+    size_t off_h, off_w, off_part, off_g, off_dh, off_dw, off_logits;
     size_t off_h2, off_w2, off_hs, off_ws;  // fp32: the logits' operands and their row scales
     size_t bytes;
 };
@@ -73,7 +75,8 @@ enum HeadMode : int32_t {
     kHeadLse = 0,   // P = W rows, Q = H rows: softmax statistics of each tile (and the targets' logits)
     kHeadGrad = 1,  // P = W rows, Q = H rows: ds as bf16 parts
     kHeadDh = 2,    // P = W (k = vocab rows, columns of hidden), Q = ds rows: fp32 sums, added per piece
-    kHeadDw = 3     // P = H (k = tokens, columns of hidden), Q = ds (k = tokens, columns of vocab): dW rows
+    kHeadDw = 3,    // P = H (k = tokens, columns of hidden), Q = ds (k = tokens, columns of vocab): dW rows
+    kHeadDwSum = 4  // the same in splits of the tokens: fp32 sums
 };
 
 struct HeadGemmArgs {
@@ -88,7 +91,7 @@ struct HeadGemmArgs {
     int64_t p_rows;              // rows of W left from the piece's first (stream kernels)
     int32_t parts;               // 1: bf16; 3: fp32
     int32_t k;                   // K extent (dH: of the piece; dW: taken from count)
-    int32_t split_k, splits;     // dH
+    int32_t split_k, splits;     // dH: K of a split; DwSum: splits of the tokens
     int32_t tiles_i;             // tiles along P's rows (or columns)
     int32_t tiles_j;             // tiles along Q's (dW: vocab); else from count
     // softmax
@@ -100,6 +103,8 @@ struct HeadGemmArgs {
     int64_t t_pad;
     int32_t first_tile;          // vocab tile index of the piece's first tile
     float* target_logit;
+    float* logits;               // Lse: the logits too (row stride logits_ld), or null
+    int32_t logits_ld;
     const float* lse;            // per compact row
     const float* cp;             // coefficient of p
     const float* ct;             // coefficient at the target
@@ -108,7 +113,7 @@ struct HeadGemmArgs {
     char* g;                     // ds out
     int64_t g_plane;             // bytes
     int32_t g_ld;
-    float* dh;                   // fp32 sums, tile by tile in the accumulators' own order
+    float* sums;                 // fp32 sums (dH; dW in splits), tile by tile in the accumulators' own order
     int32_t accumulate;          // dH: add to what earlier pieces left
     void* dw;                    // dW out (row v0 of it is at dw)
     int64_t dw_rows;             // rows of dW left from v0
@@ -155,7 +160,6 @@ hipError_t launch_head_rows(const HeadRowsArgs& a, hipStream_t stream);
 // when given), zero above up to out_rows.
 struct HeadPackArgs {
     const void* in;
-    int32_t esize;
     int64_t cols;
     const int32_t* src;
     const int32_t* count;  // device row count, or null:
@@ -166,9 +170,20 @@ struct HeadPackArgs {
     uint16_t* half2;       // fp32: 32 hi, 32 lo fp16 values of every 32 columns, rows of 2 ld
     float* scale;          // ... and the factor that restores a row's scale
 };
-hipError_t launch_head_pack(const HeadPackArgs& a, hipStream_t stream);
-// Joins the tiles' softmax statistics: lse (compact, natural units) and, for
-// cross entropy, losses and lse of the caller.
+// Distillation: the student's logits at the teacher's ids.
+struct HeadStudentArgs {
+    const int32_t* count;
+    const int32_t* src;
+    HeadTeacher t;
+    const void* hidden;
+    const void* weight;
+    int32_t esize;
+    int64_t cols;
+    float* student;
+    int64_t tokens;
+};
+hipError_t launch_head_student(const HeadStudentArgs& a, hipStream_t stream);
+// Joins the tiles' softmax statistics: the caller's lse and losses.
 struct HeadMergeArgs {
     const int32_t* count;
     const int32_t* src;
@@ -176,31 +191,18 @@ struct HeadMergeArgs {
     int64_t t_pad;
     int32_t parts;
     int64_t tokens;
-    float inv_temp;
+    float inv_temp, temp;
     const int32_t* target;      // cross entropy, else null
     const float* target_logit;
-    float* lse_c;
-    float* losses;              // cross entropy
+    HeadTeacher t;              // distillation
+    const float2* q;
+    float* student;
+    const float* logits;        // distillation: the logits themselves (written to student), or null
+    int64_t logits_ld;
+    float* losses;
     float* lse;
 };
 hipError_t launch_head_merge(const HeadMergeArgs& a, hipStream_t stream);
-// Distillation: the student's logits at the teacher's ids and the losses.
-struct HeadStudentArgs {
-    const int32_t* count;
-    const int32_t* src;
-    HeadTeacher t;
-    const float2* q;
-    const void* hidden;
-    const void* weight;
-    int32_t esize;
-    int64_t cols;
-    const float* lse_c;
-    float temp;
-    float* student;
-    float* losses;
-    int64_t tokens;
-};
-hipError_t launch_head_student(const HeadStudentArgs& a, hipStream_t stream);
 // Backward coefficients per compact row (zero in the padding).
 struct HeadCoefArgs {
     const int32_t* count;
@@ -215,7 +217,15 @@ struct HeadCoefArgs {
     float* norm;            // the largest |cp|, |ct|
     int64_t t_pad;
 };
-hipError_t launch_head_coef(const HeadCoefArgs& a, hipStream_t stream);
+// One launch of up to three independent jobs, all after launch_head_rows: rows
+// packed, W packed (out_rows 0: not) and the coefficients (t_pad 0: not).
+struct HeadPrepareArgs {
+    HeadPackArgs h, w;
+    HeadCoefArgs coef;
+    int32_t esize;
+    int32_t h_blocks, w_blocks, coef_blocks;  // set by the launcher
+};
+hipError_t launch_head_prepare(const HeadPrepareArgs& a, hipStream_t stream);
 // Distillation: ds at the teacher's ids inside one piece.
 struct HeadFixArgs {
     const int32_t* count;
@@ -235,22 +245,23 @@ struct HeadFixArgs {
     int64_t tokens;
 };
 hipError_t launch_head_fix(const HeadFixArgs& a, hipStream_t stream);
-// dH from the fp32 tile sums: splits added in order, rows scattered to their
-// tokens, zeros for rows without a loss.
-struct HeadDhArgs {
-    const int32_t* count;
-    const int32_t* src;
+// dH (or dW) from the fp32 tile sums: splits added in order, rows scattered to
+// their tokens, zeros for rows without a loss.
+struct HeadSumArgs {
+    const int32_t* count;  // null: rows
+    int64_t rows;          // rows of the output
+    const int32_t* src;    // null: in place
     const float* norm;
     int32_t low;
-    const float* dh;
+    const float* sums;
     int32_t splits;
     int32_t tiles_i;
     HeadTile tile;
     void* out;
     int32_t esize;
-    int64_t tokens, cols;
+    int64_t cols;
 };
-hipError_t launch_head_dh(const HeadDhArgs& a, hipStream_t stream);
+hipError_t launch_head_sum(const HeadSumArgs& a, hipStream_t stream);
 hipError_t launch_head_zero(void* p, int64_t bytes, hipStream_t stream);
 
 }  // namespace dmuon

@@ -85,6 +85,8 @@ struct Loads {
     int tail_k;  // dH: first k (from the tile's first) that lies in the tail copy
 };
 
+constexpr bool is_dw(int mode) { return mode == kHeadDw || mode == kHeadDwSum; }
+
 // The tiles of a launch and this workgroup's share of them: XCD x takes one
 // contiguous run of the tiles (neighbours share operand rows in its L2), its
 // workgroups in turn.
@@ -94,9 +96,9 @@ struct Share {
 template <int TQ, int MODE>
 __device__ __forceinline__ Share share_of(const HeadGemmArgs& args, int n, int n_k) {
     Share s;
-    s.tiles_j = MODE == kHeadDw ? args.tiles_j : ((MODE == kHeadGrad ? n_k : n) + TQ - 1) / TQ;
+    s.tiles_j = is_dw(MODE) ? args.tiles_j : ((MODE == kHeadGrad ? n_k : n) + TQ - 1) / TQ;
     s.per_split = args.tiles_i * s.tiles_j;
-    const int total = s.per_split * (MODE == kHeadDh ? args.splits : 1);
+    const int total = s.per_split * (MODE == kHeadDh || MODE == kHeadDwSum ? args.splits : 1);
     const int x = (int)(blockIdx.x % kXcds);
     s.step = ((int)gridDim.x - x + kXcds - 1) / kXcds;
     const int each = total / kXcds, rem = total % kXcds;
@@ -163,6 +165,15 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
         #pragma unroll
         for (int j = 0; j < C::FJ; ++j) {
             const int row = t.J * TQ + wc * C::CW + 32 * j + lrow;
+            if (args.logits != nullptr) {
+                float* out = args.logits + (int64_t)row * args.logits_ld + v_base + 4 * khalf;
+                #pragma unroll
+                for (int i = 0; i < C::FI; ++i)
+                    #pragma unroll
+                    for (int v4 = 0; v4 < 4; ++v4)
+                        *reinterpret_cast<float4*>(out + 32 * i + 8 * v4) =
+                            make_float4(acc[i][j][4 * v4], acc[i][j][4 * v4 + 1], acc[i][j][4 * v4 + 2], acc[i][j][4 * v4 + 3]);
+            }
             if (limit < C::RW) {
                 #pragma unroll
                 for (int i = 0; i < C::FI; ++i)
@@ -200,9 +211,9 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
             if (khalf == 0)
                 args.part[((int64_t)(args.first_tile + t.I) * C::WR + wr) * args.t_pad + row] = make_float2(m, l);
         }
-    } else if constexpr (MODE == kHeadDh) {
+    } else if constexpr (MODE == kHeadDh || MODE == kHeadDwSum) {
         float4* d = reinterpret_cast<float4*>(
-            args.dh + ((int64_t)(t.split * tiles_j + t.J) * args.tiles_i + t.I) * (TP * TQ));
+            args.sums + ((int64_t)(t.split * tiles_j + t.J) * args.tiles_i + t.I) * (TP * TQ));
         #pragma unroll
         for (int i = 0; i < C::FI; ++i)
             #pragma unroll
@@ -212,7 +223,7 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
                     float4* p = d + (((wave * C::FI + i) * C::FJ + j) * 4 + v4) * 64 + lane;
                     float4 o = make_float4(acc[i][j][4 * v4], acc[i][j][4 * v4 + 1], acc[i][j][4 * v4 + 2],
                                            acc[i][j][4 * v4 + 3]);
-                    if (args.accumulate) {
+                    if (MODE == kHeadDh && args.accumulate) {
                         const float4 b = *p;
                         o = make_float4(o.x + b.x, o.y + b.y, o.z + b.z, o.w + b.w);
                     }

@@ -37,8 +37,8 @@ using namespace head;
 // gradients).
 template <typename C, int MODE, int KIND>
 __global__ __launch_bounds__(C::NT, C::NT == 512 ? 1 : 2) void head_gemm_kernel(HeadGemmArgs args) {
-    constexpr bool PW = MODE == kHeadDh || MODE == kHeadDw;  // P is K-major
-    constexpr bool QW = MODE == kHeadDw;                     // Q is K-major
+    constexpr bool PW = MODE == kHeadDh || is_dw(MODE);  // P is K-major
+    constexpr bool QW = is_dw(MODE);                     // Q is K-major
     constexpr int TP = C::TP, TQ = C::TQ;
     using WP = Wide<TP>;
     using WQ = Wide<TQ>;
@@ -61,8 +61,14 @@ __global__ __launch_bounds__(C::NT, C::NT == 512 ? 1 : 2) void head_gemm_kernel(
         if (MODE == kHeadDh) {
             k_first = t.split * args.split_k;
             K = imin(args.split_k, args.k - k_first);
+        } else if (MODE == kHeadDw) {
+            K = n_k;
+        } else if (MODE == kHeadDwSum) {
+            const int each = (n_k / kBK + args.splits - 1) / args.splits * kBK;
+            k_first = imin(t.split * each, n_k);
+            K = imin(each, n_k - k_first);
         } else {
-            K = MODE == kHeadDw ? n_k : args.k;
+            K = args.k;
         }
         Loads L;
         L.tail_k = INT_MAX;
@@ -89,7 +95,7 @@ __global__ __launch_bounds__(C::NT, C::NT == 512 ? 1 : 2) void head_gemm_kernel(
             }
         }
         if (QW) {
-            L.q = args.q;
+            L.q = args.q + 2 * (int64_t)k_first * args.q_ld;
             #pragma unroll
             for (int par = 0; par < 2; ++par) {
                 const int row = lane / WQ::kChunksRow;
@@ -264,6 +270,9 @@ hipError_t launch_config(int mode, const HeadGemmArgs& a, int64_t max_tiles, hip
         case kHeadDw:
             return f32 ? launch<C, kHeadDw, kHeadBf16x3>(a, max_tiles, stream)
                        : launch<C, kHeadDw, kHeadBf16>(a, max_tiles, stream);
+        case kHeadDwSum:
+            return f32 ? launch<C, kHeadDwSum, kHeadBf16x3>(a, max_tiles, stream)
+                       : launch<C, kHeadDwSum, kHeadBf16>(a, max_tiles, stream);
         default: return hipErrorInvalidValue;
     }
 }

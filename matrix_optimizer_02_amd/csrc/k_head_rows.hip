@@ -141,7 +141,7 @@ __device__ __forceinline__ uint4 pack_bf16(const float (&x)[8]) {
 
 // One wave per output row, 8 columns a lane and step.
 template <int ESIZE>
-__global__ __launch_bounds__(kRowThreads) void head_pack_kernel(HeadPackArgs a) {
+__device__ __forceinline__ void pack_rows(const HeadPackArgs& a, int block, int blocks) {
     const int64_t limit = a.count != nullptr ? *a.count : a.rows;
     // rows past the last one: zeros up to a whole tile
     int64_t end = (limit + kHeadTile - 1) / kHeadTile * kHeadTile;
@@ -151,7 +151,7 @@ __global__ __launch_bounds__(kRowThreads) void head_pack_kernel(HeadPackArgs a) 
     const int64_t low_row = a.low ? head_low_row((int)limit) : end;
     const int lane = threadIdx.x & 63;
     constexpr int kWavesBlock = kRowThreads / 64;
-    for (int64_t r = (int64_t)blockIdx.x * kWavesBlock + (threadIdx.x >> 6); r < end; r += (int64_t)gridDim.x * kWavesBlock) {
+    for (int64_t r = (int64_t)block * kWavesBlock + (threadIdx.x >> 6); r < end; r += (int64_t)blocks * kWavesBlock) {
         const int64_t of = r < low_row ? r : r - low_row;
         const int64_t from = of < limit ? (a.src != nullptr ? (int64_t)a.src[of] : of) : -1;
         float scale = 1.f;
@@ -214,109 +214,134 @@ __global__ __launch_bounds__(kRowThreads) void head_pack_kernel(HeadPackArgs a) 
     }
 }
 
-// 16 rows by 16 groups of tiles a block: each group joins its tiles' (max, sum)
-// pairs in order, then the groups join in order.
-constexpr int kMergeRows = 16, kMergeGroups = 16;
-__global__ __launch_bounds__(kMergeRows* kMergeGroups) void head_merge_kernel(HeadMergeArgs a) {
-    __shared__ float2 part[kMergeGroups][kMergeRows];
+// R rows by 256 / R groups of tiles a block: each thread joins its group's (max,
+// sum) pairs of its row, then the groups are joined, all in a fixed order; the
+// groups then share the row's teacher entries.  R = 16 reads whole 128-byte lines
+// of the statistics; few tokens take fewer rows a block, so that more threads
+// share a row.
+template <int R>
+__global__ __launch_bounds__(256) void head_merge_kernel(HeadMergeArgs a) {
+    constexpr int kGroups = 256 / R;
+    __shared__ float red[4][R];
     const int n = *a.count;
-    const int r = threadIdx.x % kMergeRows, g = threadIdx.x / kMergeRows;
-    const int64_t c = (int64_t)blockIdx.x * kMergeRows + r;
+    const int r = threadIdx.x % R, g = threadIdx.x / R, wave = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * R + r;
     const float scale = a.inv_temp;
-    auto join = [&](float2 x, float2 y) {
-        // a NaN maximum does not survive fmaxf: it is in the sum too, and stays
-        const float m = fmaxf(x.x, y.x);
-        const float m0 = m == -INFINITY ? 0.f : m;
-        return make_float2(m, x.y * expf((x.x - m0) * scale) + y.y * expf((y.x - m0) * scale));
+    if ((int64_t)blockIdx.x * R >= n) return;
+    const bool in = c < n;
+    // over the row's groups: inside a wave, then the four waves in order
+    auto over_groups = [&](float v, bool max) {
+        #pragma unroll
+        for (int off = 32; off >= R; off >>= 1) {
+            const float o = __shfl_xor(v, off, 64);
+            v = max ? fmaxf(v, o) : v + o;
+        }
+        __syncthreads();
+        if ((threadIdx.x & 63) < R) red[wave][r] = v;
+        __syncthreads();
+        v = red[0][r];
+        #pragma unroll
+        for (int w = 1; w < 4; ++w) v = max ? fmaxf(v, red[w][r]) : v + red[w][r];
+        return v;
     };
-    float2 s = make_float2(-INFINITY, 0.f);
-    if (c < n) {
-        const int per = (a.parts + kMergeGroups - 1) / kMergeGroups;
-        const int p1 = min(a.parts, (g + 1) * per);
-        #pragma unroll 8
-        for (int p = g * per; p < p1; ++p) s = join(s, a.part[(int64_t)p * a.t_pad + c]);
+    const int per = (a.parts + kGroups - 1) / kGroups;
+    const int p0 = g * per, mine = in ? min(a.parts, p0 + per) - p0 : 0;
+    const float2* p = a.part + (int64_t)p0 * a.t_pad + c;
+    // (a NaN does not survive fmaxf, but is in the sum too, and stays)
+    float m = -INFINITY, l = 0.f;
+    #pragma unroll 4
+    for (int k = 0; k < mine; ++k) m = fmaxf(m, p[k * a.t_pad].x);
+    m = over_groups(m, true);
+    const float m0 = m == -INFINITY ? 0.f : m;
+    #pragma unroll 4
+    for (int k = 0; k < mine; ++k) {
+        const float2 x = p[k * a.t_pad];
+        l = fmaf(x.y, expf((x.x - m0) * scale), l);
     }
-    part[g][r] = s;
-    __syncthreads();
-    if (g != 0 || c >= n) return;
-    for (int k = 1; k < kMergeGroups; ++k) s = join(s, part[k][r]);
-    const float lse = fmaf(s.x, scale, logf(s.y));
-    a.lse_c[c] = lse;
-    const int t = a.src[c];
-    a.lse[t] = lse;
-    if (a.target != nullptr) a.losses[t] = a.target[c] < 0 ? nan_f() : lse - a.target_logit[c];
+    l = over_groups(l, false);
+    const float lse = fmaf(m, scale, logf(l));
+    const int t = in ? a.src[c] : 0;
+    const bool writer = in && g == 0;
+    if (writer) a.lse[t] = lse;
+    if (a.target != nullptr) {
+        if (writer) a.losses[t] = a.target[c] < 0 ? nan_f() : lse - a.target_logit[c];
+        return;
+    }
+    // distillation: sum of q (log q - s / T + lse) over the row's entries
+    float loss = 0.f;
+    if (in) {
+        const float2 q = a.q[t];
+        for (int k = g; k < a.t.k; k += kGroups) {
+            const int64_t at = (int64_t)t * a.t.k + k, id = a.t.ids[at];
+            if (id < 0) continue;
+            float s = 0.f;
+            if (a.logits != nullptr) {
+                if (id < a.t.vocab) s = a.logits[c * a.logits_ld + id];
+                a.student[at] = s;
+            } else {
+                s = a.student[at];
+            }
+            const float z = a.t.logits[at] * scale;
+            if (z == -INFINITY) continue;
+            const float logq = z - q.x - q.y;
+            loss = fmaf(expf(logq), (logq + lse) - s * scale, loss);
+        }
+    }
+    loss = over_groups(loss, false);
+    if (writer) a.losses[t] = a.temp * a.temp * loss;  // (q is NaN where an id is past the vocabulary)
 }
 
-// One block per row with a loss: the student's logits at the teacher's ids, a
-// wave per id, and the loss.
+// A wave per teacher entry of the rows with a loss: the student's logit.
 template <int ESIZE>
 __global__ __launch_bounds__(kRowThreads) void head_student_kernel(HeadStudentArgs a) {
-    __shared__ float sums[kRowThreads / 64];
-    const int n = *a.count;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int64_t entries = (int64_t)*a.count * a.t.k, step = (int64_t)gridDim.x * (kRowThreads / 64);
     const bool vec = a.cols % (16 / ESIZE) == 0;
-    for (int64_t c = blockIdx.x; c < n; c += gridDim.x) {
-        const int64_t row = a.src[c];
-        const float2 q = a.q[row];
-        const float lse = a.lse_c[c];
-        float loss = 0.f;
-        for (int k = wave; k < a.t.k; k += kRowThreads / 64) {
-            const int64_t id = a.t.ids[row * a.t.k + k];
-            if (id < 0 || id >= a.t.vocab) continue;
-            float s = 0.f;
-            if (ESIZE == 2) {
-                const uint16_t* h = static_cast<const uint16_t*>(a.hidden) + row * a.cols;
-                const uint16_t* w = static_cast<const uint16_t*>(a.weight) + id * a.cols;
-                if (vec) {
-                    #pragma unroll 4
-                    for (int64_t d = lane * 8; d < a.cols; d += 512) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(h + d), y = *reinterpret_cast<const uint4*>(w + d);
-                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-                        #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
-                            s = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), s);
-                        }
+    for (int64_t w = (int64_t)blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6); w < entries; w += step) {
+        const int64_t c = w / a.t.k;
+        const int64_t row = a.src[c], at = row * a.t.k + (w - c * a.t.k);
+        const int64_t id = a.t.ids[at];
+        if (id < 0 || id >= a.t.vocab) continue;
+        float s = 0.f;
+        if (ESIZE == 2) {
+            const uint16_t* h = static_cast<const uint16_t*>(a.hidden) + row * a.cols;
+            const uint16_t* x = static_cast<const uint16_t*>(a.weight) + id * a.cols;
+            if (vec) {
+                #pragma unroll 4
+                for (int64_t d = lane * 8; d < a.cols; d += 512) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(h + d), v = *reinterpret_cast<const uint4*>(x + d);
+                    const uint32_t us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
+                    #pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s = fmaf(__uint_as_float(us[e] << 16), __uint_as_float(vs[e] << 16), s);
+                        s = fmaf(__uint_as_float(us[e] & 0xffff0000u), __uint_as_float(vs[e] & 0xffff0000u), s);
                     }
-                } else {
-                    for (int64_t d = lane; d < a.cols; d += 64) s = fmaf(bf16_to_f32(h[d]), bf16_to_f32(w[d]), s);
                 }
             } else {
-                const float* h = static_cast<const float*>(a.hidden) + row * a.cols;
-                const float* w = static_cast<const float*>(a.weight) + id * a.cols;
-                if (vec) {
-                    #pragma unroll 4
-                    for (int64_t d = lane * 4; d < a.cols; d += 256) {
-                        const float4 x = *reinterpret_cast<const float4*>(h + d), y = *reinterpret_cast<const float4*>(w + d);
-                        s = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s))));
-                    }
-                } else {
-                    for (int64_t d = lane; d < a.cols; d += 64) s = fmaf(h[d], w[d], s);
+                #pragma unroll 4
+                for (int64_t d = lane; d < a.cols; d += 64) s = fmaf(bf16_to_f32(h[d]), bf16_to_f32(x[d]), s);
+            }
+        } else {
+            const float* h = static_cast<const float*>(a.hidden) + row * a.cols;
+            const float* x = static_cast<const float*>(a.weight) + id * a.cols;
+            if (vec) {
+                #pragma unroll 4
+                for (int64_t d = lane * 4; d < a.cols; d += 256) {
+                    const float4 u = *reinterpret_cast<const float4*>(h + d), v = *reinterpret_cast<const float4*>(x + d);
+                    s = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, s))));
                 }
-            }
-            s = wave_sum(s);
-            if (lane == 0) a.student[row * a.t.k + k] = s;
-            const float z = a.t.logits[row * a.t.k + k] * a.t.inv_temp;
-            if (z != -INFINITY) {
-                const float logq = z - q.x - q.y;
-                loss = fmaf(expf(logq), (logq + lse) - s * a.t.inv_temp, loss);
+            } else {
+                #pragma unroll 4
+                for (int64_t d = lane; d < a.cols; d += 64) s = fmaf(h[d], x[d], s);
             }
         }
-        if (lane == 0) sums[wave] = loss;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            float total = 0.f;
-            for (int w = 0; w < kRowThreads / 64; ++w) total += sums[w];
-            // a row with an id past the vocabulary has q NaN; every other term may be absent
-            if (q.x != q.x) total = nan_f();
-            a.losses[row] = a.temp * a.temp * total;
-        }
-        __syncthreads();
+        s = wave_sum(s);
+        if (lane == 0) a.student[at] = s;
     }
 }
 
-__global__ __launch_bounds__(kRowThreads) void head_coef_kernel(HeadCoefArgs a) {
-    const int64_t c = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+__device__ __forceinline__ void coefficients(const HeadCoefArgs& a, int block) {
+    const int64_t c = (int64_t)block * kRowThreads + threadIdx.x;
     if (c >= a.t_pad) return;
     float lse = 0.f, cp = 0.f, ct = 0.f;
     if (c < *a.count) {
@@ -335,9 +360,21 @@ __global__ __launch_bounds__(kRowThreads) void head_coef_kernel(HeadCoefArgs a) 
     a.ct[c] = ct;
 }
 
+template <int ESIZE>
+__global__ __launch_bounds__(kRowThreads) void head_prepare_kernel(HeadPrepareArgs a) {
+    int block = (int)blockIdx.x;
+    if (block < a.h_blocks) {
+        pack_rows<ESIZE>(a.h, block, a.h_blocks);
+        return;
+    }
+    block -= a.h_blocks;
+    if (block < a.w_blocks) pack_rows<ESIZE>(a.w, block, a.w_blocks);
+    else coefficients(a.coef, block - a.w_blocks);
+}
+
 // One wave per row with a loss: ds at each teacher id of the piece, from the
-// exact student logit; an id held twice takes the sum of its entries' q, which
-// both of them write.
+// student logit of the forward call; an id held twice takes the sum of its
+// entries' q, which both of them write.
 __global__ __launch_bounds__(kRowThreads) void head_fix_kernel(HeadFixArgs a) {
     const int lane = threadIdx.x & 63;
     const int64_t c = (int64_t)blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6);
@@ -349,15 +386,29 @@ __global__ __launch_bounds__(kRowThreads) void head_fix_kernel(HeadFixArgs a) {
     const float norm = *a.norm;
     const float cp = a.cp[c] * (1.f / (norm > 0.f ? norm : 1.f)), lse = a.lse_c[c];
     const int64_t low_step = a.low ? (int64_t)head_low_row(*a.count) * a.g_ld : a.g_plane;
-    for (int k = lane; k < a.t.k; k += 64) {
-        const int64_t id = ids[k];
-        if (id < a.v0 || id >= a.v1) continue;
+    for (int k0 = 0; k0 < a.t.k; k0 += 64) {
+        const int k = k0 + lane;
+        const int64_t id = k < a.t.k ? ids[k] : -1;
+        const bool here = id >= a.v0 && id < a.v1;
+        if (!__builtin_amdgcn_ballot_w64(here)) continue;
+        const int mine = here ? (int)(id - a.v0) : -1;  // (a piece has fewer than 2^31 rows)
         float q = 0.f;
-        for (int j = 0; j < a.t.k; ++j)
-            if (ids[j] == id) q += expf(z[j] * a.t.inv_temp - qs.x - qs.y);
+        for (int j0 = 0; j0 < a.t.k; j0 += 64) {
+            const int j = j0 + lane;
+            const int64_t other = j < a.t.k ? ids[j] : -1;
+            const int off = other >= a.v0 && other < a.v1 ? (int)(other - a.v0) : -2;
+            const float qj = off >= 0 ? expf(z[j] * a.t.inv_temp - qs.x - qs.y) : 0.f;
+            const int last = min(64, a.t.k - j0);
+            for (int i = 0; i < last; ++i) {
+                const int o = __builtin_amdgcn_readlane(off, i);
+                const float x = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(qj), i));
+                q += o == mine ? x : 0.f;
+            }
+        }
+        if (!here) continue;
         const float p = expf(fmaf(a.student[row * a.t.k + k], a.t.inv_temp, -lse));
         float g = cp * (p - q);
-        uint16_t* out = a.g + c * a.g_ld + (id - a.v0);
+        uint16_t* out = a.g + c * a.g_ld + mine;
         for (int part = 0; part < (a.low ? 2 : a.planes); ++part) {
             const uint16_t b = f32_to_bf16(g);
             out[part * low_step] = b;
@@ -368,12 +419,12 @@ __global__ __launch_bounds__(kRowThreads) void head_fix_kernel(HeadFixArgs a) {
 
 // A wave per 64 float4 of a tile's sums, in the product kernel's own order (a
 // lane's four values are 4 consecutive columns of one row).
-__global__ __launch_bounds__(kRowThreads) void head_dh_kernel(HeadDhArgs a) {
+__global__ __launch_bounds__(kRowThreads) void head_sum_kernel(HeadSumArgs a) {
     const int TP = a.tile.tp, TQ = a.tile.tq;
     const int WR = head_wave_rows(TP, TQ), NW = head_waves(TP), RW = TP / WR, CW = TQ / (NW / WR);
     const int FI = RW / 32, FJ = CW / 32;
     const int kGroups = NW * FI * FJ * 4;
-    const int n = *a.count;
+    const int n = a.count != nullptr ? *a.count : (int)a.rows;
     const int low_row = a.low ? head_low_row(n) : 0;
     const int tiles_j = (n + TQ - 1) / TQ;  // of the rows themselves
     const int64_t per_split = (int64_t)((a.low ? 2 * low_row : n) + TQ - 1) / TQ * a.tiles_i * (TP * TQ);
@@ -391,9 +442,11 @@ __global__ __launch_bounds__(kRowThreads) void head_dh_kernel(HeadDhArgs a) {
         const int64_t J = tile / a.tiles_i, I = tile % a.tiles_i;
         const int64_t c0 = J * TQ + wc * CW + 32 * j, c = c0 + (lane & 31);
         const int64_t col = I * TP + wr * RW + 32 * i + 8 * v4 + 4 * (lane >> 5);
+        if (c >= n || col >= a.cols) continue;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         auto add = [&](int64_t group) {
-            const float* p = a.dh + group * 256 + lane * 4;
+            const float* p = a.sums + group * 256 + lane * 4;
+            #pragma unroll 4
             for (int k = 0; k < a.splits; ++k) {
                 const float4 u = *reinterpret_cast<const float4*>(p + k * per_split);
                 s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
@@ -406,8 +459,7 @@ __global__ __launch_bounds__(kRowThreads) void head_dh_kernel(HeadDhArgs a) {
         }
         add(w);
         s.x *= norm, s.y *= norm, s.z *= norm, s.w *= norm;
-        if (c >= n || col >= a.cols) continue;
-        const int64_t at = (int64_t)a.src[c] * a.cols + col;
+        const int64_t at = (a.src != nullptr ? (int64_t)a.src[c] : c) * a.cols + col;
         const float x[4] = {s.x, s.y, s.z, s.w};
         if (a.esize == 2) {
             uint16_t* o = static_cast<uint16_t*>(a.out) + at;
@@ -429,7 +481,7 @@ __global__ __launch_bounds__(kRowThreads) void head_dh_kernel(HeadDhArgs a) {
         }
     }
     // rows without a loss
-    const int64_t idle = a.tokens - n;
+    const int64_t idle = a.rows - n;  // (src is given where there may be any)
     for (int64_t w = (int64_t)blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6); w < idle; w += step) {
         const int64_t at = (int64_t)a.src[n + w] * a.cols;
         for (int64_t d = lane; d < a.cols; d += 64) {
@@ -464,29 +516,34 @@ hipError_t launch_head_rows(const HeadRowsArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_head_pack(const HeadPackArgs& a, hipStream_t stream) {
-    const dim3 grid(blocks_for(a.out_rows, kRowThreads / 64, 8192)), block(kRowThreads);
-    if (a.esize == 2) hipLaunchKernelGGL((head_pack_kernel<2>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((head_pack_kernel<4>), grid, block, 0, stream, a);
+hipError_t launch_head_prepare(const HeadPrepareArgs& args, hipStream_t stream) {
+    HeadPrepareArgs a = args;
+    const int64_t per = kRowThreads / 64;
+    a.h_blocks = a.h.out_rows > 0 ? (int32_t)blocks_for(a.h.out_rows, per, 8192) : 0;
+    a.w_blocks = a.w.out_rows > 0 ? (int32_t)blocks_for(a.w.out_rows, per, 8192) : 0;
+    a.coef_blocks = (int32_t)((a.coef.t_pad + kRowThreads - 1) / kRowThreads);
+    const int32_t blocks = a.h_blocks + a.w_blocks + a.coef_blocks;
+    if (blocks == 0) return hipSuccess;
+    if (a.esize == 2) hipLaunchKernelGGL((head_prepare_kernel<2>), dim3(blocks), dim3(kRowThreads), 0, stream, a);
+    else hipLaunchKernelGGL((head_prepare_kernel<4>), dim3(blocks), dim3(kRowThreads), 0, stream, a);
     return hipGetLastError();
 }
 
 hipError_t launch_head_merge(const HeadMergeArgs& a, hipStream_t stream) {
-    const unsigned grid = blocks_for(a.tokens, kMergeRows, INT32_MAX);
-    hipLaunchKernelGGL(head_merge_kernel, dim3(grid), dim3(kMergeRows * kMergeGroups), 0, stream, a);
+    const dim3 block(256);
+    if (a.tokens > 1024)
+        hipLaunchKernelGGL((head_merge_kernel<16>), dim3(blocks_for(a.tokens, 16, INT32_MAX)), block, 0, stream, a);
+    else if (a.tokens > 128)
+        hipLaunchKernelGGL((head_merge_kernel<4>), dim3(blocks_for(a.tokens, 4, INT32_MAX)), block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((head_merge_kernel<1>), dim3(blocks_for(a.tokens, 1, INT32_MAX)), block, 0, stream, a);
     return hipGetLastError();
 }
 
 hipError_t launch_head_student(const HeadStudentArgs& a, hipStream_t stream) {
-    const dim3 grid(blocks_for(a.tokens, 1, 1 << 20)), block(kRowThreads);
+    const dim3 grid(blocks_for(a.tokens * a.t.k, kRowThreads / 64, 1 << 20)), block(kRowThreads);
     if (a.esize == 2) hipLaunchKernelGGL((head_student_kernel<2>), grid, block, 0, stream, a);
     else hipLaunchKernelGGL((head_student_kernel<4>), grid, block, 0, stream, a);
-    return hipGetLastError();
-}
-
-hipError_t launch_head_coef(const HeadCoefArgs& a, hipStream_t stream) {
-    const unsigned grid = blocks_for(a.t_pad, kRowThreads, INT32_MAX);
-    hipLaunchKernelGGL(head_coef_kernel, dim3(grid), dim3(kRowThreads), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -496,9 +553,10 @@ hipError_t launch_head_fix(const HeadFixArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_head_dh(const HeadDhArgs& a, hipStream_t stream) {
-    const dim3 grid(blocks_for(a.tokens * ((a.cols + 255) / 256) * 64, kRowThreads, 8192)), block(kRowThreads);
-    hipLaunchKernelGGL(head_dh_kernel, grid, block, 0, stream, a);
+hipError_t launch_head_sum(const HeadSumArgs& a, hipStream_t stream) {
+    const int64_t rows = (a.rows + a.tile.tq - 1) / a.tile.tq * a.tile.tq;
+    const dim3 grid(blocks_for(rows * a.tiles_i * (a.tile.tp / 4), kRowThreads, 8192)), block(kRowThreads);
+    hipLaunchKernelGGL(head_sum_kernel, grid, block, 0, stream, a);
     return hipGetLastError();
 }
 

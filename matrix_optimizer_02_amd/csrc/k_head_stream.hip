@@ -5,7 +5,7 @@
 //
 // Batches of few tokens are bound by reading W once, and a padded copy of it
 // would read it, write it and read the copy: here each lane loads 16 bytes of W
-// into registers, two slabs ahead, and writes them to LDS, fp32 values split
+// into registers, some slabs ahead, and writes them to LDS, fp32 values split
 // into three bf16 parts on the way (x = hi + mid + lo, exact to 24 bits).  All
 // parts of a slab lie in LDS together, so the six products of an fp32 tile (hi
 // hi, hi mid, mid hi, mid mid, hi lo, lo hi) read W once.
@@ -44,6 +44,9 @@ struct Stream {
     static constexpr int kPItems = C::TP * 8 / C::NT;  // 16-byte chunks of W a lane loads per slab
     static constexpr int kQChunks = kParts * C::TQ * kRowChunks;
     static constexpr int kQItems = (kQChunks + C::NT - 1) / C::NT;
+    // register sets: slabs on their way.  A 64 x 64 tile's are small, and its slabs
+    // short: it needs more of them to cover a load's latency.
+    static constexpr int kSets = C::TP == 64 ? 4 : C::TQ == 64 ? 3 : 2;
     // rows of 4 chunks: 16 rows at one chunk hit 16 bank groups
     __device__ static __forceinline__ int swz(int r) { return F32 ? (r >> 2) & 3 : swizzle(r); }
 };
@@ -72,25 +75,47 @@ __global__ __launch_bounds__(S::C::NT, S::C::NT == 512 ? 1 : 2) void head_stream
         const int slabs = (K + S::kK - 1) / S::kK;
 
         // ---- W: chunk i of this lane is chunk (i NT + tid) of the slab ------------------
+        // W's rows (dH: columns) of the tile and its slabs' columns (dH: rows) that exist:
+        // a slab inside both is loaded without a look at its lanes.
         constexpr int kPRowChunks = PW ? TP / S::kElems : 8;
+        constexpr int kSize = S::F32 ? 4 : 2;
+        const int64_t left = args.p_rows - (PW ? k_first : (int64_t)t.I * TP);
+        const int rows = left < INT_MAX ? (int)left : INT_MAX;  // from the tile's first row
+        const int cols_left = cols - (PW ? t.I * TP : 0);
+        const bool tile_full = PW ? cols_left >= TP : rows >= TP;
+        const char* const p0 = args.p + ((PW ? (int64_t)k_first : (int64_t)t.I * TP) * cols + (PW ? t.I * TP : 0)) * kSize;
+        const int64_t p_step = (PW ? (int64_t)S::kK * cols : S::kK) * kSize;  // bytes from slab to slab
+        uint32_t p_off[S::kPItems];
+        #pragma unroll
+        for (int i = 0; i < S::kPItems; ++i) {
+            const int item = i * NT + tid;
+            p_off[i] = (uint32_t)(((item / kPRowChunks) * (int64_t)cols + (item % kPRowChunks) * S::kElems) * kSize);
+        }
         auto load_p = [&](int s, u32x4_t (&r)[S::kPItems]) {
-            if (s >= slabs) return;
+            const char* const base = p0 + s * p_step;
+            if (tile_full && (PW ? (s + 1) * S::kK <= rows : (s + 1) * S::kK <= cols_left)) {
+                #pragma unroll
+                for (int i = 0; i < S::kPItems; ++i) {
+                    if (S::F32) r[i] = reinterpret_cast<const Raw4*>(base + p_off[i])->v;
+                    else r[i] = reinterpret_cast<const Raw2*>(base + p_off[i])->v;
+                }
+                return;
+            }
             #pragma unroll
             for (int i = 0; i < S::kPItems; ++i) {
                 const int item = i * NT + tid;
-                const int row = item / kPRowChunks, ch = item % kPRowChunks;
-                const int64_t at = PW ? (int64_t)k_first + s * S::kK + row : (int64_t)t.I * TP + row;  // row of the piece
-                const int col = (PW ? t.I * TP : s * S::kK) + ch * S::kElems;
-                const char* p = args.p + (at * cols + col) * (S::F32 ? 4 : 2);
+                const int row = item / kPRowChunks + (PW ? s * S::kK : 0);
+                const int col = (item % kPRowChunks) * S::kElems + (PW ? 0 : s * S::kK);
+                const char* p = base + p_off[i];
                 r[i] = u32x4_t{0, 0, 0, 0};
-                if (at >= args.p_rows || col >= cols) continue;
-                if (col + S::kElems <= cols) {
+                if (row >= rows || col >= cols_left) continue;
+                if (col + S::kElems <= cols_left) {
                     if (S::F32) r[i] = reinterpret_cast<const Raw4*>(p)->v;
                     else r[i] = reinterpret_cast<const Raw2*>(p)->v;
                 } else {  // the row ends inside the chunk
                     #pragma unroll
                     for (int e = 0; e < S::kElems; ++e)
-                        if (col + e < cols) {
+                        if (col + e < cols_left) {
                             if (S::F32) r[i][e] = reinterpret_cast<const uint32_t*>(p)[e];
                             else r[i][e / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1));
                         }
@@ -128,17 +153,15 @@ __global__ __launch_bounds__(S::C::NT, S::C::NT == 512 ? 1 : 2) void head_stream
             }
         };
         // ---- the other operand: packed, K-contiguous rows -------------------------------
-        const char* q0 = args.q + 2 * ((int64_t)t.J * TQ * args.q_ld + k_first);
+        const char* const q0 = args.q + 2 * ((int64_t)t.J * TQ * args.q_ld + k_first);
         auto load_q = [&](int s, u32x4_t (&r)[S::kQItems]) {
-            if (s >= slabs) return;
             #pragma unroll
             for (int i = 0; i < S::kQItems; ++i) {
                 const int item = i * NT + tid;
                 if (S::kQChunks % NT != 0 && item >= S::kQChunks) continue;
                 const int part = item / (TQ * S::kRowChunks), rest = item % (TQ * S::kRowChunks);
-                const int row = rest / S::kRowChunks, ch = rest % S::kRowChunks;
-                r[i] = *reinterpret_cast<const u32x4_t*>(q0 + part * args.q_plane +
-                                                         2 * ((int64_t)row * args.q_ld + s * S::kK + ch * 8));
+                const uint32_t off = (uint32_t)(2 * ((rest / S::kRowChunks) * args.q_ld + (rest % S::kRowChunks) * 8));
+                r[i] = *reinterpret_cast<const u32x4_t*>(q0 + part * args.q_plane + 2 * s * S::kK + off);
             }
         };
         auto write_q = [&](char* base, const u32x4_t (&r)[S::kQItems]) {
@@ -208,33 +231,41 @@ __global__ __launch_bounds__(S::C::NT, S::C::NT == 512 ? 1 : 2) void head_stream
         };
 
         // ---- main loop -------------------------------------------------------------------
-        // Slab s is multiplied out of stage s % 2 while slab s + 1 waits in registers and
-        // slab s + 2 of W loads.  Loads return in order, so each slab of the other operand
-        // is asked for before the W slab that is to stay in flight past it.
-        u32x4_t ra[S::kPItems], rb[S::kPItems], rq[S::kQItems];
-        auto step = [&](int s, u32x4_t (&r)[S::kPItems]) {
-            char* const next = smem + ((s + 1) & 1) * S::kStage;
-            multiply(smem + (s & 1) * S::kStage);
-            if (s + 1 < slabs) {
-                write_p(next, r);
-                write_q(next + S::kParts * S::kPPart, rq);
-                load_q(s + 2, rq);
-                load_p(s + 3, r);
-            }
-            __syncthreads();
+        // Slab s is multiplied out of stage s % 2 while slabs s + 1 .. s + kSets wait in, or
+        // load into, the register sets.
+        struct Set {
+            u32x4_t p[S::kPItems], q[S::kQItems];
+        } set[S::kSets];
+        auto fetch = [&](int s, Set& r) {
+            if (s >= slabs) return;
+            load_q(s, r.q);
+            load_p(s, r.p);
         };
-        load_q(0, rq);
-        load_p(0, rb);
-        load_p(1, ra);
+        auto put = [&](int s, const Set& r) {
+            char* const stage = smem + (s & 1) * S::kStage;
+            write_p(stage, r.p);
+            write_q(stage + S::kParts * S::kPPart, r.q);
+        };
+        #pragma unroll
+        for (int i = 0; i < S::kSets; ++i) fetch(i, set[i]);
         __syncthreads();  // the previous tile's epilogue has left the buffers
-        write_p(smem, rb);
-        write_q(smem + S::kParts * S::kPPart, rq);
-        load_q(1, rq);
-        load_p(2, rb);
+        put(0, set[0]);
+        fetch(S::kSets, set[0]);
         __syncthreads();
-        for (int s = 0; s < slabs; s += 2) {
-            step(s, ra);
-            if (s + 1 < slabs) step(s + 1, rb);
+        for (int s0 = 0; s0 < slabs; s0 += S::kSets) {
+            #pragma unroll
+            for (int i = 0; i < S::kSets; ++i) {
+                const int s = s0 + i;
+                if (s < slabs) {
+                    Set& next = set[(i + 1) % S::kSets];
+                    multiply(smem + (s & 1) * S::kStage);
+                    if (s + 1 < slabs) {
+                        put(s + 1, next);
+                        fetch(s + 1 + S::kSets, next);
+                    }
+                    __syncthreads();
+                }
+            }
         }
         write_tile<C, MODE, false, S::kParts>(args, t, sh.tiles_j, smem, acc);
     }
