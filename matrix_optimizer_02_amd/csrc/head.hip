@@ -309,28 +309,23 @@ dmuon_status gather_rows(const Call& c, const Views& v, float* losses, float* ls
     const HeadLayout& L = v.L;
     const bool backward = coef != nullptr;
     if (c.ids != nullptr) HEAD_TRY(launch_head_teacher(teacher_of(c), L.tokens, v.q(), v.flag(), student, c.stream));
-    HeadRowsArgs r{};
-    r.targets = c.ids != nullptr ? nullptr : c.targets;
-    r.flag = v.flag();
-    r.ignore_index = c.ignore_index;
-    r.vocab = L.vocab;
-    r.tokens = (int32_t)L.tokens;
-    r.t_pad = (int32_t)L.t_pad;
-    r.count = v.count();
-    r.low = L.low;
-    r.norm = v.norm();
-    r.src = v.src();
-    r.target = v.target();
-    r.losses = losses;
-    r.lse = lse;
-    HEAD_TRY(launch_head_rows(r, c.stream));
     HeadPrepareArgs a{};
     a.esize = L.esize;
+    a.rows.targets = c.ids != nullptr ? nullptr : c.targets;
+    a.rows.flag = v.flag();
+    a.rows.ignore_index = c.ignore_index;
+    a.rows.vocab = L.vocab;
+    a.rows.tokens = (int32_t)L.tokens;
+    a.rows.t_pad = (int32_t)L.t_pad;
+    a.rows.count = v.count();
+    a.rows.low = L.low;
+    a.rows.norm = v.norm();
+    a.rows.src = v.src();
+    a.rows.target = v.target();
+    a.rows.losses = losses;
+    a.rows.lse = lse;
     a.h.in = c.hidden;
     a.h.cols = L.hidden;
-    a.h.src = v.src();
-    a.h.count = v.count();
-    a.h.rows = L.tokens;
     a.h.out = L.planes == 1 || backward || L.stream_weight ? v.at<uint16_t>(L.off_h) : nullptr;
     a.h.low = L.low;
     a.h.out_rows = L.t_pad;
@@ -494,9 +489,6 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
 
     const Views v{static_cast<char*>(c.workspace), L};
     HeadCoefArgs k{};
-    k.count = v.count();
-    k.src = v.src();
-    k.target = distill ? nullptr : v.target();
     k.q = distill ? v.q() : nullptr;
     k.lse = lse;
     k.grad_losses = grad_losses;

@@ -154,16 +154,15 @@ struct HeadRowsArgs {
     float* losses;
     float* lse;
 };
-hipError_t launch_head_rows(const HeadRowsArgs& a, hipStream_t stream);
-// Rows of a rows x cols matrix to bf16 parts with rows of ld elements: row r of
-// the output is row src[r] (src null: r) for r < limit (limit from device memory
-// when given), zero above up to out_rows.
+// Up to this many tokens the launch that packs the rows finds them too.
+constexpr int kScanTokens = 1024;
+// Rows of a matrix to its operand parts, rows of ld elements: row r of the output
+// is row src[r] of the input (W: row r) below the row count, zero above up to
+// out_rows or a whole tile.
 struct HeadPackArgs {
     const void* in;
     int64_t cols;
-    const int32_t* src;
-    const int32_t* count;  // device row count, or null:
-    int64_t rows;          // rows of the input
+    int64_t rows;          // W: rows of the input
     uint16_t* out;         // bf16: the rows; fp32: three bf16 parts (null: not)
     int64_t out_rows, ld, plane;  // plane in elements
     int32_t low;           // 1: every row again, head_low_row(count) rows further
@@ -205,9 +204,6 @@ struct HeadMergeArgs {
 hipError_t launch_head_merge(const HeadMergeArgs& a, hipStream_t stream);
 // Backward coefficients per compact row (zero in the padding).
 struct HeadCoefArgs {
-    const int32_t* count;
-    const int32_t* src;
-    const int32_t* target;  // cross entropy, else null
     const float2* q;        // distillation, else null
     const float* lse;
     const float* grad_losses;
@@ -217,9 +213,11 @@ struct HeadCoefArgs {
     float* norm;            // the largest |cp|, |ct|
     int64_t t_pad;
 };
-// One launch of up to three independent jobs, all after launch_head_rows: rows
-// packed, W packed (out_rows 0: not) and the coefficients (t_pad 0: not).
+// The rows that carry a loss (rows.tokens 0: found before), then up to three
+// independent jobs: those rows packed, W packed (out_rows 0: not) and the
+// coefficients (t_pad 0: not).
 struct HeadPrepareArgs {
+    HeadRowsArgs rows;
     HeadPackArgs h, w;
     HeadCoefArgs coef;
     int32_t esize;

@@ -202,11 +202,12 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
                 for (int v = 0; v < 16; ++v) m = fmaxf(m, acc[i][j][v]);
             m = fmaxf(m, __shfl_xor(m, 32, 64));
             const float m0 = m == -INFINITY ? 0.f : m;
-            float l = 0.f;
+            float ls[4] = {0.f, 0.f, 0.f, 0.f};  // four chains: an addition need not wait for the one before
             #pragma unroll
             for (int i = 0; i < C::FI; ++i)
                 #pragma unroll
-                for (int v = 0; v < 16; ++v) l += __builtin_amdgcn_exp2f((acc[i][j][v] - m0) * scale);
+                for (int v = 0; v < 16; ++v) ls[v & 3] += __builtin_amdgcn_exp2f((acc[i][j][v] - m0) * scale);
+            float l = (ls[0] + ls[1]) + (ls[2] + ls[3]);
             l += __shfl_xor(l, 32, 64);
             if (khalf == 0)
                 args.part[((int64_t)(args.first_tile + t.I) * C::WR + wr) * args.t_pad + row] = make_float2(m, l);

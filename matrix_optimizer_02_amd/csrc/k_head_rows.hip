@@ -58,14 +58,15 @@ __global__ __launch_bounds__(kRowThreads) void head_teacher_kernel(HeadTeacher t
     }
 }
 
-// One block: the rows that carry a loss keep their order at the front of src,
-// the others fill it from the back.
-constexpr int kScanThreads = 1024;
-__global__ __launch_bounds__(kScanThreads) void head_rows_kernel(HeadRowsArgs a) {
-    __shared__ int wave_n[kScanThreads / 64];
+// The rows that carry a loss keep their order at the front of src, the others
+// fill it from the back.  Run by a whole block; list (null: not) receives the
+// front as well, and only a writer writes to memory.  Returns the rows' number.
+template <int THREADS>
+__device__ __forceinline__ int scan_rows(const HeadRowsArgs& a, bool writer, int* list) {
+    __shared__ int wave_n[THREADS / 64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int n = 0;
-    for (int t0 = 0; t0 < a.tokens; t0 += kScanThreads) {
+    for (int t0 = 0; t0 < a.tokens; t0 += THREADS) {
         const int t = t0 + threadIdx.x;
         const bool in = t < a.tokens;
         const int64_t target = in && a.targets != nullptr ? a.targets[t] : 0;
@@ -74,17 +75,18 @@ __global__ __launch_bounds__(kScanThreads) void head_rows_kernel(HeadRowsArgs a)
         if (lane == 0) wave_n[wave] = __popcll(b);
         __syncthreads();
         int before = __popcll(b & ((1ull << lane) - 1)), all = 0;
-        for (int w = 0; w < kScanThreads / 64; ++w) {
+        for (int w = 0; w < THREADS / 64; ++w) {
             before += w < wave ? wave_n[w] : 0;
             all += wave_n[w];
         }
         __syncthreads();
-        if (live) {
-            const int c = n + before;
+        const int c = n + before;
+        if (live && list != nullptr) list[c] = t;
+        if (live && writer) {
             a.src[c] = t;
             if (a.targets != nullptr) a.target[c] = target >= 0 && target < a.vocab ? (int)target : -2;
-        } else if (in) {
-            a.src[a.tokens - 1 - (t - (n + before))] = t;
+        } else if (in && writer) {
+            a.src[a.tokens - 1 - (t - c)] = t;
             if (a.losses != nullptr) {
                 a.losses[t] = 0.f;
                 a.lse[t] = 0.f;
@@ -92,13 +94,19 @@ __global__ __launch_bounds__(kScanThreads) void head_rows_kernel(HeadRowsArgs a)
         }
         n += all;
     }
-    if (a.targets != nullptr)
-        for (int c = n + threadIdx.x; c < a.t_pad; c += kScanThreads) a.target[c] = -1;
-    if (threadIdx.x == 0) {
+    if (a.targets != nullptr && writer)
+        for (int c = n + threadIdx.x; c < a.t_pad; c += THREADS) a.target[c] = -1;
+    if (threadIdx.x == 0 && writer) {
         a.count[0] = n;
         a.count[1] = a.low ? 2 * head_low_row(n) : n;
-        *a.norm = 0.f;
     }
+    return n;
+}
+
+constexpr int kScanThreads = 1024;
+__global__ __launch_bounds__(kScanThreads) void head_rows_kernel(HeadRowsArgs a) {
+    scan_rows<kScanThreads>(a, true, nullptr);
+    if (threadIdx.x == 0) *a.norm = 0.f;
 }
 
 // Eight columns c .. c + 7 of a row, zeros past its end.
@@ -141,8 +149,8 @@ __device__ __forceinline__ uint4 pack_bf16(const float (&x)[8]) {
 
 // One wave per output row, 8 columns a lane and step.
 template <int ESIZE>
-__device__ __forceinline__ void pack_rows(const HeadPackArgs& a, int block, int blocks) {
-    const int64_t limit = a.count != nullptr ? *a.count : a.rows;
+__device__ __forceinline__ void pack_rows(const HeadPackArgs& a, const int32_t* src, int64_t limit, int block,
+                                          int blocks) {
     // rows past the last one: zeros up to a whole tile
     int64_t end = (limit + kHeadTile - 1) / kHeadTile * kHeadTile;
     if (end == 0) end = kHeadTile;
@@ -153,7 +161,7 @@ __device__ __forceinline__ void pack_rows(const HeadPackArgs& a, int block, int 
     constexpr int kWavesBlock = kRowThreads / 64;
     for (int64_t r = (int64_t)block * kWavesBlock + (threadIdx.x >> 6); r < end; r += (int64_t)blocks * kWavesBlock) {
         const int64_t of = r < low_row ? r : r - low_row;
-        const int64_t from = of < limit ? (a.src != nullptr ? (int64_t)a.src[of] : of) : -1;
+        const int64_t from = of < limit ? (src != nullptr ? (int64_t)src[of] : of) : -1;
         float scale = 1.f;
         if (ESIZE == 4 && a.half2 != nullptr) {
             // a power of two that puts the row's largest element in [2^14, 2^15)
@@ -340,41 +348,95 @@ __global__ __launch_bounds__(kRowThreads) void head_student_kernel(HeadStudentAr
     }
 }
 
-__device__ __forceinline__ void coefficients(const HeadCoefArgs& a, int block) {
-    const int64_t c = (int64_t)block * kRowThreads + threadIdx.x;
-    if (c >= a.t_pad) return;
-    float lse = 0.f, cp = 0.f, ct = 0.f;
-    if (c < *a.count) {
-        const int t = a.src[c];
-        lse = a.lse[t];
-        ct = a.temp * a.grad_losses[t];
-        cp = a.grad_lse != nullptr ? ct + a.grad_lse[t] : ct;
-        const bool bad = a.target != nullptr ? a.target[c] < 0 : a.q[t].x != a.q[t].x;
-        // (integer order is float order for these bits; the maximum does not depend on the order)
-        const float m = fmaxf(fabsf(cp), fabsf(ct));
-        if (m < INFINITY) atomicMax(reinterpret_cast<unsigned int*>(a.norm), __float_as_uint(m));
-        if (bad) cp = nan_f();
-    }
-    a.lse_c[c] = lse;
-    a.cp[c] = cp;
+// The coefficients of compact row c < n, of token t; the larger one's magnitude.
+__device__ __forceinline__ float coefficients(const HeadCoefArgs& a, int64_t c, int t, bool bad) {
+    const float ct = a.temp * a.grad_losses[t];
+    const float cp = a.grad_lse != nullptr ? ct + a.grad_lse[t] : ct;
+    a.lse_c[c] = a.lse[t];
+    a.cp[c] = bad ? nan_f() : cp;
     a.ct[c] = ct;
+    const float m = fmaxf(fabsf(cp), fabsf(ct));
+    return m < INFINITY ? m : 0.f;
+}
+__device__ __forceinline__ void no_coefficients(const HeadCoefArgs& a, int64_t c) {
+    a.lse_c[c] = 0.f;
+    a.cp[c] = 0.f;
+    a.ct[c] = 0.f;
 }
 
+// After head_rows_kernel.
 template <int ESIZE>
 __global__ __launch_bounds__(kRowThreads) void head_prepare_kernel(HeadPrepareArgs a) {
     int block = (int)blockIdx.x;
     if (block < a.h_blocks) {
-        pack_rows<ESIZE>(a.h, block, a.h_blocks);
+        pack_rows<ESIZE>(a.h, a.rows.src, *a.rows.count, block, a.h_blocks);
         return;
     }
     block -= a.h_blocks;
-    if (block < a.w_blocks) pack_rows<ESIZE>(a.w, block, a.w_blocks);
-    else coefficients(a.coef, block - a.w_blocks);
+    if (block < a.w_blocks) {
+        pack_rows<ESIZE>(a.w, nullptr, a.w.rows, block, a.w_blocks);
+        return;
+    }
+    const HeadCoefArgs& k = a.coef;
+    const int64_t c = (int64_t)(block - a.w_blocks) * kRowThreads + threadIdx.x;
+    if (c >= k.t_pad) return;
+    if (c >= *a.rows.count) {
+        no_coefficients(k, c);
+        return;
+    }
+    const int t = a.rows.src[c];
+    const float m = coefficients(k, c, t, k.q != nullptr ? k.q[t].x != k.q[t].x : a.rows.target[c] < 0);
+    // (integer order is float order for these bits; the maximum does not depend on the order)
+    atomicMax(reinterpret_cast<unsigned int*>(k.norm), __float_as_uint(m));
 }
 
-// One wave per row with a loss: ds at each teacher id of the piece, from the
-// student logit of the forward call; an id held twice takes the sum of its
-// entries' q, which both of them write.
+// The same with the rows found here, by every block for itself (at most
+// kScanTokens tokens): one launch less.
+template <int ESIZE>
+__global__ __launch_bounds__(kRowThreads) void head_scan_prepare_kernel(HeadPrepareArgs a) {
+    __shared__ int list[kScanTokens];
+    __shared__ float largest[kRowThreads / 64];
+    int block = (int)blockIdx.x;
+    if (block >= a.h_blocks && block < a.h_blocks + a.w_blocks) {
+        pack_rows<ESIZE>(a.w, nullptr, a.w.rows, block - a.h_blocks, a.w_blocks);
+        return;
+    }
+    const int n = scan_rows<kRowThreads>(a.rows, block == 0, list);
+    __syncthreads();
+    if (block < a.h_blocks) {
+        pack_rows<ESIZE>(a.h, list, n, block, a.h_blocks);
+        return;
+    }
+    const HeadCoefArgs& k = a.coef;  // one block
+    float m = 0.f;
+    for (int c = threadIdx.x; c < k.t_pad; c += kRowThreads) {
+        if (c >= n) {
+            no_coefficients(k, c);
+            continue;
+        }
+        const int t = list[c];
+        bool bad;
+        if (k.q != nullptr) {
+            bad = k.q[t].x != k.q[t].x;
+        } else {
+            const int64_t target = a.rows.targets[t];
+            bad = target < 0 || target >= a.rows.vocab;
+        }
+        m = fmaxf(m, coefficients(k, c, t, bad));
+    }
+    m = wave_max(m);
+    if ((threadIdx.x & 63) == 0) largest[threadIdx.x >> 6] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kRowThreads / 64; ++w) m = fmaxf(m, largest[w]);
+        *k.norm = m;
+    }
+}
+
+// One wave per row with a loss: ds at each teacher id of the piece; an id held
+// twice takes the sum of its entries' q.  bf16: from the student logit of the
+// forward call, so that p - q is rounded once.  fp32: the tile's own cp p, whole in
+// its three parts, less cp q (its p and lse come from one and the same logit).
 __global__ __launch_bounds__(kRowThreads) void head_fix_kernel(HeadFixArgs a) {
     const int lane = threadIdx.x & 63;
     const int64_t c = (int64_t)blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6);
@@ -393,6 +455,7 @@ __global__ __launch_bounds__(kRowThreads) void head_fix_kernel(HeadFixArgs a) {
         if (!__builtin_amdgcn_ballot_w64(here)) continue;
         const int mine = here ? (int)(id - a.v0) : -1;  // (a piece has fewer than 2^31 rows)
         float q = 0.f;
+        bool first = true;  // of the entries with this id
         for (int j0 = 0; j0 < a.t.k; j0 += 64) {
             const int j = j0 + lane;
             const int64_t other = j < a.t.k ? ids[j] : -1;
@@ -403,12 +466,19 @@ __global__ __launch_bounds__(kRowThreads) void head_fix_kernel(HeadFixArgs a) {
                 const int o = __builtin_amdgcn_readlane(off, i);
                 const float x = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(qj), i));
                 q += o == mine ? x : 0.f;
+                first = first && !(o == mine && j0 + i < k);
             }
         }
-        if (!here) continue;
-        const float p = expf(fmaf(a.student[row * a.t.k + k], a.t.inv_temp, -lse));
-        float g = cp * (p - q);
+        if (!here || !first) continue;
         uint16_t* out = a.g + c * a.g_ld + mine;
+        float g;
+        if (a.planes > 1) {
+            float cpp = 0.f;
+            for (int part = a.planes - 1; part >= 0; --part) cpp += bf16_to_f32(out[part * a.g_plane]);
+            g = fmaf(-cp, q, cpp);
+        } else {
+            g = cp * (expf(fmaf(a.student[row * a.t.k + k], a.t.inv_temp, -lse)) - q);
+        }
         for (int part = 0; part < (a.low ? 2 : a.planes); ++part) {
             const uint16_t b = f32_to_bf16(g);
             out[part * low_step] = b;
@@ -511,21 +581,26 @@ hipError_t launch_head_teacher(const HeadTeacher& t, int64_t tokens, float2* q, 
     return hipGetLastError();
 }
 
-hipError_t launch_head_rows(const HeadRowsArgs& a, hipStream_t stream) {
-    hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(kScanThreads), 0, stream, a);
-    return hipGetLastError();
-}
-
 hipError_t launch_head_prepare(const HeadPrepareArgs& args, hipStream_t stream) {
     HeadPrepareArgs a = args;
     const int64_t per = kRowThreads / 64;
+    const bool scan = a.rows.tokens > 0 && a.rows.tokens <= kScanTokens;
+    if (a.rows.tokens > kScanTokens) {
+        hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(kScanThreads), 0, stream, a.rows);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     a.h_blocks = a.h.out_rows > 0 ? (int32_t)blocks_for(a.h.out_rows, per, 8192) : 0;
     a.w_blocks = a.w.out_rows > 0 ? (int32_t)blocks_for(a.w.out_rows, per, 8192) : 0;
-    a.coef_blocks = (int32_t)((a.coef.t_pad + kRowThreads - 1) / kRowThreads);
-    const int32_t blocks = a.h_blocks + a.w_blocks + a.coef_blocks;
-    if (blocks == 0) return hipSuccess;
-    if (a.esize == 2) hipLaunchKernelGGL((head_prepare_kernel<2>), dim3(blocks), dim3(kRowThreads), 0, stream, a);
-    else hipLaunchKernelGGL((head_prepare_kernel<4>), dim3(blocks), dim3(kRowThreads), 0, stream, a);
+    a.coef_blocks = scan ? (a.coef.t_pad > 0) : (int32_t)((a.coef.t_pad + kRowThreads - 1) / kRowThreads);
+    const dim3 grid(a.h_blocks + a.w_blocks + a.coef_blocks), block(kRowThreads);
+    if (a.esize == 2) {
+        if (scan) hipLaunchKernelGGL((head_scan_prepare_kernel<2>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((head_prepare_kernel<2>), grid, block, 0, stream, a);
+    } else {
+        if (scan) hipLaunchKernelGGL((head_scan_prepare_kernel<4>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((head_prepare_kernel<4>), grid, block, 0, stream, a);
+    }
     return hipGetLastError();
 }
 
