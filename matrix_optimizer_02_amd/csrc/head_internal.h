@@ -22,11 +22,10 @@ constexpr int kHeadTile = 256;  // every tile edge divides it: arrays are padded
 constexpr int kHeadSlab = 64;   // K slab
 constexpr int kHeadMaxPlanes = 3;
 
-// Parts of an operand element.
+// Parts of an operand element (fp32 operands of dH and dW: three bf16 parts).
 enum HeadKind : int32_t {
     kHeadBf16 = 0,    // as it is
-    kHeadHalf2 = 1,   // fp32 as two fp16 parts, rows scaled (logits)
-    kHeadBf16x3 = 2   // fp32 as three bf16 parts (gradients)
+    kHeadHalf2 = 1    // fp32 as two fp16 parts, rows scaled (logits)
 };
 // bf16 parts of the gradients' operands: 1 (bf16) or 3 (fp32).
 inline int head_planes(int32_t dtype) { return dtype == DMUON_BF16 ? 1 : kHeadMaxPlanes; }
@@ -121,6 +120,8 @@ struct HeadGemmArgs {
 };
 
 hipError_t launch_head_gemm(int mode, HeadTile tile, const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream);
+// ... dH and dW of fp32 operands (k_head_x3.hip).
+hipError_t launch_head_x3(int mode, HeadTile tile, const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream);
 // The same with W read in place whatever its width and type (Lse, Grad, dH;
 // tiles 256 x 128, 256 x 64 and 64 x 64).
 hipError_t launch_head_stream(int mode, HeadTile tile, const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream);

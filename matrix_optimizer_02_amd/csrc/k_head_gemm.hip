@@ -15,10 +15,8 @@
 // than fp32's own additions of more than 8 products may be (a logit's error
 // counts absolutely: exp turns it into a relative one).  A row's 32 hi and 32 lo
 // values of a k-block lie next to each other, so a slab holds both and takes 6
-// MFMA k-steps (hi hi, hi lo, lo hi).  The gradients' operands come as three
-// bf16 parts (24 bits whatever the magnitude: ds spans all of fp32's range) and
-// six products hi hi, hi mid, mid hi, mid mid, hi lo, lo hi, one after the
-// other; they leave out only terms below 2^-23 of a product.
+// MFMA k-steps (hi hi, hi lo, lo hi).  The gradients of fp32 operands:
+// k_head_x3.hip.
 //
 // Tiles.  256 x 256 outputs, 8 waves, for work that fills the chip; 256 x 128
 // where 256 token rows would be mostly padding; 256 x 64 for batches of at most
@@ -33,8 +31,7 @@ namespace {
 
 using namespace head;
 
-// KIND: kHeadBf16, kHeadHalf2 (logits of fp32 operands) or kHeadBf16x3 (their
-// gradients).
+// KIND: kHeadBf16, or kHeadHalf2 (logits of fp32 operands).
 template <typename C, int MODE, int KIND>
 __global__ __launch_bounds__(C::NT, C::NT == 512 ? 1 : 2) void head_gemm_kernel(HeadGemmArgs args) {
     constexpr bool PW = MODE == kHeadDh || is_dw(MODE);  // P is K-major
@@ -111,10 +108,9 @@ __global__ __launch_bounds__(C::NT, C::NT == 512 ? 1 : 2) void head_gemm_kernel(
                 L.voff_q[par] = (uint32_t)(2 * (row * args.q_ld + lc * 8));
             }
         }
-        // the next slab to load: product of parts (hi hi, hi mid, mid hi, mid mid, hi lo, lo hi) and k
-        int seg = 0, k0 = 0;
+        int k0 = 0;  // of the next slab to load
         auto load_slab = [&](int stage) {
-            const char* pb = L.p + (KIND == kHeadBf16x3 ? ((0x201100 >> (4 * seg)) & 15) * args.p_plane : 0);
+            const char* pb = L.p;
             if (PW) {
                 if (MODE == kHeadDh && k0 >= L.tail_k)
                     pb = args.p_tail + 2 * (int64_t)(k0 - L.tail_k) * args.p_ld;
@@ -130,8 +126,7 @@ __global__ __launch_bounds__(C::NT, C::NT == 512 ? 1 : 2) void head_gemm_kernel(
                 const int q = wave * C::kPLoads + i;
                 dma16(pb + (int64_t)q * (kPStep * (int64_t)args.p_ld), L.voff_p[i & 1], lds_offset(pd + q * 1024));
             }
-            const char* qb = L.q + (KIND == kHeadBf16x3 ? ((0x021010 >> (4 * seg)) & 15) * args.q_plane : 0) +
-                             (QW ? 2 * (int64_t)k0 * args.q_ld : 2 * (int64_t)k0);
+            const char* qb = L.q + (QW ? 2 * (int64_t)k0 * args.q_ld : 2 * (int64_t)k0);
             char* qd = pd + C::kPBytes;
             constexpr int kQStep = QW ? 2 * WQ::kRows : 16;
             #pragma unroll
@@ -141,10 +136,6 @@ __global__ __launch_bounds__(C::NT, C::NT == 512 ? 1 : 2) void head_gemm_kernel(
                 dma16(qb + (int64_t)q * (kQStep * (int64_t)args.q_ld), vo, lds_offset(qd + q * 1024));
             }
             k0 += kBK;
-            if (k0 == K) {
-                k0 = 0;
-                ++seg;
-            }
         };
         static_assert(C::kPLoads % 2 == 0, "load parity");
 
@@ -157,7 +148,7 @@ __global__ __launch_bounds__(C::NT, C::NT == 512 ? 1 : 2) void head_gemm_kernel(
                 for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
 
         // ---- main loop ---------------------------------------------------------------
-        const int slabs = K / kBK * (KIND == kHeadBf16x3 ? 6 : 1);
+        const int slabs = K / kBK;
         const int swz = swizzle(lrow);
         // transposing read: lane 16 g + s addresses row s / 4 and columns 4 (s % 4) ..
         // of a 4 x 16 block and receives the block's column s: 4 consecutive k
@@ -265,14 +256,11 @@ hipError_t launch_config(int mode, const HeadGemmArgs& a, int64_t max_tiles, hip
             return f32 ? launch<C, kHeadGrad, kHeadHalf2>(a, max_tiles, stream)
                        : launch<C, kHeadGrad, kHeadBf16>(a, max_tiles, stream);
         case kHeadDh:
-            return f32 ? launch<C, kHeadDh, kHeadBf16x3>(a, max_tiles, stream)
-                       : launch<C, kHeadDh, kHeadBf16>(a, max_tiles, stream);
+            return launch<C, kHeadDh, kHeadBf16>(a, max_tiles, stream);
         case kHeadDw:
-            return f32 ? launch<C, kHeadDw, kHeadBf16x3>(a, max_tiles, stream)
-                       : launch<C, kHeadDw, kHeadBf16>(a, max_tiles, stream);
+            return launch<C, kHeadDw, kHeadBf16>(a, max_tiles, stream);
         case kHeadDwSum:
-            return f32 ? launch<C, kHeadDwSum, kHeadBf16x3>(a, max_tiles, stream)
-                       : launch<C, kHeadDwSum, kHeadBf16>(a, max_tiles, stream);
+            return launch<C, kHeadDwSum, kHeadBf16>(a, max_tiles, stream);
         default: return hipErrorInvalidValue;
     }
 }
@@ -282,6 +270,7 @@ hipError_t launch_config(int mode, const HeadGemmArgs& a, int64_t max_tiles, hip
 hipError_t launch_head_gemm(int mode, HeadTile tile, const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream) {
     if (max_tiles <= 0) return hipSuccess;
     if (max_tiles > (int64_t)0x3fffffff) return hipErrorInvalidValue;
+    if (a.parts > 1 && mode != kHeadLse && mode != kHeadGrad) return launch_head_x3(mode, tile, a, max_tiles, stream);
     if (tile.tp == 64) return launch_config<Config<64, 64, 4>>(mode, a, max_tiles, stream);
     if (tile.tq == 64) return launch_config<Config<256, 64, 2>>(mode, a, max_tiles, stream);
     if (tile.tq == 128) return launch_config<Config<256, 128, 3>>(mode, a, max_tiles, stream);
