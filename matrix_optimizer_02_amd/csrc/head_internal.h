@@ -135,7 +135,7 @@ struct HeadTeacher {
     int64_t vocab;
     float inv_temp;
 };
-// Per token: (max, log sum) of the teacher's z / T in q (NaN for a bad id), the
+// Per token: (largest z, log sum of exp((z - it) / T)) of the teacher in q (NaN for a bad id), the
 // flag that the row carries a loss; zeros student_logits (null: not).
 hipError_t launch_head_teacher(const HeadTeacher& t, int64_t tokens, float2* q, int32_t* flag, float* student,
                                hipStream_t stream);

@@ -22,8 +22,10 @@ __device__ __forceinline__ float wave_max(float v) {
 
 __device__ __forceinline__ float nan_f() { return __uint_as_float(0x7fc00000u); }
 
-// One wave per token: the teacher's softmax over its K entries, as (max, log
-// of the sum) of z / T.  A row whose entries are all absent or -inf carries no
+// One wave per token: the teacher's softmax over its K entries, as the largest z
+// and the log of the sum of exp((z - max) / T).  The difference is taken before the
+// division: equal entries then differ by 0 however large they are, also where the
+// compiler fuses the two (the type's lowest value stands in masks).  A row whose entries are all absent or -inf carries no
 // loss; an id past the vocabulary marks the row NaN.
 __global__ __launch_bounds__(kRowThreads) void head_teacher_kernel(HeadTeacher t, int64_t tokens, float2* q,
                                                                    int32_t* flag, float* student) {
@@ -38,7 +40,7 @@ __global__ __launch_bounds__(kRowThreads) void head_teacher_kernel(HeadTeacher t
         const int64_t id = ids[k];
         if (student != nullptr) student[row * t.k + k] = 0.f;
         if (id < 0) continue;
-        const float y = z[k] * t.inv_temp;
+        const float y = z[k];
         if (y == -INFINITY) continue;  // no mass
         held = true;
         bad = bad || id >= t.vocab || y != y;
@@ -50,7 +52,7 @@ __global__ __launch_bounds__(kRowThreads) void head_teacher_kernel(HeadTeacher t
     float l = 0.f;
     if (held && !bad)
         for (int k = lane; k < t.k; k += 64)
-            if (ids[k] >= 0) l += expf(z[k] * t.inv_temp - m);
+            if (ids[k] >= 0) l += expf((z[k] - m) * t.inv_temp);
     l = wave_sum(l);
     if (lane == 0) {
         flag[row] = held;
@@ -289,9 +291,8 @@ __global__ __launch_bounds__(256) void head_merge_kernel(HeadMergeArgs a) {
             } else {
                 s = a.student[at];
             }
-            const float z = a.t.logits[at] * scale;
-            if (z == -INFINITY) continue;
-            const float logq = z - q.x - q.y;
+            const float logq = (a.t.logits[at] - q.x) * scale - q.y;
+            if (logq == -INFINITY) continue;  // no mass
             loss = fmaf(expf(logq), (logq + lse) - s * scale, loss);
         }
     }
@@ -460,7 +461,7 @@ __global__ __launch_bounds__(kRowThreads) void head_fix_kernel(HeadFixArgs a) {
             const int j = j0 + lane;
             const int64_t other = j < a.t.k ? ids[j] : -1;
             const int off = other >= a.v0 && other < a.v1 ? (int)(other - a.v0) : -2;
-            const float qj = off >= 0 ? expf(z[j] * a.t.inv_temp - qs.x - qs.y) : 0.f;
+            const float qj = off >= 0 ? expf((z[j] - qs.x) * a.t.inv_temp - qs.y) : 0.f;
             const int last = min(64, a.t.k - j0);
             for (int i = 0; i < last; ++i) {
                 const int o = __builtin_amdgcn_readlane(off, i);

@@ -2,9 +2,13 @@
 oracle, element by element, with bounds derived from the arithmetic.
 
 With A = |H| |W|^T and u32 = 2^-24, u16 = 2^-8 (half a step of bf16):
-  * a logit is a sum of D exact products (6 D products of bf16 parts for fp32,
-    which leave out at most 3 x 2^-24 of each) in fp32, every addition off by
-    at most 2 u32 of the running sum of magnitudes:
+  * a logit is a sum of D exact products in fp32, every addition off by at most
+    2 u32 of the running sum of magnitudes.  fp32 operands are multiplied in parts:
+    6 D products of three bf16 parts, which leave out at most 3 x 2^-24 = 3 u32 of
+    each, or 3 D products of two fp16 parts (the row scaled so that its largest
+    element is near 2^14), which leave out 2^-21 = 8 u32 of each and, where a low
+    part is a subnormal of fp16, 2^-39 of the row's largest element.  The second
+    form is charged 6 D additions too, which is far more than it leaves out:
         es = (2 D' + 8) u32 A,  D' = D (bf16) or 6 D (fp32), padded to slabs
   * lse: the largest es of the row over T, the sum over the vocabulary in chains
     of at most 64 + 2 parts/16 + 16 additions and exponentials good to 4 u32 with
@@ -259,9 +263,74 @@ def test_distill_parity(shape, k, kind, tau, dtype):
     assert not got["dh"].cpu()[dead].float().any() and not got["losses"].cpu()[dead].any()
 
 
+# More than 1024 tokens: rows found and packed by two launches.  fp32: packed weights, products in three parts, several
+# pieces of the vocabulary.  bf16 rows of odd width that are packed; sums over the tokens in several splits.
+MANY = [(400, 130, 1001), (500, 128, 9000), (1030, 33, 129), (1100, 96, 700), (2100, 64, 300), (2049, 200, 70)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape", MANY, ids=str)
+def test_cross_entropy_parity_many_tokens(shape, dtype):
+    t, d, v = shape
+    say(f"case cross entropy, many tokens {shape} {dtype}")
+    live = np.random.default_rng(t).random(t) < 0.8
+    h, w, y, g = make(t, d, v, dtype, 500 + t, live)
+    got = run_ce(h, w, y, g)
+    clean = torch.where(torch.from_numpy(live)[:, None], h.float(), torch.zeros(())).to(dtype)
+    check_ce(clean, w, y, torch.nan_to_num(g), None, got, str(shape))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape,k,kind,tau", [
+    ((400, 130, 1001), 20, "ragged", 2.0), ((500, 128, 9000), 9, "repeated", 1.0), ((1100, 96, 700), 33, "ragged", 1.5),
+    ((2100, 64, 300), 5, "masked", 3.0)], ids=str)
+def test_distill_parity_many_tokens(shape, k, kind, tau, dtype):
+    t, d, v = shape
+    say(f"case distill, many tokens {shape} k {k} {kind} tau {tau} {dtype}")
+    h, w, _, g = make(t, d, v, dtype, 600 + t)
+    ids, z = teacher(t, k, v, 700 + t, kind)
+    dead = ~(((ids >= 0) & ~(z == -np.inf)).any(1))
+    h[dead] = float("nan")
+    got = run_kd(h, w, ids, z, g, tau)
+    h[dead] = 0.0
+    check_kd(h, w, ids, z, g, tau, got, f"{shape} {kind}")
+    assert not got["dh"].cpu()[dead].float().any() and not got["losses"].cpu()[dead].any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("t", [5, 1100])
+def test_distill_teacher_logits_at_the_types_limits(t, dtype):
+    # equal entries at the lowest value at a temperature whose inverse is no power of two; the lowest beside an
+    # ordinary and beside a large one, whose difference overflows: no mass
+    v, k, lo = 40, 4, float(np.finfo(np.float32).min)
+    say(f"case teacher at the limits {t} {dtype}")
+    h, w, _, g = make(t, 64, v, dtype, 31)
+    ids, z = teacher(t, k, v, 32, "full")
+    z[0] = lo
+    z[1] = torch.tensor([lo, 2.0, lo, 1.0])
+    z[2] = torch.tensor([lo, 1e38, 1e38, -3.0])
+    z[t - 1] = torch.tensor([lo, lo, -np.inf, -np.inf])
+    check_kd(h, w, ids, z, g, 3.0, run_kd(h, w, ids, z, g, 3.0), "limits")
+    check_kd(h, w, ids, z, g, 0.7, run_kd(h, w, ids, z, g, 0.7), "limits, T < 1")
+
+
+def test_a_mask_that_differs_from_call_to_call_leaves_nothing_behind():
+    # one workspace: all rows, then few, then all again
+    t, d, v = 1100, 72, 500
+    ws = workspace(t, d, v, BF16)
+    for kept in (1.0, 0.01, 1.0):
+        live = np.random.default_rng(3).random(t) < kept
+        say(f"case changing mask {kept}")
+        h, w, y, g = make(t, d, v, BF16, 17, live)
+        got = run_ce(h, w, y, g, ws=ws)
+        clean = torch.where(torch.from_numpy(live)[:, None], h.float(), torch.zeros(())).to(BF16)
+        check_ce(clean, w, y, torch.nan_to_num(g), None, got, f"kept {kept}")
+
+
 def test_fp32_products_keep_24_bits():
-    # one word, one non-zero product a row: lse is the logit itself.  The parts left out are at most
-    # 2 x 2^-8 2^-16 + 2^-32 of it, six additions add 6 x 2^-23, lse one rounding: below 2^-20
+    # one word, one non-zero product a row: lse is the logit itself.  Three bf16 parts leave out at most
+    # 2 x 2^-8 2^-16 + 2^-32 of it, two fp16 parts 2^-22 (the low parts' roundings, 2^-23 each, and the
+    # product of the two low parts, 2^-22), six additions add 6 x 2^-23, lse one rounding: below 2^-20
     r = np.random.default_rng(5)
     t, d = 300, 130
     h = np.zeros((t, d), np.float32)
