@@ -85,6 +85,20 @@ struct Loads {
     int tail_k;  // dH: first k (from the tile's first) that lies in the tail copy
 };
 
+// Orders a region of M MFMAs and D fragment reads (of the next region): after
+// each MFMA some of the reads, so that they are on their way under the MFMAs.
+// Left alone, the compiler reads a fragment, waits for it and uses it.
+template <int M, int D>
+__device__ __forceinline__ void weave() {
+    constexpr int kPer = (D + M - 1) / M;
+    #pragma unroll
+    for (int m = 0; m < M; ++m) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);     // MFMA
+        if (m * kPer < D) __builtin_amdgcn_sched_group_barrier(0x100, kPer, 0);  // LDS reads
+    }
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 constexpr bool is_dw(int mode) { return mode == kHeadDw || mode == kHeadDwSum; }
 
 // The tiles of a launch and this workgroup's share of them: XCD x takes one
@@ -127,14 +141,23 @@ __device__ __forceinline__ float norm_of(const float* norm) {
 // Writes a finished tile.  acc[i][j][v]: P row wr RW + 32 i + 8 (v / 4) + 4 khalf
 // + v % 4, Q row wc CW + 32 j + lrow.  SCALED: fp32 logits of scaled rows.  PARTS:
 // bf16 parts of the outputs (Grad) or an fp32 output (dW) where 3.
-template <typename C, int MODE, bool SCALED, int PARTS>
+//
+// The staged tile takes PIECES pieces of its Q rows one after the other, each in
+// the first TQ / PIECES x 2 TP bytes of smem.  prefetch() is called once, when the
+// waves are done with the slabs and what the epilogue itself loads has come: what
+// it loads (into the rest of the LDS) is on its way while the tile is written.
+template <typename C, int MODE, bool SCALED, int PARTS, int PIECES = 1, typename F>
 __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile& t, int tiles_j, char* smem,
-                                           floatx16 (&acc)[C::FI][C::FJ]) {
+                                           floatx16 (&acc)[C::FI][C::FJ], F&& prefetch) {
     constexpr int TP = C::TP, TQ = C::TQ;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave % C::WR, wc = wave / C::WR;
-    const int lrow = lane & 31, khalf = lane >> 5;
+    const int lrow = lane & 31;
+    // Rows are compared as (constant) against (bound - 4 khalf), the lane's part on the one
+    // side that is not a constant: 64 row numbers would otherwise be kept in registers.
+    int khalf = lane >> 5;
+    asm volatile("" : "+v"(khalf));
     if constexpr (SCALED) {
         // the rows' scales out again (powers of two)
         float sq[C::FJ];
@@ -162,6 +185,15 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
         const int64_t left = args.vocab - v_base;
         const int limit = left < C::RW ? (int)(left < 0 ? 0 : left) : C::RW;  // rows inside the vocabulary
         const float scale = args.inv_temp * kLog2e;
+        int target[C::FJ];
+        #pragma unroll
+        for (int j = 0; j < C::FJ; ++j) {
+            target[j] = -1;
+            if (args.target != nullptr) target[j] = args.target[t.J * TQ + wc * C::CW + 32 * j + lrow];
+            asm volatile("" : "+v"(target[j]));
+        }
+        __syncthreads();
+        prefetch();
         #pragma unroll
         for (int j = 0; j < C::FJ; ++j) {
             const int row = t.J * TQ + wc * C::CW + 32 * j + lrow;
@@ -179,10 +211,10 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
                 for (int i = 0; i < C::FI; ++i)
                     #pragma unroll
                     for (int v = 0; v < 16; ++v)
-                        if (32 * i + 8 * (v / 4) + 4 * khalf + v % 4 >= limit) acc[i][j][v] = -INFINITY;
+                        if (32 * i + 8 * (v / 4) + v % 4 >= limit - 4 * khalf) acc[i][j][v] = -INFINITY;
             }
             if (args.target != nullptr) {
-                const int64_t off = args.target[row] - v_base;
+                const int64_t off = target[j] - v_base;
                 const int at = off >= 0 && off < limit ? (int)off : -1;
                 const bool mine = at >= 0 && ((at >> 2) & 1) == khalf;
                 if (__builtin_amdgcn_ballot_w64(mine)) {
@@ -191,7 +223,7 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
                     for (int i = 0; i < C::FI; ++i)
                         #pragma unroll
                         for (int v = 0; v < 16; ++v)
-                            if (at == 32 * i + 8 * (v / 4) + 4 * khalf + v % 4) s = acc[i][j][v];
+                            if (at - 4 * khalf == 32 * i + 8 * (v / 4) + v % 4) s = acc[i][j][v];
                     if (mine) args.target_logit[row] = s;
                 }
             }
@@ -204,15 +236,19 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
             const float m0 = m == -INFINITY ? 0.f : m;
             float ls[4] = {0.f, 0.f, 0.f, 0.f};  // four chains: an addition need not wait for the one before
             #pragma unroll
-            for (int i = 0; i < C::FI; ++i)
+            for (int i = 0; i < C::FI; ++i) {
                 #pragma unroll
                 for (int v = 0; v < 16; ++v) ls[v & 3] += __builtin_amdgcn_exp2f((acc[i][j][v] - m0) * scale);
+                __builtin_amdgcn_sched_barrier(0);  // no more of the differences in registers at once
+            }
             float l = (ls[0] + ls[1]) + (ls[2] + ls[3]);
             l += __shfl_xor(l, 32, 64);
             if (khalf == 0)
                 args.part[((int64_t)(args.first_tile + t.I) * C::WR + wr) * args.t_pad + row] = make_float2(m, l);
         }
     } else if constexpr (MODE == kHeadDh || MODE == kHeadDwSum) {
+        __syncthreads();
+        prefetch();
         float4* d = reinterpret_cast<float4*>(
             args.sums + ((int64_t)(t.split * tiles_j + t.J) * args.tiles_i + t.I) * (TP * TQ));
         #pragma unroll
@@ -233,28 +269,44 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
     } else {
         if constexpr (MODE == kHeadGrad) {
             const float inv_norm = 1.f / norm_of(args.norm);
+            float row_lse[C::FJ], row_cp[C::FJ], row_ct[C::FJ];
+            int row_target[C::FJ];
+            #pragma unroll
+            for (int j = 0; j < C::FJ; ++j) {
+                const int row = t.J * TQ + wc * C::CW + 32 * j + lrow;
+                row_lse[j] = args.lse[row];
+                row_cp[j] = args.cp[row] * inv_norm;
+                row_ct[j] = args.ct[row] * inv_norm;
+                row_target[j] = -1;
+                if (args.target != nullptr) row_target[j] = args.target[row];
+                asm volatile("" : "+v"(row_lse[j]), "+v"(row_cp[j]), "+v"(row_ct[j]), "+v"(row_target[j]));
+            }
+            __syncthreads();
+            prefetch();
             const int64_t v_base = args.v0 + (int64_t)t.I * TP + wr * C::RW;
             const int64_t left = args.vocab - v_base;
             const int limit = left < C::RW ? (int)(left < 0 ? 0 : left) : C::RW;
             #pragma unroll
             for (int j = 0; j < C::FJ; ++j) {
-                const int row = t.J * TQ + wc * C::CW + 32 * j + lrow;
-                const float lse = args.lse[row], cp = args.cp[row] * inv_norm, ct = args.ct[row] * inv_norm;
-                const int64_t off = args.target != nullptr ? args.target[row] - v_base : -1;
+                const float lse = row_lse[j], cp = row_cp[j], ct = row_ct[j];
+                const int64_t off = row_target[j] - v_base;
                 const int at = off >= 0 && off < limit ? (int)off : -1;
                 #pragma unroll
                 for (int i = 0; i < C::FI; ++i)
                     #pragma unroll
                     for (int v = 0; v < 16; ++v) {
-                        const int r = 32 * i + 8 * (v / 4) + 4 * khalf + v % 4;
+                        const int r = 32 * i + 8 * (v / 4) + v % 4;  // less 4 khalf
                         float g = cp * __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], args.inv_temp, -lse) * kLog2e);
-                        if (r == at) g -= ct;
-                        acc[i][j][v] = r < limit ? g : 0.f;
+                        if (r == at - 4 * khalf) g -= ct;
+                        acc[i][j][v] = r < limit - 4 * khalf ? g : 0.f;
                     }
             }
         }
         if constexpr (MODE == kHeadDw) {
-            const float norm = norm_of(args.norm);
+            float norm = norm_of(args.norm);
+            asm volatile("" : "+v"(norm));
+            __syncthreads();
+            prefetch();
             #pragma unroll
             for (int i = 0; i < C::FI; ++i)
                 #pragma unroll
@@ -292,36 +344,39 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
             // (256 token rows: never in two parts)
             constexpr bool kSplit = MODE == kHeadGrad && (PARTS > 1 || TQ <= 128);
             const int kOut = !kSplit ? 1 : PARTS > 1 ? PARTS : args.low + 1;
-            constexpr int kEBytes = 2 * TP, kEChunks = TP / 8;
+            constexpr int kEBytes = 2 * TP, kEChunks = TP / 8, kRows = TQ / PIECES;
             const int low_row = kSplit && PARTS == 1 && args.low ? head_low_row(*args.count) : 0;
             #pragma unroll 1
-            for (int part = 0; part < kOut; ++part) {
-                __syncthreads();
-                #pragma unroll
-                for (int i = 0; i < C::FI; ++i)
+            for (int turn = 0; turn < kOut * PIECES; ++turn) {
+                const int part = turn / PIECES, first = turn % PIECES * kRows;
+                if (turn > 0) __syncthreads();  // the piece before has been read
+                if (PIECES == 1 || wc * C::CW / kRows * kRows == first) {
                     #pragma unroll
-                    for (int j = 0; j < C::FJ; ++j)
+                    for (int i = 0; i < C::FI; ++i)
                         #pragma unroll
-                        for (int v4 = 0; v4 < 4; ++v4) {
-                            const int r = wr * C::RW + 32 * i + 8 * v4 + 4 * khalf;
-                            const int c = wc * C::CW + 32 * j + lrow;
-                            uint16_t b[4];
+                        for (int j = 0; j < C::FJ; ++j)
                             #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                b[e] = f32_to_bf16(acc[i][j][4 * v4 + e]);
-                                if (kSplit) acc[i][j][4 * v4 + e] -= bf16_to_f32(b[e]);
+                            for (int v4 = 0; v4 < 4; ++v4) {
+                                const int r = wr * C::RW + 32 * i + 8 * v4 + 4 * khalf;
+                                const int c = wc * C::CW + 32 * j + lrow - first;
+                                uint16_t b[4];
+                                #pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    b[e] = f32_to_bf16(acc[i][j][4 * v4 + e]);
+                                    if (kSplit) acc[i][j][4 * v4 + e] -= bf16_to_f32(b[e]);
+                                }
+                                uint2 o;
+                                o.x = (uint32_t)b[0] | ((uint32_t)b[1] << 16);
+                                o.y = (uint32_t)b[2] | ((uint32_t)b[3] << 16);
+                                *reinterpret_cast<uint2*>(smem + c * kEBytes + (((r >> 3) ^ (c & (kEChunks - 1))) << 4) +
+                                                          (r & 7) * 2) = o;
                             }
-                            uint2 o;
-                            o.x = (uint32_t)b[0] | ((uint32_t)b[1] << 16);
-                            o.y = (uint32_t)b[2] | ((uint32_t)b[3] << 16);
-                            *reinterpret_cast<uint2*>(smem + c * kEBytes + (((r >> 3) ^ (c & (kEChunks - 1))) << 4) +
-                                                      (r & 7) * 2) = o;
-                        }
+                }
                 __syncthreads();
-                for (int q = tid; q < TQ * kEChunks; q += C::NT) {
-                    const int c = q / kEChunks, ch = q % kEChunks;
-                    const uint4 v = *reinterpret_cast<const uint4*>(smem + c * kEBytes +
-                                                                    ((ch ^ (c & (kEChunks - 1))) << 4));
+                for (int q = tid; q < kRows * kEChunks; q += C::NT) {
+                    const int cp = q / kEChunks, ch = q % kEChunks, c = first + cp;
+                    const uint4 v = *reinterpret_cast<const uint4*>(smem + cp * kEBytes +
+                                                                    ((ch ^ (cp & (kEChunks - 1))) << 4));
                     if (MODE == kHeadGrad) {
                         // the low parts' rows begin where this tile's padding may reach
                         if (low_row != 0 && t.J * TQ + c >= low_row) continue;

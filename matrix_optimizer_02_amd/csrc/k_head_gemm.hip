@@ -21,9 +21,20 @@
 // Tiles.  256 x 256 outputs, 8 waves, for work that fills the chip; 256 x 128
 // where 256 token rows would be mostly padding; 256 x 64 for batches of at most
 // 64 rows, which are bound by reading W; 64 x 64, 4 waves, where the others
-// would leave most CUs idle (head_config in head.hip has the rule).  K goes
-// through a ring of ST slabs of 64 in LDS, filled by direct global->LDS loads
-// ST - 1 slabs ahead; 16-byte chunks are XOR-swizzled by row.
+// would leave most CUs idle (pick_tile in head.hip has the rule, with the measured
+// cost of each shape).  K goes through a ring of ST slabs of 64 in LDS, filled by
+// direct global->LDS loads ST - 1 slabs ahead; 16-byte chunks are XOR-swizzled by row.
+//
+// What bounds it: the MFMA.  The main loop is pipelined in registers: while one set
+// of fragments is multiplied the next is read from LDS, also across the barrier that
+// lands the next slab, and the first slab of the next tile loads behind the epilogue.
+// Against read, wait, multiply (8192 tokens, hidden 4096, vocabulary 128256, bf16):
+// forward 7.33 ms for 7.50, backward 21.4 for 21.8; 238 x 1792 x 16374 backward 92 us
+// for 103.  At that first size Lse reaches 1174 TFLOP/s, dH 1200 and dW 1230, where a
+// library's plain product of the same operands, logits written, reaches 1451, 1345
+// and 1124.  What keeps Lse from more is its epilogue (an exponential a logit, with
+// the MFMA idle: two tiles' accumulators do not fit in one wave's registers) and one
+// workgroup a CU, so that no other covers the barriers.
 #include "head_tile.h"
 
 namespace dmuon {
@@ -33,7 +44,7 @@ using namespace head;
 
 // KIND: kHeadBf16, or kHeadHalf2 (logits of fp32 operands).
 template <typename C, int MODE, int KIND>
-__global__ __launch_bounds__(C::NT, C::NT == 512 ? 1 : 2) void head_gemm_kernel(HeadGemmArgs args) {
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void head_gemm_kernel(HeadGemmArgs args) {
     constexpr bool PW = MODE == kHeadDh || is_dw(MODE);  // P is K-major
     constexpr bool QW = is_dw(MODE);                     // Q is K-major
     constexpr int TP = C::TP, TQ = C::TQ;
@@ -50,10 +61,18 @@ __global__ __launch_bounds__(C::NT, C::NT == 512 ? 1 : 2) void head_gemm_kernel(
     const int n = __builtin_amdgcn_readfirstlane(*args.count);
     const int n_k = n <= kBK ? kBK : (n + kBK - 1) / kBK * kBK;  // dW's K extent
     const Share sh = share_of<TQ, MODE>(args, n, n_k);
-    for (int kq = sh.at; kq < sh.count; kq += sh.step) {
-        const Tile t = tile_at(args, sh, kq);
+    // Where a tile's slabs come from, and its K extent (a multiple of kBK).
+    struct Plan {
+        Tile t;
+        Loads L;
+        int K;
+        bool empty;
+    };
+    auto plan = [&](int kq, Plan& pl) {
+        const Tile t = pl.t = tile_at(args, sh, kq);
+        Loads& L = pl.L;
+        int& K = pl.K;
         // ---- operands ----------------------------------------------------------------
-        int K;  // this tile's K extent, a multiple of kBK
         int k_first = 0;
         if (MODE == kHeadDh) {
             k_first = t.split * args.split_k;
@@ -62,12 +81,16 @@ __global__ __launch_bounds__(C::NT, C::NT == 512 ? 1 : 2) void head_gemm_kernel(
             K = n_k;
         } else if (MODE == kHeadDwSum) {
             const int each = (n_k / kBK + args.splits - 1) / args.splits * kBK;
-            k_first = imin(t.split * each, n_k);
+            k_first = t.split * each;
             K = imin(each, n_k - k_first);
+            pl.empty = K <= 0;  // a last split may have nothing: it multiplies a slab for nothing
+            if (pl.empty) {
+                k_first = 0;
+                K = kBK;
+            }
         } else {
             K = args.k;
         }
-        Loads L;
         L.tail_k = INT_MAX;
         if (PW) {
             L.p = args.p + 2 * (int64_t)k_first * args.p_ld;
@@ -108,37 +131,53 @@ __global__ __launch_bounds__(C::NT, C::NT == 512 ? 1 : 2) void head_gemm_kernel(
                 L.voff_q[par] = (uint32_t)(2 * (row * args.q_ld + lc * 8));
             }
         }
-        int k0 = 0;  // of the next slab to load
-        auto load_slab = [&](int stage) {
-            const char* pb = L.p;
-            if (PW) {
-                if (MODE == kHeadDh && k0 >= L.tail_k)
-                    pb = args.p_tail + 2 * (int64_t)(k0 - L.tail_k) * args.p_ld;
-                else
-                    pb += 2 * (int64_t)k0 * args.p_ld;
-            } else {
-                pb += 2 * k0;
-            }
-            char* pd = smem + stage * (C::kPBytes + C::kQBytes);
-            constexpr int kPStep = PW ? 2 * WP::kRows : 16;  // bytes per element of the row stride between 1 KB blocks
-            #pragma unroll
-            for (int i = 0; i < C::kPLoads; ++i) {
-                const int q = wave * C::kPLoads + i;
-                dma16(pb + (int64_t)q * (kPStep * (int64_t)args.p_ld), L.voff_p[i & 1], lds_offset(pd + q * 1024));
-            }
-            const char* qb = L.q + (QW ? 2 * (int64_t)k0 * args.q_ld : 2 * (int64_t)k0);
-            char* qd = pd + C::kPBytes;
-            constexpr int kQStep = QW ? 2 * WQ::kRows : 16;
-            #pragma unroll
-            for (int i = 0; i < C::kQLoads; ++i) {
-                const int q = wave * C::kQLoads + i;
-                const uint32_t vo = C::kQLoads % 2 == 0 ? L.voff_q[i & 1] : (q & 1 ? L.voff_q[1] : L.voff_q[0]);
-                dma16(qb + (int64_t)q * (kQStep * (int64_t)args.q_ld), vo, lds_offset(qd + q * 1024));
-            }
-            k0 += kBK;
-        };
-        static_assert(C::kPLoads % 2 == 0, "load parity");
+    };
+    // the slab at k0 into a stage
+    auto load_slab = [&](const Loads& L, int k0, int stage) {
+        const char* pb = L.p;
+        if (PW) {
+            if (MODE == kHeadDh && k0 >= L.tail_k)
+                pb = args.p_tail + 2 * (int64_t)(k0 - L.tail_k) * args.p_ld;
+            else
+                pb += 2 * (int64_t)k0 * args.p_ld;
+        } else {
+            pb += 2 * k0;
+        }
+        char* pd = smem + stage * (C::kPBytes + C::kQBytes);
+        constexpr int kPStep = PW ? 2 * WP::kRows : 16;  // bytes per element of the row stride between 1 KB blocks
+        #pragma unroll
+        for (int i = 0; i < C::kPLoads; ++i) {
+            const int q = wave * C::kPLoads + i;
+            dma16(pb + (int64_t)q * (kPStep * (int64_t)args.p_ld), L.voff_p[i & 1], lds_offset(pd + q * 1024));
+        }
+        const char* qb = L.q + (QW ? 2 * (int64_t)k0 * args.q_ld : 2 * (int64_t)k0);
+        char* qd = pd + C::kPBytes;
+        constexpr int kQStep = QW ? 2 * WQ::kRows : 16;
+        #pragma unroll
+        for (int i = 0; i < C::kQLoads; ++i) {
+            const int q = wave * C::kQLoads + i;
+            const uint32_t vo = C::kQLoads % 2 == 0 ? L.voff_q[i & 1] : (q & 1 ? L.voff_q[1] : L.voff_q[0]);
+            dma16(qb + (int64_t)q * (kQStep * (int64_t)args.q_ld), vo, lds_offset(qd + q * 1024));
+        }
+    };
+    static_assert(C::kPLoads % 2 == 0, "load parity");
 
+    if (sh.at >= sh.count) return;
+    // The first slab of a tile goes to the last stage: the others hold the output of
+    // the tile before, piece by piece, while it loads.
+    constexpr int kRest = (C::ST - 1) * (C::kPBytes + C::kQBytes);
+    constexpr int kPieces = (TQ * TP * 2 + kRest - 1) / kRest;
+    static_assert(TQ % kPieces == 0 && TQ / kPieces % C::CW == 0, "a wave's columns lie in one piece");
+    // Stores that every wave issues behind that slab's loads, at least: they need not
+    // have completed for the slab to be there.
+    constexpr int kStores = MODE == kHeadLse ? C::FJ
+                            : MODE == kHeadGrad && TQ == 256 ? TQ * TP / 8 / C::NT
+                            : MODE == kHeadDh ? C::FI * C::FJ * 4 : 0;
+    bool behind = false;
+    Plan pl;
+    plan(sh.at, pl);
+    load_slab(pl.L, 0, C::ST - 1);
+    for (int kq = sh.at;;) {
         floatx16 acc[C::FI][C::FJ];
         #pragma unroll
         for (int i = 0; i < C::FI; ++i)
@@ -148,7 +187,7 @@ __global__ __launch_bounds__(C::NT, C::NT == 512 ? 1 : 2) void head_gemm_kernel(
                 for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
 
         // ---- main loop ---------------------------------------------------------------
-        const int slabs = K / kBK;
+        const int slabs = pl.K / kBK;
         const int swz = swizzle(lrow);
         // transposing read: lane 16 g + s addresses row s / 4 and columns 4 (s % 4) ..
         // of a 4 x 16 block and receives the block's column s: 4 consecutive k
@@ -180,60 +219,153 @@ __global__ __launch_bounds__(C::NT, C::NT == 512 ? 1 : 2) void head_gemm_kernel(
         };
         __syncthreads();  // the previous tile's epilogue has left the buffers
         #pragma unroll
-        for (int s = 0; s < C::ST - 1; ++s)
-            if (s < slabs) load_slab(s);
-        int stage = 0;
-        for (int s = 0; s < slabs; ++s) {
-            // loads complete in order: slab s has landed when only later slabs' may be in flight
-            if (C::ST > 2 && s + C::ST - 2 < slabs)
-                wait_vm<(C::ST - 2) * (C::kPLoads + C::kQLoads)>();
-            else
-                wait_vm<0>();
-            __syncthreads();  // ... for every wave, and every wave is done with slab s - 1
-            if (s + C::ST - 1 < slabs) load_slab(stage == 0 ? C::ST - 1 : stage - 1);
-            const char* pb = smem + stage * (C::kPBytes + C::kQBytes);
-            const char* qb = pb + C::kPBytes;
+        for (int s = 1; s < C::ST - 1; ++s)
+            load_slab(pl.L, imin(s, slabs - 1) * kBK, s - 1);
+        int stage = C::ST - 1;
+        // Loads complete in order: a slab has landed when only later slabs' may be in flight.
+        // The barrier lands it for every wave; each is then done with the slab before.
+        auto arrive = [&] {
+            wait_vm<(C::ST - 2) * (C::kPLoads + C::kQLoads)>();
+            __syncthreads();
+        };
+        if (C::ST == 2 && behind) {
+            wait_vm<kStores>();
+            __syncthreads();
+        } else {
+            arrive();
+        }
+        // The slab ST - 1 further, into the stage that the slab before s has left.  Past the
+        // tile's end the last slab again: no branch may part the loop's regions, or the
+        // compiler moves the accumulators about.
+        auto load_ahead = [&](int s) {
+            load_slab(pl.L, imin(s + C::ST - 1, slabs - 1) * kBK, stage == 0 ? C::ST - 1 : stage - 1);
+        };
+        constexpr int kPReads = PW ? 2 : 1, kQReads = QW ? 2 : 1;  // LDS reads a fragment takes
+        const char* pb = smem + stage * (C::kPBytes + C::kQBytes);
+        const char* qb = pb + C::kPBytes;
+        auto next_stage = [&] {
             stage = stage + 1 == C::ST ? 0 : stage + 1;
-            if constexpr (KIND == kHeadHalf2) {
-                // k-steps 0, 1 of the slab hold hi, 2, 3 lo
-                bf16x8 fb[KS][C::FJ];
+            pb = smem + stage * (C::kPBytes + C::kQBytes);
+            qb = pb + C::kPBytes;
+        };
+        // Regions: MFMAs on one set of fragments while the next set is read.  The last
+        // region of a slab runs behind the barrier that lands the next one.
+        if constexpr (KIND == kHeadHalf2) {
+            // k-steps 0, 1 of the slab hold hi, 2, 3 lo.  A region: one P fragment pair (i)
+            // of one k-step, its three products with the Q pairs.
+            bf16x8 ph[2], pl_[2], qh[2][C::FJ], ql[2][C::FJ];
+            auto read_pair = [&](int set, int i, int ks) {
+                ph[set] = read_p(pb, i, ks);
+                pl_[set] = read_p(pb, i, ks + 2);
+            };
+            auto read_q_pairs = [&](int ks) {
                 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-                    #pragma unroll
-                    for (int j = 0; j < C::FJ; ++j) fb[ks][j] = read_q(qb, j, ks);
-                #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    #pragma unroll
-                    for (int i = 0; i < C::FI; ++i) {
-                        const halfx8 fa = __builtin_bit_cast(halfx8, read_p(pb, i, ks));
-                        #pragma unroll
-                        for (int j = 0; j < C::FJ; ++j) {
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                                fa, __builtin_bit_cast(halfx8, fb[ks & 1][j]), acc[i][j], 0, 0, 0);
-                            if (ks < 2)
-                                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                                    fa, __builtin_bit_cast(halfx8, fb[2 + ks][j]), acc[i][j], 0, 0, 0);
-                        }
-                    }
+                for (int j = 0; j < C::FJ; ++j) {
+                    qh[ks][j] = read_q(qb, j, ks);
+                    ql[ks][j] = read_q(qb, j, ks + 2);
                 }
-            } else {
+            };
+            auto mma = [&](floatx16& c, const bf16x8& x, const bf16x8& y) {
+                c = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(halfx8, x),
+                                                           __builtin_bit_cast(halfx8, y), c, 0, 0, 0);
+            };
+            auto multiply = [&](int set, int i, int ks) {
                 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    bf16x8 fa[C::FI], fb[C::FJ];
-                    #pragma unroll
-                    for (int i = 0; i < C::FI; ++i) fa[i] = read_p(pb, i, ks);
-                    #pragma unroll
-                    for (int j = 0; j < C::FJ; ++j) fb[j] = read_q(qb, j, ks);
-                    #pragma unroll
-                    for (int i = 0; i < C::FI; ++i)
-                        #pragma unroll
-                        for (int j = 0; j < C::FJ; ++j)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+                for (int j = 0; j < C::FJ; ++j) mma(acc[i][j], pl_[set], qh[ks][j]);
+                #pragma unroll
+                for (int j = 0; j < C::FJ; ++j) mma(acc[i][j], ph[set], ql[ks][j]);
+                #pragma unroll
+                for (int j = 0; j < C::FJ; ++j) mma(acc[i][j], ph[set], qh[ks][j]);
+            };
+            constexpr int U = 2 * C::FI;  // regions of a slab (even)
+            load_ahead(0);
+            read_q_pairs(0);
+            read_pair(0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            for (int s = 0;;) {
+                #pragma unroll
+                for (int u = 0; u < U - 1; ++u) {
+                    if ((u + 1) % C::FI == 0) read_q_pairs((u + 1) / C::FI);
+                    read_pair((u + 1) & 1, (u + 1) % C::FI, (u + 1) / C::FI);
+                    multiply(u & 1, u % C::FI, u / C::FI);
+                    weave<3 * C::FJ, 2 + 2 * C::FJ>();
                 }
+                if (++s == slabs) break;
+                arrive();
+                next_stage();
+                load_ahead(s);
+                read_q_pairs(0);
+                read_pair(0, 0, 0);
+                multiply(1, C::FI - 1, 1);
+                weave<3 * C::FJ, 2 + 2 * C::FJ>();
             }
+            multiply(1, C::FI - 1, 1);
+        } else {
+            // A region: kI P fragments of one k-step.
+            constexpr int kI = C::FI >= 2 ? C::FI / 2 : 1, kParts = C::FI / kI, U = KS * kParts;
+            bf16x8 fa[2][kI], fb[2][C::FJ];
+            auto read_a = [&](int set, int u) {
+                #pragma unroll
+                for (int i = 0; i < kI; ++i) fa[set][i] = read_p(pb, u % kParts * kI + i, u / kParts);
+            };
+            auto read_b = [&](int ks) {
+                #pragma unroll
+                for (int j = 0; j < C::FJ; ++j) fb[ks & 1][j] = read_q(qb, j, ks);
+            };
+            auto multiply = [&](int u) {
+                #pragma unroll
+                for (int i = 0; i < kI; ++i)
+                    #pragma unroll
+                    for (int j = 0; j < C::FJ; ++j)
+                        acc[u % kParts * kI + i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                            fa[u & 1][i], fb[u / kParts & 1][j], acc[u % kParts * kI + i][j], 0, 0, 0);
+            };
+            constexpr int kAReads = kPReads * kI, kAllReads = kAReads + kQReads * C::FJ;
+            static_assert(U % 2 == 0 && KS % 2 == 0, "a slab starts with the sets 0");
+            load_ahead(0);
+            read_b(0);
+            read_a(0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            for (int s = 0;;) {
+                #pragma unroll
+                for (int u = 0; u < U - 1; ++u) {
+                    const bool turn = (u + 1) % kParts == 0;
+                    if (turn) read_b((u + 1) / kParts);
+                    read_a((u + 1) & 1, u + 1);
+                    multiply(u);
+                    if (turn) weave<kI * C::FJ, kAllReads>(); else weave<kI * C::FJ, kAReads>();
+                }
+                if (++s == slabs) break;
+                arrive();
+                next_stage();
+                load_ahead(s);
+                read_b(0);
+                read_a(0, 0);
+                multiply(U - 1);
+                weave<kI * C::FJ, kAllReads>();
+            }
+            multiply(U - 1);
         }
 
-        write_tile<C, MODE, KIND == kHeadHalf2, KIND == kHeadBf16 ? 1 : kHeadMaxPlanes>(args, t, sh.tiles_j, smem, acc);
+        wait_vm<0>();  // the loads past the end, before their stages hold the output
+        if (MODE == kHeadDwSum && pl.empty) {
+            #pragma unroll
+            for (int i = 0; i < C::FI; ++i)
+                #pragma unroll
+                for (int j = 0; j < C::FJ; ++j)
+                    #pragma unroll
+                    for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+        }
+        const Tile t = pl.t;
+        kq += sh.step;
+        const bool more = kq < sh.count;
+        if (more) plan(kq, pl);
+        write_tile<C, MODE, KIND == kHeadHalf2, KIND == kHeadBf16 ? 1 : kHeadMaxPlanes, kPieces>(
+            args, t, sh.tiles_j, smem, acc, [&] {
+                if (more) load_slab(pl.L, 0, C::ST - 1);
+            });
+        if (!more) break;
+        behind = true;
     }
 }
 

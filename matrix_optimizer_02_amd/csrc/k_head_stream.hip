@@ -267,7 +267,7 @@ __global__ __launch_bounds__(S::C::NT, S::C::NT == 512 ? 1 : 2) void head_stream
                 }
             }
         }
-        write_tile<C, MODE, false, S::kParts>(args, t, sh.tiles_j, smem, acc);
+        write_tile<C, MODE, false, S::kParts>(args, t, sh.tiles_j, smem, acc, [] {});
     }
 }
 

@@ -176,7 +176,7 @@ __global__ __launch_bounds__(S::C::NT, S::C::NT == 512 ? 1 : 2) void head_x3_ker
                 }
             }
         }
-        write_tile<C, MODE, false, kHeadMaxPlanes>(args, t, sh.tiles_j, smem, acc);
+        write_tile<C, MODE, false, kHeadMaxPlanes>(args, t, sh.tiles_j, smem, acc, [] {});
     }
 }
 
