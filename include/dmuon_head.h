@@ -28,10 +28,16 @@
  * not ignore_index, or a teacher id >= vocab, makes the row's loss NaN and the
  * gradients NaN (dW too): nothing outside the arrays is ever read or written.
  *
- * Arithmetic.  DMUON_BF16: bf16 operands, fp32 sums, softmax statistics in
- * fp32; ds is rounded to bf16 once as the operand of its two products.
- * DMUON_F32: operands split into three bf16 parts that together hold their 24
- * bits, so the products keep fp32 accuracy (inputs of magnitude up to 3e38).
+ * Arithmetic.  Sums and softmax statistics are fp32.  DMUON_BF16: bf16
+ * operands; ds is rounded to bf16 once as the operand of its two products,
+ * relative to the largest gradient weight, and for at most 128 tokens with a
+ * loss held in two bf16 parts (16 bits).  DMUON_F32: operands are multiplied in
+ * parts, three bf16 parts that hold all 24 bits for the gradients and for the
+ * logits of few tokens, two fp16 parts of rows scaled by a power of two (22 bits)
+ * for the logits otherwise; inputs of magnitude up to 3e38.  A probability is
+ * exp(s / T - lse) with lse rounded to fp32, so it is good to about
+ * 2^-24 (1 + |lse|) relative.  Teacher logits may hold fp32's lowest value
+ * (equal ones share the row's mass) and -inf (no mass).
  *
  * Conventions are those of dmuon_ns.h: status codes, dense row-major arrays,
  * 16-byte aligned device pointers of the current device, a 256-byte aligned

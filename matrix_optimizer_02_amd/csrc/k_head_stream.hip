@@ -13,6 +13,12 @@
 // A slab is 128 bytes of every row of W (Lse, Grad: 32 fp32 or 64 bf16 of K) or
 // as many rows of it (dH).  Two LDS stages; the other operand (packed hidden
 // states, or ds) goes through registers as well.
+//
+// What bounds it: few tokens, the reads of W and the instructions that split it.
+// 64 tokens, fp32, hidden 4090, vocabulary 50000: forward 303 us, 2.7 TB/s of W
+// (a copy reaches 6.0), backward 1320 us.  From some hundred tokens on the split,
+// repeated for every tile of tokens, costs more than a padded copy (layout_of in
+// head.hip has both sides measured).
 #include "head_tile.h"
 
 namespace dmuon {

@@ -315,10 +315,10 @@ def test_distill_teacher_logits_at_the_types_limits(t, dtype):
 
 
 def test_a_mask_that_differs_from_call_to_call_leaves_nothing_behind():
-    # one workspace: all rows, then few, then all again
+    # one workspace: all rows, few, none, all again
     t, d, v = 1100, 72, 500
     ws = workspace(t, d, v, BF16)
-    for kept in (1.0, 0.01, 1.0):
+    for kept in (1.0, 0.01, 0.0, 1.0):
         live = np.random.default_rng(3).random(t) < kept
         say(f"case changing mask {kept}")
         h, w, y, g = make(t, d, v, BF16, 17, live)
