@@ -211,7 +211,7 @@ struct HeadCoefArgs {
     const float* grad_lse;  // or null
     float temp;
     float *lse_c, *cp, *ct;
-    float* norm;            // the largest |cp|, |ct|
+    float* norm;            // the largest |cp|, |ct|, within 2^100 either way
     int64_t t_pad;
 };
 // The rows that carry a loss (rows.tokens 0: found before), then up to three

@@ -357,7 +357,8 @@ __global__ __launch_bounds__(kRowThreads) void head_student_kernel(HeadStudentAr
     }
 }
 
-// The coefficients of compact row c < n, of token t; the larger one's magnitude.
+// The coefficients of compact row c < n, of token t; the larger one's magnitude, for
+// the largest of all, by which ds is divided.
 __device__ __forceinline__ float coefficients(const HeadCoefArgs& a, int64_t c, int t, bool bad) {
     const float ct = a.temp * a.grad_losses[t];
     const float cp = a.grad_lse != nullptr ? ct + a.grad_lse[t] : ct;
@@ -365,7 +366,8 @@ __device__ __forceinline__ float coefficients(const HeadCoefArgs& a, int64_t c, 
     a.cp[c] = bad ? nan_f() : cp;
     a.ct[c] = ct;
     const float m = fmaxf(fabsf(cp), fabsf(ct));
-    return m < INFINITY ? m : 0.f;
+    // (within 2^100 either way, so that its inverse is a normal number)
+    return m > 0.f && m < INFINITY ? fminf(fmaxf(m, 0x1p-100f), 0x1p100f) : 0.f;
 }
 __device__ __forceinline__ void no_coefficients(const HeadCoefArgs& a, int64_t c) {
     a.lse_c[c] = 0.f;

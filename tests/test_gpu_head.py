@@ -314,6 +314,26 @@ def test_distill_teacher_logits_at_the_types_limits(t, dtype):
     check_kd(h, w, ids, z, g, 0.7, run_kd(h, w, ids, z, g, 0.7), "limits, T < 1")
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("t", [9, 1030])
+def test_gradient_weights_of_any_size(t, dtype):
+    # subnormal weights give nothing beyond the underflow that the bounds count, large ones no overflow on the way
+    for size in (1e-40, 1e-30, 1e30):
+        say(f"case weights {size} t {t} {dtype}")
+        h, w, y, g = make(t, 64, 130, dtype, 41)
+        g = (g.double() / g.abs().max() * size).float()
+        got = run_ce(h, w, y, g)
+        check_ce(h, w, y, g, None, got, f"weights {size}")
+    g[0] = float("inf")  # its row's gradients and dW are not finite; the other rows' are right
+    got = run_ce(h, w, y, g)
+    g0 = g.clone()
+    g0[0] = 0.0
+    o = ho.cross_entropy(f64(h), f64(w), y.numpy(), IGN, f64(g0), None)
+    b = bounds(o, f64(h), f64(w), 1.0, dtype)
+    within("others' dh", f64(got["dh"])[1:], o["dh"][1:], b["dh"][1:])
+    assert not bool(got["dh"][0].isfinite().any())
+
+
 def test_a_mask_that_differs_from_call_to_call_leaves_nothing_behind():
     # one workspace: all rows, few, none, all again
     t, d, v = 1100, 72, 500
