@@ -138,6 +138,18 @@ __device__ __forceinline__ float norm_of(const float* norm) {
     return x > 0.f ? x : 1.f;
 }
 
+// Which product tiles take the main loop that is not pipelined in registers: the
+// softmax statistics of 256 x 256 bf16 tiles.  The compiler makes it 82 instructions
+// and the loads, with the row numbers of the epilogue kept in registers, where the
+// pipelined loop takes 300.  Forward, pipelined against plain, one card: 8192 x 4096 x
+// 128256 7.55 / 7.38 ms, 3687 x 3584 x 128256 3.31 / 3.14, 4225 x 396 x 82304 470 / 447
+// us; smaller tiles lose 1 to 2% by it (300 x 576 x 3904 19.3 / 19.6 us), and so do
+// the backward modes (3687 x 3584 x 128256 9.06 / 9.25 ms).
+template <typename C, int MODE>
+constexpr bool plain_loop(bool scaled) {
+    return MODE == kHeadLse && !scaled && C::TQ == 256;
+}
+
 // Writes a finished tile.  acc[i][j][v]: P row wr RW + 32 i + 8 (v / 4) + 4 khalf
 // + v % 4, Q row wc CW + 32 j + lrow.  SCALED: fp32 logits of scaled rows.  PARTS:
 // bf16 parts of the outputs (Grad) or an fp32 output (dW) where 3.
@@ -156,8 +168,10 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
     const int lrow = lane & 31;
     // Rows are compared as (constant) against (bound - 4 khalf), the lane's part on the one
     // side that is not a constant: 64 row numbers would otherwise be kept in registers.
+    // (The plain loop leaves room for them, and is compiled to the shorter code with them.)
+    constexpr bool kRowNumbers = plain_loop<C, MODE>(SCALED);
     int khalf = lane >> 5;
-    asm volatile("" : "+v"(khalf));
+    if constexpr (!kRowNumbers) asm volatile("" : "+v"(khalf));
     if constexpr (SCALED) {
         // the rows' scales out again (powers of two)
         float sq[C::FJ];
@@ -211,7 +225,9 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
                 for (int i = 0; i < C::FI; ++i)
                     #pragma unroll
                     for (int v = 0; v < 16; ++v)
-                        if (32 * i + 8 * (v / 4) + v % 4 >= limit - 4 * khalf) acc[i][j][v] = -INFINITY;
+                        if (kRowNumbers ? 32 * i + 8 * (v / 4) + 4 * khalf + v % 4 >= limit
+                                        : 32 * i + 8 * (v / 4) + v % 4 >= limit - 4 * khalf)
+                            acc[i][j][v] = -INFINITY;
             }
             if (args.target != nullptr) {
                 const int64_t off = target[j] - v_base;
@@ -223,7 +239,9 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
                     for (int i = 0; i < C::FI; ++i)
                         #pragma unroll
                         for (int v = 0; v < 16; ++v)
-                            if (at - 4 * khalf == 32 * i + 8 * (v / 4) + v % 4) s = acc[i][j][v];
+                            if (kRowNumbers ? at == 32 * i + 8 * (v / 4) + 4 * khalf + v % 4
+                                            : at - 4 * khalf == 32 * i + 8 * (v / 4) + v % 4)
+                                s = acc[i][j][v];
                     if (mine) args.target_logit[row] = s;
                 }
             }
@@ -239,7 +257,7 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
             for (int i = 0; i < C::FI; ++i) {
                 #pragma unroll
                 for (int v = 0; v < 16; ++v) ls[v & 3] += __builtin_amdgcn_exp2f((acc[i][j][v] - m0) * scale);
-                __builtin_amdgcn_sched_barrier(0);  // no more of the differences in registers at once
+                if (!kRowNumbers) __builtin_amdgcn_sched_barrier(0);  // no more of the differences in registers at once
             }
             float l = (ls[0] + ls[1]) + (ls[2] + ls[3]);
             l += __shfl_xor(l, 32, 64);

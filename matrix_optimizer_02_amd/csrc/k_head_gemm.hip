@@ -29,12 +29,13 @@
 // of fragments is multiplied the next is read from LDS, also across the barrier that
 // lands the next slab, and the first slab of the next tile loads behind the epilogue.
 // Against read, wait, multiply (8192 tokens, hidden 4096, vocabulary 128256, bf16):
-// forward 7.33 ms for 7.50, backward 21.4 for 21.8; 238 x 1792 x 16374 backward 92 us
-// for 103.  At that first size Lse reaches 1174 TFLOP/s, dH 1200 and dW 1230, where a
-// library's plain product of the same operands, logits written, reaches 1451, 1345
-// and 1124.  What keeps Lse from more is its epilogue (an exponential a logit, with
-// the MFMA idle: two tiles' accumulators do not fit in one wave's registers) and one
-// workgroup a CU, so that no other covers the barriers.
+// backward 21.4 ms for 21.8; 238 x 1792 x 16374 backward 92 us for 103.  The softmax
+// statistics of 256 x 256 bf16 tiles keep the plain loop (plain_loop in head_tile.h
+// has the figures).  At that first size Lse reaches 1200 TFLOP/s, dH 1215 and dW
+// 1220, where a library's plain product of the same operands, logits written, reaches
+// 1451, 1345 and 1124.  What keeps Lse from more is its epilogue (an exponential a
+// logit, with the MFMA idle: two tiles' accumulators do not fit in one wave's
+// registers) and one workgroup a CU, so that no other covers the barriers.
 #include "head_tile.h"
 
 namespace dmuon {
@@ -44,7 +45,8 @@ using namespace head;
 
 // KIND: kHeadBf16, or kHeadHalf2 (logits of fp32 operands).
 template <typename C, int MODE, int KIND>
-__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void head_gemm_kernel(HeadGemmArgs args) {
+__global__ __launch_bounds__(C::NT) __attribute__((
+    amdgpu_waves_per_eu(2, plain_loop<C, MODE>(KIND == kHeadHalf2) ? 8 : 2))) void head_gemm_kernel(HeadGemmArgs args) {
     constexpr bool PW = MODE == kHeadDh || is_dw(MODE);  // P is K-major
     constexpr bool QW = is_dw(MODE);                     // Q is K-major
     constexpr int TP = C::TP, TQ = C::TQ;
@@ -186,6 +188,7 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
                 #pragma unroll
                 for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
 
+        constexpr bool kPlain = plain_loop<C, MODE>(KIND == kHeadHalf2);
         // ---- main loop ---------------------------------------------------------------
         const int slabs = pl.K / kBK;
         const int swz = swizzle(lrow);
@@ -220,7 +223,7 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
         __syncthreads();  // the previous tile's epilogue has left the buffers
         #pragma unroll
         for (int s = 1; s < C::ST - 1; ++s)
-            load_slab(pl.L, imin(s, slabs - 1) * kBK, s - 1);
+            if (!kPlain || s < slabs) load_slab(pl.L, imin(s, slabs - 1) * kBK, s - 1);
         int stage = C::ST - 1;
         // Loads complete in order: a slab has landed when only later slabs' may be in flight.
         // The barrier lands it for every wave; each is then done with the slab before.
@@ -228,12 +231,14 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
             wait_vm<(C::ST - 2) * (C::kPLoads + C::kQLoads)>();
             __syncthreads();
         };
-        if (C::ST == 2 && behind) {
-            wait_vm<kStores>();
-            __syncthreads();
-        } else {
-            arrive();
-        }
+        auto first = [&] {
+            if (C::ST == 2 && behind) {
+                wait_vm<kStores>();
+                __syncthreads();
+            } else {
+                arrive();
+            }
+        };
         // The slab ST - 1 further, into the stage that the slab before s has left.  Past the
         // tile's end the last slab again: no branch may part the loop's regions, or the
         // compiler moves the accumulators about.
@@ -250,7 +255,36 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
         };
         // Regions: MFMAs on one set of fragments while the next set is read.  The last
         // region of a slab runs behind the barrier that lands the next one.
-        if constexpr (KIND == kHeadHalf2) {
+        if constexpr (kPlain) {
+            // read, wait, multiply: see plain_loop
+            for (int s = 0; s < slabs; ++s) {
+                if (C::ST > 2 && s + C::ST - 2 < slabs)
+                    wait_vm<(C::ST - 2) * (C::kPLoads + C::kQLoads)>();
+                else if (C::ST == 2 && s == 0 && behind)
+                    wait_vm<kStores>();
+                else
+                    wait_vm<0>();
+                __syncthreads();
+                if (s + C::ST - 1 < slabs)
+                    load_slab(pl.L, (s + C::ST - 1) * kBK, stage == 0 ? C::ST - 1 : stage - 1);
+                const char* pb = smem + stage * (C::kPBytes + C::kQBytes);
+                const char* qb = pb + C::kPBytes;
+                stage = stage + 1 == C::ST ? 0 : stage + 1;
+                #pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    bf16x8 fa[C::FI], fb[C::FJ];
+                    #pragma unroll
+                    for (int i = 0; i < C::FI; ++i) fa[i] = read_p(pb, i, ks);
+                    #pragma unroll
+                    for (int j = 0; j < C::FJ; ++j) fb[j] = read_q(qb, j, ks);
+                    #pragma unroll
+                    for (int i = 0; i < C::FI; ++i)
+                        #pragma unroll
+                        for (int j = 0; j < C::FJ; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+                }
+            }
+        } else if constexpr (KIND == kHeadHalf2) {
             // k-steps 0, 1 of the slab hold hi, 2, 3 lo.  A region: one P fragment pair (i)
             // of one k-step, its three products with the Q pairs.
             bf16x8 ph[2], pl_[2], qh[2][C::FJ], ql[2][C::FJ];
@@ -278,6 +312,7 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
                 for (int j = 0; j < C::FJ; ++j) mma(acc[i][j], ph[set], qh[ks][j]);
             };
             constexpr int U = 2 * C::FI;  // regions of a slab (even)
+            first();
             load_ahead(0);
             read_q_pairs(0);
             read_pair(0, 0, 0);
@@ -322,6 +357,7 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
             };
             constexpr int kAReads = kPReads * kI, kAllReads = kAReads + kQReads * C::FJ;
             static_assert(U % 2 == 0 && KS % 2 == 0, "a slab starts with the sets 0");
+            first();
             load_ahead(0);
             read_b(0);
             read_a(0, 0);
