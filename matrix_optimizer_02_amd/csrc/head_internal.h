@@ -1,5 +1,5 @@
-// Internal types of the output-head losses: the workspace layout and the
-// kernels' launchers (k_head_gemm.hip, k_head_rows.hip, head.hip).
+// Internal types of the output-head losses: the kernels' arguments and launchers
+// (k_head_gemm.hip, k_head_rows.hip, head.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -7,66 +7,14 @@
 #include <cstddef>
 #include <cstdint>
 
-#include "../../include/dmuon_head.h"
-#include "dmuon_internal.h"
+#include "head_layout.h"
 
 namespace dmuon {
-
-constexpr int64_t kHeadMaxTokens = (int64_t(1) << 24) - 1;
-constexpr int64_t kHeadMaxHidden = 65536;
-constexpr int64_t kHeadMaxVocab = (int64_t(1) << 27) - 1;
-constexpr int32_t kHeadMaxTopK = 1024;
-constexpr int64_t kHeadMaxLogits = int64_t(1) << 42;  // tokens x vocab: keeps every launch's tile count in 31 bits
-
-constexpr int kHeadTile = 256;  // every tile edge divides it: arrays are padded to it
-constexpr int kHeadSlab = 64;   // K slab
-constexpr int kHeadMaxPlanes = 3;
 
 // Parts of an operand element (fp32 operands of dH and dW: three bf16 parts).
 enum HeadKind : int32_t {
     kHeadBf16 = 0,    // as it is
     kHeadHalf2 = 1    // fp32 as two fp16 parts, rows scaled (logits)
-};
-// bf16 parts of the gradients' operands: 1 (bf16) or 3 (fp32).
-inline int head_planes(int32_t dtype) { return dtype == DMUON_BF16 ? 1 : kHeadMaxPlanes; }
-
-// First row of the low parts of ds behind n token rows.
-#if defined(__HIPCC__)
-__host__ __device__
-#endif
-inline int head_low_row(int n) { return n <= kHeadSlab ? kHeadSlab : (n + kHeadSlab - 1) / kHeadSlab * kHeadSlab; }
-
-// An output tile: tp rows of P by tq rows of Q.
-struct HeadTile {
-    int32_t tp, tq;
-};
-constexpr int head_waves(int tp) { return tp == 64 ? 4 : 8; }
-// Waves along a tile's P rows: rows of statistics written per vocab tile.
-constexpr int head_wave_rows(int tp, int tq) { return tp == 64 || tq == 256 ? 2 : 4; }
-// Workgroups the chip holds at once (two of the 64 x 64 tiles' to a CU).
-constexpr int head_slots(int tp) { return tp == 64 ? 512 : 256; }
-
-// Where everything lies in the workspace, and how the work is cut.
-struct HeadLayout {
-    int64_t tokens, hidden, vocab;
-    int32_t top_k, planes, esize;
-    HeadTile s_tile, dh_tile, dw_tile;  // of the logits, dH and dW
-    int64_t t_pad;          // token rows of the padded arrays (multiple of 256)
-    int64_t d_pad;          // K extent of packed rows (multiple of 64)
-    int32_t pack_weight;    // 1: pieces of W are copied (split) into the workspace
-    int32_t stream_weight;  // 1: the stream kernels read W in place
-    int32_t low;            // 1: ds in two bf16 parts, the low ones as further token rows
-    int64_t piece;          // vocab rows of a piece (multiple of 256)
-    int32_t pieces;
-    int64_t split_k;        // dH: vocab rows of a split (multiple of 64)
-    int32_t splits;         // ... splits of a full piece
-    int32_t dw_splits;      // dW: splits of the tokens
-    int32_t keep_logits;    // distillation, small vocabularies: see layout_of
-    // byte offsets
-    size_t off_count, off_norm, off_src, off_tgt, off_lse, off_cp, off_ct, off_tl, off_q, off_flag;
-    size_t off_h, off_w, off_part, off_g, off_dh, off_dw, off_logits;
-    size_t off_h2, off_w2, off_hs, off_ws;  // fp32: the logits' operands and their row scales
-    size_t bytes;
 };
 
 // One launch of tile products: C[r][c] = sum over k of P[r][k] Q[c][k].

@@ -21,8 +21,8 @@
 // Tiles.  256 x 256 outputs, 8 waves, for work that fills the chip; 256 x 128
 // where 256 token rows would be mostly padding; 256 x 64 for batches of at most
 // 64 rows, which are bound by reading W; 64 x 64, 4 waves, where the others
-// would leave most CUs idle (pick_tile in head.hip has the rule, with the measured
-// cost of each shape).  K goes through a ring of ST slabs of 64 in LDS, filled by
+// would leave most CUs idle (pick_tile in head_layout.cpp has the rule, with the
+// measured cost of each shape).  K goes through a ring of ST slabs of 64 in LDS, filled by
 // direct global->LDS loads ST - 1 slabs ahead; 16-byte chunks are XOR-swizzled by row.
 //
 // What bounds it: the MFMA.  The main loop is pipelined in registers: while one set

@@ -17,8 +17,8 @@
 // What bounds it: few tokens, the reads of W and the instructions that split it.
 // 64 tokens, fp32, hidden 4090, vocabulary 50000: forward 303 us, 2.7 TB/s of W
 // (a copy reaches 6.0), backward 1320 us.  From some hundred tokens on the split,
-// repeated for every tile of tokens, costs more than a padded copy (layout_of in
-// head.hip has both sides measured).
+// repeated for every tile of tokens, costs more than a padded copy (head_layout.cpp
+// has both sides measured).
 #include "head_tile.h"
 
 namespace dmuon {

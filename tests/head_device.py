@@ -1,0 +1,188 @@
+"""Device-side checks of the output-head losses for large shapes: inputs, the
+definitions in fp64 on the GPU (a block of tokens at a time) and error bounds.
+
+The bounds are those that tests/test_gpu_head.py derives (its docstring), with
+u32 = 2^-24 and u16 = 2^-8:
+    es = (2 D' + 8) u32 |H| |W|^T            a logit; D' = D (bf16) or 6 D (fp32), padded
+    el = max es / T + (chain + 8) 2 u32 + 4 u32 xmax + 2 u32 |lse|
+    ed = cp p (es / T + el + 8 u32 (1 + |x|)) + 8 u32 (cp p + ct q) + ur |ds|
+    dH: ed |W| + (2 V' + 64) u32 |ds| |W| + out |dH|, dW the same over the tokens
+"""
+
+import torch
+
+from matrix_optimizer_02_amd import dmuon_head as hd
+
+U32, U16 = 2.0 ** -24, 2.0 ** -8
+BF16, F32, F64 = torch.bfloat16, torch.float32, torch.float64
+IGN = -100
+DEVICE = "cuda" if torch.cuda.is_available() else "cpu"  # (the checks themselves are tested on the CPU)
+BLOCK = 1024
+
+
+def pad(x):
+    return max(128, (x + 255) // 256 * 256)
+
+
+def inputs(t, d, v, dtype, seed, edges=(), dead=0.0):
+    """hidden, weight, targets, the words that the rows lean towards, weights.
+    A row's target and the word it leans to (with nearly all of its probability
+    for most rows) are drawn apart, a quarter of them from `edges` (rows next to
+    the borders of pieces and tiles): an output that lost a part of the
+    vocabulary is off by whole terms.  Rows without a loss hold NaN."""
+    g = torch.Generator(device=DEVICE)
+    g.manual_seed(seed)
+    rand = lambda *s: torch.randn(s, generator=g, device=DEVICE)
+    w = (rand(v, d) * (1.3 / d ** 0.5)).to(dtype)
+
+    def words():
+        x = torch.randint(0, v, (t,), generator=g, device=DEVICE)
+        if len(edges):
+            e = torch.tensor(edges, device=DEVICE)
+            pick = e[torch.randint(0, len(e), (t,), generator=g, device=DEVICE)]
+            x = torch.where(torch.rand(t, generator=g, device=DEVICE) < 0.25, pick, x)
+        return x
+
+    y, lean = words(), words()
+    h = (rand(t, d) + (torch.rand((t, 1), generator=g, device=DEVICE) * 12) * w[lean].float()).to(dtype)
+    up = rand(t) / t
+    if dead:
+        off = torch.rand(t, generator=g, device=DEVICE) < dead
+        y[off] = IGN
+        h[off] = float("nan")
+        up[off] = float("nan")
+    return h, w, y, up
+
+
+def teacher(t, k, v, seed, edges=()):
+    g = torch.Generator(device=DEVICE)
+    g.manual_seed(seed)
+    ids = torch.randint(0, v, (t, k), generator=g, device=DEVICE)  # (now and then an id twice)
+    if len(edges):
+        e = torch.tensor(edges, device=DEVICE)
+        pick = e[torch.randint(0, len(e), (t, k), generator=g, device=DEVICE)]
+        ids = torch.where(torch.rand((t, k), generator=g, device=DEVICE) < 0.25, pick, ids)
+    held = torch.randint(0, k + 1, (t, 1), generator=g, device=DEVICE)
+    ids = torch.where(torch.arange(k, device=DEVICE) < held, ids, -1)
+    z = torch.randn((t, k), generator=g, device=DEVICE) * 2 + 5
+    return ids, torch.where(ids >= 0, z, float("nan"))
+
+
+def guarded(shape, dtype):
+    n = 1
+    for s in shape:
+        n *= s
+    full = torch.full((n + 128,), 7.0, dtype=dtype, device=DEVICE)
+    view = full[64:64 + n].view(shape)
+    view.fill_(float("nan"))
+    return full, view
+
+
+def untouched(full, what):
+    assert bool((full[:64] == 7.0).all()) and bool((full[-64:] == 7.0).all()), what
+
+
+def workspace(t, d, v, dtype, k=0):
+    ws = hd.workspace_for(t, d, v, dtype, top_k=k)
+    ws.fill_(0xFF)  # NaN patterns: what a call reads it must have written
+    return ws
+
+
+def run(h, w, up, y=None, ids=None, z=None, tau=1.0, gl=None):
+    """Forward and backward of cross entropy (y) or distillation (ids, z)."""
+    t, d, v, k = h.shape[0], h.shape[1], w.shape[0], 0 if ids is None else ids.shape[1]
+    ws = workspace(t, d, v, h.dtype, k)
+    o = {n: guarded(s, dt) for n, s, dt in (("losses", (t,), F32), ("lse", (t,), F32), ("student", (t, k), F32),
+                                            ("dh", (t, d), h.dtype), ("dw", (v, d), h.dtype))}
+    r = {n: x[1] for n, x in o.items()}
+    if ids is None:
+        hd.head_cross_entropy_forward(h, w, y, r["losses"], r["lse"], ignore_index=IGN, workspace=ws)
+        hd.head_cross_entropy_backward(h, w, y, r["lse"], up, r["dh"], r["dw"], grad_lse=gl, ignore_index=IGN,
+                                       workspace=ws)
+    else:
+        hd.head_distill_forward(h, w, ids, z, r["losses"], r["lse"], r["student"], temperature=tau, workspace=ws)
+        hd.head_distill_backward(h, w, ids, z, r["lse"], r["student"], up, r["dh"], r["dw"], temperature=tau,
+                                 workspace=ws)
+    torch.cuda.synchronize()
+    for n, x in o.items():
+        untouched(x[0], n)
+    return r
+
+
+def within(name, got, ref, bound):
+    err = (got.to(F64) - ref).abs()
+    bad = ~(err <= bound)
+    if bool(bad.any()):
+        i = tuple(int(x) for x in torch.nonzero(bad)[0])
+        raise AssertionError(f"{name}{i}: gpu {float(got[i])!r} ref {float(ref[i])!r} err {float(err[i]):.3e} bound "
+                             f"{float(bound[i]):.3e}; {int(bad.sum())} of {bad.numel()} outside")
+
+
+def check(what, got, h, w, up, y=None, ids=None, z=None, tau=1.0, gl=None):
+    """Every element of every output against the definitions in fp64."""
+    t, d, v, dtype = h.shape[0], h.shape[1], w.shape[0], h.dtype
+    mul = 1 if dtype == BF16 else 6
+    out = U16 if dtype == BF16 else 2 * U32
+    ur = 2.0 ** -22 if dtype == F32 else U16 if t > 128 else 2.0 ** -15
+    chain = 64 + 2 * (v / 64 / 16 + 1) + 16
+    W = w.to(F64)
+    Wt, aW = W.t(), W.abs()
+    aWt = aW.t()
+    dw, bdw, mdw = (torch.zeros_like(W) for _ in range(3))
+    for r0 in range(0, t, BLOCK):
+        rows = slice(r0, min(t, r0 + BLOCK))
+        n = rows.stop - r0
+        if ids is None:
+            live = y[rows] != IGN
+            I = torch.where(live, y[rows], 0)[:, None]
+            Q = live.to(F64)[:, None]
+            LQ, dq = torch.zeros_like(Q), torch.zeros_like(Q)
+        else:
+            held = ids[rows] >= 0
+            live = held.any(1)
+            I = ids[rows].clamp(min=0)
+            zt = torch.where(held, z[rows].to(F64) / tau, float("-inf"))
+            zt = torch.where(live[:, None], zt, 0.0)
+            LQ = torch.log_softmax(zt, 1)
+            Q = torch.where(held, LQ.exp(), 0.0)
+            LQ = torch.where(held, LQ, 0.0)
+            dq = (16 * (1 + torch.where(held, zt.abs(), 0.0)) + ids.shape[1]) * U32 * Q
+        L = live[:, None]
+        H = torch.where(L, h[rows].to(F64), 0.0)
+        G = torch.where(live, up[rows].to(F64), 0.0)[:, None] * tau
+        GL = 0.0 if gl is None else torch.where(live, gl[rows].to(F64), 0.0)[:, None]
+        s = H @ Wt
+        es = (2 * mul * pad(d) + 8) * U32 * (H.abs() @ aWt)
+        lse = torch.logsumexp(s / tau, 1)
+        x = s / tau - lse[:, None]
+        el = es.max(1).values / tau + (chain + 8) * 2 * U32 + 4 * U32 * x.abs().max(1).values + 2 * U32 * lse.abs()
+        within(f"{what} lse from row {r0}", got["lse"][rows], torch.where(live, lse, 0.0), torch.where(live, el, 0.0))
+        sk, ek = s.gather(1, I), es.gather(1, I)
+        if ids is None:
+            ref, b = lse - sk[:, 0], el + ek[:, 0]
+            b = b + 2 * U32 * ref.abs()
+        else:
+            within(f"{what} student from row {r0}", got["student"][rows], torch.where(held & L, sk, 0.0),
+                   torch.where(held & L, ek, 0.0))
+            bracket = LQ.abs() + sk.abs() / tau + lse.abs()[:, None]
+            ref = tau ** 2 * (Q * (LQ - sk / tau + lse[:, None])).sum(1)
+            b = 2 * tau ** 2 * ((Q * (ek / tau + el[:, None])) + dq * (1 + bracket)).sum(1) + 1e-30
+        within(f"{what} losses from row {r0}", got["losses"][rows], torch.where(live, ref, 0.0),
+               torch.where(live, b, 0.0))
+        p = x.exp()
+        hot = torch.zeros_like(s).scatter_add_(1, I, Q)
+        eh = torch.zeros_like(s).scatter_add_(1, I, dq) * G.abs()
+        cp, ct = (G + GL).abs(), G.abs()
+        ds = (G + GL) * p - G * hot
+        ed = cp * p * (es / tau + el[:, None] + 8 * U32 * (1 + x.abs())) + 8 * U32 * (cp * p + ct * hot)
+        ed = torch.where(L, ed + ur * (ds.abs() + ed) + (cp + 2) * 2.0 ** -126, 0.0)
+        mag = ds.abs() + ed
+        ed = ed + 2 * eh
+        ref = ds @ W
+        b = (ed @ aW + (2 * mul * pad(v) + 64) * U32 * (mag @ aW)) * (1 + out) + out * ref.abs()
+        within(f"{what} dh from row {r0}", got["dh"][rows], ref, b)
+        dw += ds.t() @ H
+        bdw += ed.t() @ H.abs()
+        mdw += mag.t() @ H.abs()
+    b = (bdw + (2 * mul * pad(t) + 64) * U32 * mdw) * (1 + out) + out * dw.abs()
+    within(f"{what} dw", got["dw"], dw, b)
