@@ -33,8 +33,14 @@
  * relative to the largest gradient weight, and for at most 128 tokens with a
  * loss held in two bf16 parts (16 bits).  DMUON_F32: operands are multiplied in
  * parts, three bf16 parts that hold all 24 bits for the gradients and for the
- * logits of few tokens, two fp16 parts of rows scaled by a power of two (22 bits)
- * for the logits otherwise; inputs of magnitude up to 3e38.  A probability is
+ * logits of few tokens (forward up to 256, backward up to 384, ignored ones
+ * included), two fp16 parts of rows scaled by a power of two for the logits
+ * otherwise.  A logit is then off by at most 2^-21 of the sum of its products'
+ * magnitudes, and by 2^-22 T more where a row's elements differ by more than 2^17;
+ * calls whose rows could make it more (the largest element of one operand times
+ * the largest sum of a row's magnitudes of the other above 2^17 T) take the three
+ * parts, at up to three times the time of their logits' product.  Inputs of
+ * magnitude up to 3e38.  A probability is
  * exp(s / T - lse) with lse rounded to fp32, so it is good to about
  * 2^-24 (1 + |lse|) relative.  Teacher logits may hold fp32's lowest value
  * (equal ones share the row's mass) and -inf (no mass).

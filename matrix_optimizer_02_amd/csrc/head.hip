@@ -4,6 +4,8 @@
 //             (-> student logits and loss)
 //   backward  (teacher) rows -> pack H, coefficients -> per piece of the
 //             vocabulary: [pack W piece,] ds, (teacher's ids,) dH sums, dW -> dH
+// fp32 with W packed: behind statistics and ds the same from three bf16 parts, by a
+// launch that returns at once unless a row's range needs it (launch_logits).
 // No device memory is allocated and nothing is synchronised.  The number of
 // rows that carry a loss stays on the device: the launches are sized for every
 // token and their workgroups read it.
@@ -128,6 +130,7 @@ HeadPackArgs pack_weight(const Call& c, const Views& v, bool backward, int64_t v
     p.plane = L.piece * L.d_pad;
     p.half2 = v.at<uint16_t>(L.off_w2);
     p.scale = v.at<float>(L.off_ws);
+    if (L.planes > 1) p.range = v.at<float2>(L.off_rw);
     return p;
 }
 
@@ -156,13 +159,14 @@ dmuon_status gather_rows(const Call& c, const Views& v, float* losses, float* ls
     a.rows.lse = lse;
     a.h.in = c.hidden;
     a.h.cols = L.hidden;
-    a.h.out = L.planes == 1 || backward || L.stream_weight ? v.at<uint16_t>(L.off_h) : nullptr;
+    a.h.out = v.at<uint16_t>(L.off_h);
     a.h.low = L.low;
     a.h.out_rows = L.t_pad;
     a.h.ld = L.d_pad;
     a.h.plane = L.t_pad * L.d_pad;
     a.h.half2 = L.pack_weight ? v.at<uint16_t>(L.off_h2) : nullptr;
     a.h.scale = v.at<float>(L.off_hs);
+    if (L.planes > 1 && L.pack_weight) a.h.range = v.at<float2>(L.off_rh);
     const int64_t tail = L.vocab % kHeadTile;
     if (L.pack_weight) a.w = pack_weight(c, v, backward, 0, std::min(L.piece, L.vocab));
     else if (!L.stream_weight && tail != 0) a.w = pack_weight(c, v, backward, L.vocab - tail, tail);
@@ -223,11 +227,26 @@ void logits_args(const Call& c, const Views& v, int64_t v0, int64_t rows, HeadGe
     a.first_tile = (int32_t)(v0 / L.s_tile.tp);
 }
 
-// A product with W as its P operand.
-hipError_t launch_w(int mode, const HeadLayout& L, HeadTile tile, const HeadGemmArgs& a, int64_t max_tiles,
-                    hipStream_t stream) {
-    return L.stream_weight ? launch_head_stream(mode, tile, a, max_tiles, stream)
-                           : launch_head_gemm(mode, tile, a, max_tiles, stream);
+// The logits of vocab rows v0 .. (a: logits_args') and what becomes of them.  fp32 rows in
+// two fp16 parts: then once more from three bf16 parts, by a launch that returns at once
+// unless some row's range is more than two parts hold.
+hipError_t launch_logits(int mode, const Call& c, const Views& v, int64_t v0, int64_t rows, const HeadGemmArgs& a,
+                         int64_t token_rows) {
+    const HeadLayout& L = v.L;
+    const int64_t tiles = a.tiles_i * ceil_div(token_rows, L.s_tile.tq);
+    if (L.stream_weight) return launch_head_stream(mode, L.s_tile, a, tiles, c.stream);
+    const hipError_t e = launch_head_gemm(mode, L.s_tile, a, tiles, c.stream);
+    if (e != hipSuccess || L.planes == 1) return e;
+    HeadGemmArgs b = a;
+    b.p = static_cast<const char*>(c.weight) + v0 * L.hidden * L.esize;
+    b.q = v.ws + L.off_h;
+    b.p_ld = (int32_t)L.hidden;
+    b.q_ld = b.k = (int32_t)L.d_pad;
+    b.p_range = v.at<float2>(L.off_rw);
+    b.p_ranges = head_range_blocks(round_up(std::min(rows, L.vocab - v0), kHeadTile));
+    b.q_range = v.at<float2>(L.off_rh);
+    b.q_ranges = head_range_blocks(L.t_pad);
+    return launch_head_stream(mode, L.s_tile, b, a.tiles_i * ceil_div(token_rows, std::min(128, L.s_tile.tq)), c.stream);
 }
 
 dmuon_status forward(const Call& c, bool distill, float* losses, float* lse, float* student) {
@@ -270,7 +289,7 @@ dmuon_status forward(const Call& c, bool distill, float* losses, float* lse, flo
         a.target_logit = v.target_logit();
         if (L.keep_logits) a.logits = v.at<float>(L.off_logits);
         a.logits_ld = (int32_t)round_up(L.vocab, kHeadTile);
-        HEAD_TRY(launch_w(kHeadLse, L, L.s_tile, a, (int64_t)a.tiles_i * ceil_div(L.tokens, L.s_tile.tq), c.stream));
+        HEAD_TRY(launch_logits(kHeadLse, c, v, v0, step, a, L.tokens));
     }
     HeadMergeArgs m{};
     m.count = v.count();
@@ -348,8 +367,7 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
         a.g = v.ws + L.off_g;
         a.g_plane = 2 * L.t_pad * L.piece;
         a.g_ld = (int32_t)L.piece;
-        const int64_t g_tiles = ceil_div(round_up(L.tokens, kHeadSlab), L.s_tile.tq);
-        HEAD_TRY(launch_w(kHeadGrad, L, L.s_tile, a, a.tiles_i * g_tiles, c.stream));
+        HEAD_TRY(launch_logits(kHeadGrad, c, v, v0, L.piece, a, round_up(L.tokens, kHeadSlab)));
         if (distill) {
             HeadFixArgs f{};
             f.count = v.count();
@@ -383,7 +401,8 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
             h.tiles_i = dh_tiles_i;
             h.sums = v.at<float>(L.off_dh);
             h.accumulate = v0 != 0;
-            HEAD_TRY(launch_w(kHeadDh, L, L.dh_tile, h, h.splits * dh_tiles_i * dh_tiles_j, c.stream));
+            const auto launch = L.stream_weight ? launch_head_stream : launch_head_gemm;
+            HEAD_TRY(launch(kHeadDh, L.dh_tile, h, h.splits * dh_tiles_i * dh_tiles_j, c.stream));
         }
         if (grad_weight != nullptr) {
             HeadGemmArgs g{};

@@ -34,6 +34,8 @@ struct HeadGemmArgs {
     const char* q;
     int64_t p_plane, q_plane;    // bytes between the parts of an operand
     const float *p_scale, *q_scale;  // fp32 logits: what the rows' products are multiplied by
+    const float2 *p_range, *q_range; // stream kernels: run only where two fp16 parts do not hold these ranges (null: run)
+    int32_t p_ranges, q_ranges;
     int32_t p_ld, q_ld;          // elements between rows
     int64_t p_rows;              // rows of W left from the piece's first (stream kernels)
     int32_t parts;               // 1: bf16; 3: fp32
@@ -117,6 +119,7 @@ struct HeadPackArgs {
     int32_t low;           // 1: every row again, head_low_row(count) rows further
     uint16_t* half2;       // fp32: 32 hi, 32 lo fp16 values of every 32 columns, rows of 2 ld
     float* scale;          // ... and the factor that restores a row's scale
+    float2* range;         // ... and per block the largest element and the largest sum of magnitudes of a row
 };
 // Distillation: the student's logits at the teacher's ids.
 struct HeadStudentArgs {

@@ -151,7 +151,7 @@ HeadLayout head_layout_of(dmuon_head_desc d, bool backward) {
     L.off_tl = take(4 * L.t_pad);
     L.off_q = take(8 * L.t_pad);
     L.off_flag = take(4 * L.t_pad);
-    if (!f32 || backward || L.stream_weight) L.off_h = take(2 * L.planes * L.t_pad * L.d_pad);
+    L.off_h = take(2 * L.planes * L.t_pad * L.d_pad);
     // a packed piece of W, or the copy of its last, partial tile
     if (!L.pack_weight && !L.stream_weight) L.off_w = take(2 * kHeadTile * L.d_pad);
     else if (L.pack_weight && (!f32 || backward)) L.off_w = take(2 * L.planes * L.piece * L.d_pad);
@@ -160,6 +160,8 @@ HeadLayout head_layout_of(dmuon_head_desc d, bool backward) {
         L.off_hs = take(4 * L.t_pad);
         L.off_w2 = take(4 * L.piece * L.d_pad);
         L.off_ws = take(4 * L.piece);
+        L.off_rh = take(8 * kHeadRangeBlocks);
+        L.off_rw = take(8 * kHeadRangeBlocks);
     }
     if (backward) {
         L.off_g = take(2 * L.planes * L.t_pad * L.piece);

@@ -40,6 +40,14 @@ constexpr int head_wave_rows(int tp, int tq) { return tp == 64 || tq == 256 ? 2 
 // Workgroups the chip holds at once (two of the 64 x 64 tiles' to a CU).
 constexpr int head_slots(int tp) { return tp == 64 ? 512 : 256; }
 
+// Blocks that pack rows as two fp16 parts, at most: each leaves the largest element
+// and the largest sum of magnitudes of its rows.
+constexpr int kHeadRangeBlocks = 8192;
+inline int head_range_blocks(int64_t rows) {
+    const int64_t b = (rows + 3) / 4;  // a wave a row
+    return (int)(b < kHeadRangeBlocks ? b : kHeadRangeBlocks);
+}
+
 // Where everything lies in the workspace, and how the work is cut.
 struct HeadLayout {
     int64_t tokens, hidden, vocab;
@@ -60,6 +68,7 @@ struct HeadLayout {
     size_t off_count, off_norm, off_src, off_tgt, off_lse, off_cp, off_ct, off_tl, off_q, off_flag;
     size_t off_h, off_w, off_part, off_g, off_dh, off_dw, off_logits;
     size_t off_h2, off_w2, off_hs, off_ws;  // fp32: the logits' operands and their row scales
+    size_t off_rh, off_rw;                  // ... and ranges (kHeadRangeBlocks pairs each)
     size_t bytes;
 };
 

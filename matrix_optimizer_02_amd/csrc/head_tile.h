@@ -25,10 +25,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
 
 // A tile's wave grid: WR waves along P's rows, WC along Q's.
-template <int TP_, int TQ_, int ST_>
+template <int TP_, int TQ_, int ST_, int WR_ = head_wave_rows(TP_, TQ_)>
 struct Config {
     static constexpr int TP = TP_, TQ = TQ_, ST = ST_;
-    static constexpr int WR = head_wave_rows(TP, TQ);
+    static constexpr int WR = WR_;
     static constexpr int WC = head_waves(TP) / WR;
     static constexpr int NW = WR * WC, NT = 64 * NW;
     static constexpr int RW = TP / WR, CW = TQ / WC;

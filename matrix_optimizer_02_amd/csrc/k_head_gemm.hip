@@ -13,7 +13,11 @@
 // scaled by a power of two to put its largest element near 2^14: 22 bits, so a
 // logit is off by at most 2^-21 of the sum of its products' magnitudes, less
 // than fp32's own additions of more than 8 products may be (a logit's error
-// counts absolutely: exp turns it into a relative one).  A row's 32 hi and 32 lo
+// counts absolutely: exp turns it into a relative one).  An element below 2^-17 of
+// its row's largest has a low part among fp16's subnormals and is off by up to
+// 2^-39 of that largest; calls in which this could move a logit by more than 2^-22 T
+// take the three-part products of k_head_stream.hip instead, decided on the device
+// from the rows' largest elements and sums (wide_range there).  A row's 32 hi and 32 lo
 // values of a k-block lie next to each other, so a slab holds both and takes 6
 // MFMA k-steps (hi hi, hi lo, lo hi).  The gradients of fp32 operands:
 // k_head_x3.hip.

@@ -169,21 +169,27 @@ __device__ __forceinline__ void pack_rows(const HeadPackArgs& a, const int32_t* 
     const int64_t low_row = a.low ? head_low_row((int)limit) : end;
     const int lane = threadIdx.x & 63;
     constexpr int kWavesBlock = kRowThreads / 64;
+    float2 range = make_float2(0.f, 0.f);
     for (int64_t r = (int64_t)block * kWavesBlock + (threadIdx.x >> 6); r < end; r += (int64_t)blocks * kWavesBlock) {
         const int64_t of = r < low_row ? r : r - low_row;
         const int64_t from = of < limit ? (src != nullptr ? (int64_t)src[of] : of) : -1;
         float scale = 1.f;
         if (ESIZE == 4 && a.half2 != nullptr) {
             // a power of two that puts the row's largest element in [2^14, 2^15)
-            float m = 0.f;
+            float m = 0.f, sum = 0.f;
             if (from >= 0)
                 for (int64_t c = lane * 8; c < a.cols; c += 512) {
                     float x[8];
                     load_cols<ESIZE>(a.in, from, a.cols, c, vec, x);
                     #pragma unroll
-                    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+                    for (int e = 0; e < 8; ++e) {
+                        m = fmaxf(m, fabsf(x[e]));
+                        sum += fabsf(x[e]);
+                    }
                 }
             m = wave_max(m);
+            // (a NaN counts for neither: it makes its logits NaN in any form)
+            range = make_float2(fmaxf(range.x, m), fmaxf(range.y, wave_sum(sum)));
             // exponents below 2^-100 would need a scale past fp32's range
             const int e = min(max((int)(__float_as_uint(m) >> 23), 27), 254);
             scale = __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
@@ -228,6 +234,16 @@ __device__ __forceinline__ void pack_rows(const HeadPackArgs& a, const int32_t* 
                     for (int e = 0; e < 8; ++e) x[e] -= bf16_to_f32(f32_to_bf16(x[e]));
                 }
             }
+        }
+    }
+    if (ESIZE == 4 && a.range != nullptr) {
+        __shared__ float2 of_wave[kWavesBlock];
+        if (lane == 0) of_wave[threadIdx.x >> 6] = range;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kWavesBlock; ++w)
+                range = make_float2(fmaxf(range.x, of_wave[w].x), fmaxf(range.y, of_wave[w].y));
+            a.range[block] = range;
         }
     }
 }
@@ -601,8 +617,12 @@ hipError_t launch_head_prepare(const HeadPrepareArgs& args, hipStream_t stream) 
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    a.h_blocks = a.h.out_rows > 0 ? (int32_t)blocks_for(a.h.out_rows, per, 8192) : 0;
-    a.w_blocks = a.w.out_rows > 0 ? (int32_t)blocks_for(a.w.out_rows, per, 8192) : 0;
+    auto blocks_of = [&](const HeadPackArgs& p) {
+        if (p.out_rows <= 0) return 0;
+        return p.range != nullptr ? head_range_blocks(p.out_rows) : (int32_t)blocks_for(p.out_rows, per, 8192);
+    };
+    a.h_blocks = blocks_of(a.h);
+    a.w_blocks = blocks_of(a.w);
     a.coef_blocks = scan ? (a.coef.t_pad > 0) : (int32_t)((a.coef.t_pad + kRowThreads - 1) / kRowThreads);
     const dim3 grid(a.h_blocks + a.w_blocks + a.coef_blocks), block(kRowThreads);
     if (a.esize == 2) {

@@ -14,6 +14,12 @@
 // as many rows of it (dH).  Two LDS stages; the other operand (packed hidden
 // states, or ds) goes through registers as well.
 //
+// It also multiplies the logits of larger fp32 calls in which a row's range is more
+// than two fp16 parts hold (wide_range below).  Its launch follows the two-part one,
+// whose results it writes over; in other calls it returns at once (5 us).
+// 819 tokens, hidden 1536, vocabulary 32000 with such rows: forward 807 us for 369,
+// backward 1721 for 1349.
+//
 // What bounds it: few tokens, the reads of W and the instructions that split it.
 // 64 tokens, fp32, hidden 4090, vocabulary 50000: forward 303 us, 2.7 TB/s of W
 // (a copy reaches 6.0), backward 1320 us.  From some hundred tokens on the split,
@@ -57,6 +63,40 @@ struct Stream {
     __device__ static __forceinline__ int swz(int r) { return F32 ? (r >> 2) & 3 : swizzle(r); }
 };
 
+// Whether two fp16 parts, each row scaled by its largest element, leave a logit of
+// these operands off by more than 2^-22 T beside what they leave out of each product:
+// an element is then off by up to 2^-39 of its row's largest, a logit by
+// 2^-39 (max |h| sum |w| + max |w| sum |h|).  Run by a whole block.
+template <int NT>
+__device__ __forceinline__ bool wide_range(const HeadGemmArgs& args, float4* red) {
+    float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+    // eight loads on their way at once
+    auto largest = [](const float2* range, int n, float& element, float& sum) {
+        for (int i = threadIdx.x; i < n; i += 8 * NT) {
+            float2 x[8];
+            #pragma unroll
+            for (int u = 0; u < 8; ++u) x[u] = range[imin(i + u * NT, n - 1)];
+            #pragma unroll
+            for (int u = 0; u < 8; ++u) element = fmaxf(element, x[u].x), sum = fmaxf(sum, x[u].y);
+        }
+    };
+    largest(args.q_range, args.q_ranges, m.x, m.y);
+    largest(args.p_range, args.p_ranges, m.z, m.w);
+    auto join = [&](const float4& o) {
+        m = make_float4(fmaxf(m.x, o.x), fmaxf(m.y, o.y), fmaxf(m.z, o.z), fmaxf(m.w, o.w));
+    };
+    #pragma unroll
+    for (int off = 32; off > 0; off >>= 1)
+        join(make_float4(__shfl_xor(m.x, off, 64), __shfl_xor(m.y, off, 64), __shfl_xor(m.z, off, 64),
+                         __shfl_xor(m.w, off, 64)));
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+    __syncthreads();
+    #pragma unroll
+    for (int w = 0; w < NT / 64; ++w) join(red[w]);
+    __syncthreads();
+    return !((m.x * m.w + m.z * m.y) * args.inv_temp <= 0x1p17f);
+}
+
 template <typename S, int MODE>
 __global__ __launch_bounds__(S::C::NT, S::C::NT == 512 ? 1 : 2) void head_stream_kernel(HeadGemmArgs args) {
     using C = typename S::C;
@@ -69,6 +109,7 @@ __global__ __launch_bounds__(S::C::NT, S::C::NT == 512 ? 1 : 2) void head_stream
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave % C::WR, wc = wave / C::WR;
     const int lrow = lane & 31, khalf = lane >> 5;
+    if (S::F32 && !PW && args.q_range != nullptr && !wide_range<NT>(args, reinterpret_cast<float4*>(smem))) return;
     const int n = __builtin_amdgcn_readfirstlane(*args.count);
     const int n_k = n <= kBK ? kBK : (n + kBK - 1) / kBK * kBK;
     const Share sh = share_of<TQ, MODE>(args, n, n_k);
@@ -306,6 +347,13 @@ hipError_t launch_config(int mode, const HeadGemmArgs& a, int64_t max_tiles, hip
 hipError_t launch_head_stream(int mode, HeadTile tile, const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream) {
     if (max_tiles <= 0) return hipSuccess;
     if (max_tiles > (int64_t)0x3fffffff) return hipErrorInvalidValue;
+    if (tile.tq == 256) {
+        // in the place of a 256 x 256 tile: half of one, its statistics laid out as the whole one's
+        using F = Stream<Config<256, 128, 3, head_wave_rows(256, 256)>, true>;
+        if (a.parts == 1) return hipErrorInvalidValue;
+        if (mode == kHeadLse) return launch<F, kHeadLse>(a, max_tiles, stream);
+        return mode == kHeadGrad ? launch<F, kHeadGrad>(a, max_tiles, stream) : hipErrorInvalidValue;
+    }
     if (tile.tp == 64) return launch_config<Config<64, 64, 4>>(mode, a, max_tiles, stream);
     if (tile.tq == 64) return launch_config<Config<256, 64, 2>>(mode, a, max_tiles, stream);
     return launch_config<Config<256, 128, 3>>(mode, a, max_tiles, stream);
