@@ -9,6 +9,7 @@ import subprocess
 import pytest
 
 import test_gpu_head_large as large
+import test_gpu_head_parts as parts
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "matrix_optimizer_02_amd", "csrc")
@@ -89,6 +90,25 @@ def test_large_cases_reach_every_wide_tile(layouts):
         assert have(kernel, "statistics", M, True) and have(kernel, "ds", M) and have(kernel, "dH", None, None, True)
     assert have("stream f32", "dH", M) and have("stream f32", "ds", M, True, True)
     assert partial_tail >= 8
+
+
+def test_single_product_cases_reach_every_fp32_tile(layouts):
+    reached = set()
+    for t, d, v in parts.SHAPES:
+        fwd, back = layouts([(t, d, v, 0, F32, 0), (t, d, v, 0, F32, 1)])
+        reached |= {r[:3] for r in launches(t, d, v, 0, F32, fwd, back)}
+    W, M, N = (256, 256), (256, 128), (64, 64)
+    for tile in (W, M, N):
+        for what in (("x3 f32", "dH"), ("x3 f32", "dW"), ("x3 f32", "dW in splits"), ("gemm f32", "ds")):
+            assert (*what, tile) in reached, (what, tile)
+    for tile in (M, N):
+        assert ("stream f32", "dH", tile) in reached and ("stream f32", "ds", tile) in reached
+    kept = set()
+    for t, d, v in parts.KEPT:
+        L, = layouts([(t, d, v, 256, F32, 0)])
+        assert L["keep"]
+        kept.add((L["stream"], L["s_tp"], L["s_tq"]))
+    assert kept >= {(1, 64, 64), (1, 256, 64), (1, 256, 128), (0, 64, 64), (0, 256, 128), (0, 256, 256)}
 
 
 def test_layouts_are_consistent(layouts):
