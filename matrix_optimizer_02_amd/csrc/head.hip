@@ -65,8 +65,8 @@ dmuon_status check_call(const Call& c, bool distill, Buffers& b) {
     if (st != DMUON_OK) return st;
     const dmuon_head_desc& d = *c.desc;
     if (distill ? d.top_k < 1 : d.top_k != 0) return DMUON_ERR_INVALID_ARG;
-    if (distill && !(std::isfinite(c.temp) && c.temp > 0.f && std::isfinite(1.f / c.temp) && 1.f / c.temp > 0.f))
-        return DMUON_ERR_INVALID_ARG;
+    // the losses are multiplied by T^2, the logits by 1 / T
+    if (distill && !(c.temp > 0.f && std::isnormal(c.temp * c.temp))) return DMUON_ERR_INVALID_ARG;
     const int64_t e = d.dtype == DMUON_BF16 ? 2 : 4;
     b.add(c.hidden, d.tokens * d.hidden * e, false);
     b.add(c.weight, d.vocab * d.hidden * e, false);
