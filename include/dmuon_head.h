@@ -27,6 +27,9 @@
  * hold (NaN included) reaches nothing.  A target outside [0, vocab) that is
  * not ignore_index, or a teacher id >= vocab, makes the row's loss NaN and the
  * gradients NaN (dW too): nothing outside the arrays is ever read or written.
+ * A teacher entry whose logit is -inf has no mass and its id is not held against
+ * the row: from vocab on it is passed over like an absent one (student_logits 0).
+ * A NaN or +inf logit of a present entry makes the row's loss NaN.
  *
  * Arithmetic.  Sums and softmax statistics are fp32.  DMUON_BF16: bf16
  * operands; ds is rounded to bf16 once as the operand of its two products,

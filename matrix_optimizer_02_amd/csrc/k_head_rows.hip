@@ -33,8 +33,9 @@ __device__ __forceinline__ float nan_f() { return __uint_as_float(0x7fc00000u); 
 // One wave per token: the teacher's softmax over its K entries, as the largest z
 // and the log of the sum of exp((z - max) / T).  The difference is taken before the
 // division: equal entries then differ by 0 however large they are, also where the
-// compiler fuses the two (the type's lowest value stands in masks).  A row whose entries are all absent or -inf carries no
-// loss; an id past the vocabulary marks the row NaN.
+// compiler fuses the two (the type's lowest value stands in masks).  A row whose entries
+// are all absent or -inf carries no loss; an id past the vocabulary marks the row NaN,
+// unless its entry is -inf.
 __global__ __launch_bounds__(kRowThreads) void head_teacher_kernel(HeadTeacher t, int64_t tokens, float2* q,
                                                                    int32_t* flag, float* student) {
     const int lane = threadIdx.x & 63;
