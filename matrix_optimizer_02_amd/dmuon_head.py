@@ -11,6 +11,10 @@ computed by the library's HIP kernels: there is no fallback.
     head_cross_entropy_backward(H, W, targets, lse, grad_losses, grad_H, grad_W, workspace=ws)
 
 grad_W is what adamw_step_batched takes for the head.
+
+The calls write into tensors that they are given and take no part in autograd:
+inputs may require gradients, outputs carry no graph, and the gradients come from
+the backward call alone.
 """
 
 from __future__ import annotations

@@ -50,3 +50,12 @@ def test_teacher_logits_without_a_softmax_make_their_rows_nan(value):
     rows = torch.arange(t, device="cuda") == 9
     assert bool(torch.isnan(got["losses"][rows]).all()) and bool(torch.isfinite(got["losses"][~rows]).all())
     assert bool(torch.isfinite(got["dh"][~rows]).all()) and bool(torch.isnan(got["dh"][rows]).any())
+
+
+def test_inputs_that_require_gradients():
+    print("case requires grad", flush=True)
+    h, w, y, up = dev.inputs(90, 64, 500, F32, 90)
+    plain = dev.run(h, w, up, y=y)
+    got = dev.run(h.clone().requires_grad_(), w.clone().requires_grad_(), up, y=y)
+    for n in ("losses", "lse", "dh", "dw"):
+        assert torch.equal(got[n], plain[n]) and got[n].grad_fn is None
