@@ -33,8 +33,9 @@
  *
  * Arithmetic.  Sums and softmax statistics are fp32.  DMUON_BF16: bf16
  * operands; ds is rounded to bf16 once as the operand of its two products,
- * relative to the largest gradient weight, and for at most 128 tokens with a
- * loss held in two bf16 parts (16 bits).  DMUON_F32: operands are multiplied in
+ * relative to the largest gradient weight (gradients are then off by 1.1 to 1.4
+ * times what rounding them to bf16 alone costs), and in calls of at most 128
+ * tokens, ignored ones included, held in two bf16 parts (16 bits).  DMUON_F32: operands are multiplied in
  * parts, three bf16 parts that hold all 24 bits for the gradients and for the
  * logits of few tokens (forward up to 256, backward up to 384, ignored ones
  * included), two fp16 parts of rows scaled by a power of two for the logits
