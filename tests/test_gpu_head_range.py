@@ -95,3 +95,36 @@ def test_ranges_that_two_parts_hold(temperature):
     mag = (np.abs(h).astype(np.float64) @ np.abs(w).astype(np.float64).T)[:, 0] / temperature
     # 6 x 64 products added up, 8 u32 of each left out, one rounding of lse; and 2^-22
     assert (np.abs(got - ref) <= (2 * 6 * 64 + 16) * 2.0 ** -24 * mag + 2.0 ** -22).all()
+
+
+def test_captured_calls_follow_the_range():
+    # one graph of forward and backward; its inputs' range changes between replays
+    print("case graph, changing range", flush=True)
+    t, d, v = 400, 96, 900
+    h, w, y, up = dev.inputs(t, d, v, torch.float32, 20)
+    w[:, 7] = 0.0
+    ws = {n: dev.workspace(t, d, v, torch.float32) for n in ("graph", "eager")}
+
+    def outs():
+        f = lambda *s: torch.zeros(s, device="cuda")
+        return [f(t), f(t), f(t, d), f(v, d)]
+
+    def call(o, n):
+        dev.hd.head_cross_entropy_forward(h, w, y, o[0], o[1], workspace=ws[n])
+        dev.hd.head_cross_entropy_backward(h, w, y, o[1], up, o[2], o[3], workspace=ws[n])
+
+    captured, eager = outs(), outs()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph):
+            call(captured, "graph")
+    torch.cuda.current_stream().wait_stream(side)
+    for turn, big in enumerate((1.0, 2.0 ** 40, 1.0, -2.0 ** 30, 2.0 ** 40)):
+        h[:, 7] = big
+        call(eager, "eager")
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(captured, eager)), turn
+        got = dict(zip(("losses", "lse", "dh", "dw"), captured))
+        dev.check(f"replay {turn}", got, h, w, up, y=y)
