@@ -46,7 +46,8 @@
  * parts, at up to three times the time of their logits' product.  Inputs of
  * magnitude up to 3e38.  A probability is
  * exp(s / T - lse) with lse rounded to fp32, so it is good to about
- * 2^-24 (1 + |lse|) relative.  Teacher logits may hold fp32's lowest value
+ * 2^-24 (1 + |lse|) relative.  A loss is formed from the distances of logits, not
+ * from lse.  Teacher logits may hold fp32's lowest value
  * (equal ones share the row's mass) and -inf (no mass).
  *
  * Conventions are those of dmuon_ns.h: status codes, dense row-major arrays,
@@ -109,7 +110,8 @@ DMUON_API dmuon_status head_cross_entropy_backward(const dmuon_head_desc* desc, 
  * the gradient.  student_logits (tokens x top_k fp32, written) receives
  * s_t,id(t,k), 0 for absent entries and rows without loss; the backward call
  * takes it.  temperature is > 0 with a normal fp32 square (1.1e-19 to 1.8e19);
- * a loss is good to about T^2 2^-24 (1 + |lse|), beside its logits' error. */
+ * a loss is good to about T^2 2^-24 times its largest term (log q, log vocab, the
+ * distance of s from the row's largest logit over T), beside its logits' error. */
 DMUON_API dmuon_status head_distill_forward(const dmuon_head_desc* desc, const void* hidden, const void* weight,
                                             const int64_t* teacher_ids, const float* teacher_logits,
                                             float temperature, float* losses, float* lse, float* student_logits,

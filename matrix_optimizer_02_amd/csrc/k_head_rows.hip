@@ -294,12 +294,14 @@ __global__ __launch_bounds__(256) void head_merge_kernel(HeadMergeArgs a) {
         l = fmaf(x.y, expf((x.x - m0) * scale), l);
     }
     l = over_groups(l, false);
-    const float lse = fmaf(m, scale, logf(l));
+    // A loss takes the largest logit's distance first: lse, rounded at its own size, would
+    // leave a loss of large logits 2^-24 of those.
+    const float log_l = logf(l), lse = fmaf(m, scale, log_l);
     const int t = in ? a.src[c] : 0;
     const bool writer = in && g == 0;
     if (writer) a.lse[t] = lse;
     if (a.target != nullptr) {
-        if (writer) a.losses[t] = a.target[c] < 0 ? nan_f() : lse - a.target_logit[c];
+        if (writer) a.losses[t] = a.target[c] < 0 ? nan_f() : (m - a.target_logit[c]) + log_l;
         return;
     }
     // distillation: sum of q (log q - s / T + lse) over the row's entries
@@ -318,7 +320,7 @@ __global__ __launch_bounds__(256) void head_merge_kernel(HeadMergeArgs a) {
             }
             const float logq = (a.t.logits[at] - q.x) * scale - q.y;
             if (logq == -INFINITY) continue;  // no mass
-            loss = fmaf(expf(logq), (logq + lse) - s * scale, loss);
+            loss = fmaf(expf(logq), logq + fmaf(m - s, scale, log_l), loss);
         }
     }
     loss = over_groups(loss, false);

@@ -59,3 +59,39 @@ def test_inputs_that_require_gradients():
     got = dev.run(h.clone().requires_grad_(), w.clone().requires_grad_(), up, y=y)
     for n in ("losses", "lse", "dh", "dw"):
         assert torch.equal(got[n], plain[n]) and got[n].grad_fn is None
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("t", [5, 300, 1100])
+def test_losses_of_large_logits_keep_their_bits(t, dtype):
+    # s = 32768 + x, x a multiple of 1/16: exact in every form, 2^-9 to 2^-4 of its rounding.  A loss is a matter of
+    # the differences.  u = 2^-24: the sum of at most 2 (the largest logit's 1 and the rest) in chains of at most
+    # 64 + 24 additions, 2 u each, exponentials of |x| <= 16 good to (4 + 2 |x|) u: 400 u; its logarithm and the
+    # loss's own additions 8 u (1 + loss).  The teacher's part: q good to (16 (1 + |z|) + K) u as ever.
+    print(f"case losses of large logits {t} {dtype}", flush=True)
+    u, v, d, k = 2.0 ** -24, 300, 64, 4
+    g = torch.Generator(device="cuda")
+    g.manual_seed(100 + t)
+    h, w = torch.zeros(t, d, device="cuda"), torch.zeros(v, d, device="cuda")
+    h[:, 0] = 1.0
+    w[:, 0] = 32768.0
+    c = 1 + torch.arange(t, device="cuda") % (d - 1)
+    h[torch.arange(t, device="cuda"), c] = 1.0
+    w[:, 1:] = torch.randint(0, 33, (v, d - 1), generator=g, device="cuda") / 16.0
+    y = torch.randint(0, v, (t,), generator=g, device="cuda")
+    best = torch.randint(0, v, (d,), generator=g, device="cuda")
+    w[best[1:], torch.arange(1, d, device="cuda")] = 12.0
+    y = torch.where(torch.arange(t, device="cuda") % 3 == 0, best[c], y)  # small losses and large ones
+    h, w, up = h.to(dtype), w.to(dtype), torch.full((t,), 1.0 / t, device="cuda")
+    x = w.double()[:, c].t()  # less the common 32768
+    lse = torch.logsumexp(x, 1)
+    got = dev.run(h, w, up, y=y)
+    ref = lse - x.gather(1, y[:, None])[:, 0]
+    dev.within("ce", got["losses"], ref, 400 * u + 8 * u * (1 + ref))
+    ids = torch.stack([y, best[c], (y + 1) % v, (y + 7) % v], 1)
+    z = torch.randn((t, k), generator=g, device="cuda")
+    q = torch.softmax(z.double(), 1)
+    parts = torch.log_softmax(z.double(), 1) - x.gather(1, ids) + lse[:, None]
+    got = dev.run(h, w, up, ids=ids, z=z)
+    bound = (q * (400 * u + 8 * u * (1 + parts.abs()) + 2 * (16 * (1 + z.double().abs()) + k) * u * (1 + parts.abs()))).sum(1)
+    dev.within("kd", got["losses"], (q * parts).sum(1), bound)
