@@ -1,9 +1,9 @@
 // The products of the output-head losses on bf16 MFMA (gfx950), one tile
-// kernel in four modes, each C[r][c] = sum over k of P[r][k] Q[c][k]:
-//   Lse   s^T = W H^T     softmax statistics of every 256-row vocab tile
+// kernel in five modes, each C[r][c] = sum over k of P[r][k] Q[c][k]:
+//   Lse   s^T = W H^T     softmax statistics of every vocab tile
 //   Grad  s^T = W H^T     again, ds = cp exp(s / T - lse) - ct [target] out
 //   dH    dH^T = W^T ds^T  k over the vocab rows of the piece, fp32 sums
-//   dW    dW^T = H^T ds    k over the tokens
+//   dW    dW^T = H^T ds    k over the tokens (DwSum: in splits of them, fp32 sums)
 // s itself never leaves the registers.  With the vocabulary along the tile's P
 // rows, a lane holds 32 x FI / 2 logits of each of its tokens, so the running
 // maximum and sum of the softmax are formed inside a lane and joined across
@@ -35,9 +35,12 @@
 // Against read, wait, multiply (8192 tokens, hidden 4096, vocabulary 128256, bf16):
 // backward 21.4 ms for 21.8; 238 x 1792 x 16374 backward 92 us for 103.  The softmax
 // statistics of 256 x 256 bf16 tiles keep the plain loop (plain_loop in head_tile.h
-// has the figures).  At that first size Lse reaches 1244 TFLOP/s, Grad 1160, dH 1229
-// and dW 1238, where a library's plain products of the same operands, logits written,
-// reach 1451 (logits), 1345 (dH) and 1124 (dW).  What keeps Lse from more is its epilogue (an exponential a
+// has the figures).  At that first size Lse reaches 1148 TFLOP/s, Grad 1063, dH 1160
+// and dW 1166 on one card (1234, 1153, 1221 and 1235 on another), where a library's plain
+// products of the same operands, logits written, reach 1451 (logits), 1345 (dH) and 1124
+// (dW).  The matrix cores are busy for 56 to 60% of the cycles, LDS conflicts take at most
+// 2% of its own and memory is read and written at 1.0 to 1.2 TB/s: what is lost is lost
+// at barriers and in epilogues.  What keeps Lse from more is its epilogue (an exponential a
 // logit, with the MFMA idle: two tiles' accumulators do not fit in one wave's
 // registers) and one workgroup a CU, so that no other covers the barriers.
 #include "head_tile.h"

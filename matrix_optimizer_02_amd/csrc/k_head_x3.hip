@@ -11,9 +11,9 @@
 // (48 KB), of 32 for 64 x 64 ones, in a ring of three.
 //
 // What bounds it: the MFMA, six products of fp32's one.  820 tokens, hidden 1536,
-// vocabulary 32000: dH 549 us, dW 461 us, 881 and 1049 TFLOP/s of bf16 products
-// (147 and 175 of fp32, counting the 820 of 1024 token rows that are not padding;
-// a library's fp32 product reaches 153).  One product after the other, each with
+// vocabulary 32000: dH 507 us, dW 412 us, 954 and 1174 TFLOP/s of bf16 products
+// (159 and 196 of fp32, counting the 820 of 1024 token rows that are not padding;
+// a library's fp32 product reaches 153), the matrix cores busy for 53% of the cycles.  One product after the other, each with
 // slabs of its own, took 618 and 527 us where this took 513 and 415 (one card).
 // Fragments in two sets, as in k_head_gemm.hip, do not fit beside the 128
 // accumulators of a 256 x 256 tile.
