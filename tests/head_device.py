@@ -30,6 +30,7 @@ def inputs(t, d, v, dtype, seed, edges=(), dead=0.0):
     for most rows) are drawn apart, a quarter of them from `edges` (rows next to
     the borders of pieces and tiles): an output that lost a part of the
     vocabulary is off by whole terms.  Rows without a loss hold NaN."""
+    assert all(0 <= x < v for x in edges)
     g = torch.Generator(device=DEVICE)
     g.manual_seed(seed)
     rand = lambda *s: torch.randn(s, generator=g, device=DEVICE)
@@ -55,17 +56,23 @@ def inputs(t, d, v, dtype, seed, edges=(), dead=0.0):
 
 
 def teacher(t, k, v, seed, edges=()):
+    assert all(0 <= x < v for x in edges)
     g = torch.Generator(device=DEVICE)
     g.manual_seed(seed)
-    ids = torch.randint(0, v, (t, k), generator=g, device=DEVICE)  # (now and then an id twice)
-    if len(edges):
-        e = torch.tensor(edges, device=DEVICE)
-        pick = e[torch.randint(0, len(e), (t, k), generator=g, device=DEVICE)]
-        ids = torch.where(torch.rand((t, k), generator=g, device=DEVICE) < 0.25, pick, ids)
-    held = torch.randint(0, k + 1, (t, 1), generator=g, device=DEVICE)
-    ids = torch.where(torch.arange(k, device=DEVICE) < held, ids, -1)
-    z = torch.randn((t, k), generator=g, device=DEVICE) * 2 + 5
-    return ids, torch.where(ids >= 0, z, float("nan"))
+    e = torch.tensor(edges, device=DEVICE) if len(edges) else None
+    ids = torch.empty((t, k), dtype=torch.int64, device=DEVICE)
+    z = torch.empty((t, k), device=DEVICE)
+    for r0 in range(0, t, 65536):
+        n = min(65536, t - r0)
+        x = torch.randint(0, v, (n, k), generator=g, device=DEVICE)  # (now and then an id twice)
+        if e is not None:
+            pick = e[torch.randint(0, len(e), (n, k), generator=g, device=DEVICE)]
+            x = torch.where(torch.rand((n, k), generator=g, device=DEVICE) < 0.25, pick, x)
+        held = torch.randint(0, k + 1, (n, 1), generator=g, device=DEVICE)
+        x = torch.where(torch.arange(k, device=DEVICE) < held, x, -1)
+        ids[r0:r0 + n] = x
+        z[r0:r0 + n] = torch.where(x >= 0, torch.randn((n, k), generator=g, device=DEVICE) * 2 + 5, float("nan"))
+    return ids, z
 
 
 def guarded(shape, dtype):
@@ -118,8 +125,8 @@ def within(name, got, ref, bound):
                              f"{float(bound[i]):.3e}; {int(bad.sum())} of {bad.numel()} outside")
 
 
-def check(what, got, h, w, up, y=None, ids=None, z=None, tau=1.0, gl=None):
-    """Every element of every output against the definitions in fp64."""
+def check(what, got, h, w, up, y=None, ids=None, z=None, tau=1.0, gl=None, block=BLOCK):
+    """Every element of every output against the definitions in fp64, `block` tokens at a time."""
     t, d, v, dtype = h.shape[0], h.shape[1], w.shape[0], h.dtype
     mul = 1 if dtype == BF16 else 6
     out = U16 if dtype == BF16 else 2 * U32
@@ -129,8 +136,8 @@ def check(what, got, h, w, up, y=None, ids=None, z=None, tau=1.0, gl=None):
     Wt, aW = W.t(), W.abs()
     aWt = aW.t()
     dw, bdw, mdw = (torch.zeros_like(W) for _ in range(3))
-    for r0 in range(0, t, BLOCK):
-        rows = slice(r0, min(t, r0 + BLOCK))
+    for r0 in range(0, t, block):
+        rows = slice(r0, min(t, r0 + block))
         n = rows.stop - r0
         if ids is None:
             live = y[rows] != IGN
