@@ -31,24 +31,27 @@
  * the row: from vocab on it is passed over like an absent one (student_logits 0).
  * A NaN or +inf logit of a present entry makes the row's loss NaN.
  *
- * Arithmetic.  Sums and softmax statistics are fp32.  DMUON_BF16: bf16
- * operands; ds is rounded to bf16 once as the operand of its two products,
- * relative to the largest gradient weight (gradients are then off by 1.1 to 1.4
- * times what rounding them to bf16 alone costs), and in calls of at most 128
- * tokens, ignored ones included, held in two bf16 parts (16 bits).  DMUON_F32: operands are multiplied in
- * parts, three bf16 parts that hold all 24 bits for the gradients and for the
- * logits of few tokens (forward up to 256, backward up to 384, ignored ones
- * included), two fp16 parts of rows scaled by a power of two for the logits
- * otherwise.  A logit is then off by at most 2^-21 of the sum of its products'
- * magnitudes, and by 2^-22 T more where a row's elements differ by more than 2^17;
- * calls whose rows could make it more (the largest element of one operand times
- * the largest sum of a row's magnitudes of the other above 2^17 T) take the three
- * parts, at up to three times the time of their logits' product.  Inputs of
- * magnitude up to 3e38.  A probability is
- * exp(s / T - lse) with lse rounded to fp32, so it is good to about
- * 2^-24 (1 + |lse|) relative.  A loss is formed from the distances of logits, not
- * from lse.  Teacher logits may hold fp32's lowest value
- * (equal ones share the row's mass) and -inf (no mass).
+ * Arithmetic.  Sums and softmax statistics are fp32.  A loss is formed from the
+ * distances of logits, not from lse.  A probability is exp(s / T - lse) with lse
+ * rounded to fp32, so it is good to about 2^-24 (1 + |lse|) relative.  Entries of ds
+ * below 2^-126 of the largest gradient weight count as 0.  Teacher logits may hold
+ * fp32's lowest value (equal ones share the row's mass) and -inf (no mass).
+ *
+ * DMUON_BF16: bf16 operands.  ds is rounded to bf16 once as the operand of its two
+ * products, relative to the largest gradient weight (gradients are then off by 1.1
+ * to 1.4 times what rounding them to bf16 alone costs); in calls of at most 128
+ * tokens, ignored ones included, it is held in two bf16 parts (16 bits).
+ *
+ * DMUON_F32: operands are multiplied in parts.  Gradients, and the logits of few
+ * tokens (forward up to 256, backward up to 384, ignored ones included): three bf16
+ * parts that hold all 24 bits.  Logits otherwise: two fp16 parts of rows scaled by a
+ * power of two; a logit is off by at most 2^-21 of the sum of its products'
+ * magnitudes, and by 2^-22 T more where a row's elements differ by more than 2^17.
+ * Calls whose rows could make that more take the three parts, at up to three times
+ * the time of the logits' product: decided on the device, where the largest |h|
+ * times the largest sum of a row of |W|, plus the same the other way round, is above
+ * 2^17 T.  Inputs of magnitude up to 3e38; elements below 2^-108 lose their last
+ * bits.
  *
  * Conventions are those of dmuon_ns.h: status codes, dense row-major arrays,
  * 16-byte aligned device pointers of the current device, a 256-byte aligned
