@@ -18,33 +18,13 @@
 
 #include "dmuon_internal.h"
 #include "launch.h"
+#include "spans.h"
 
 using namespace dmuon;
 
 namespace {
 
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// A caller buffer's byte range and whether the call writes it.
-struct Span {
-    uintptr_t lo, hi;
-    bool written;
-};
-
-// True when no two of the spans overlap where one of them is written.  Read-
-// only spans may overlap each other (the same gradient passed twice is
-// harmless).  Sorted by start, a span overlaps an earlier one exactly when it
-// starts below that one's end, so one sweep suffices.
-bool disjoint_where_written(std::vector<Span>& v) {
-    std::sort(v.begin(), v.end(), [](const Span& x, const Span& y) { return x.lo < y.lo; });
-    uintptr_t end_any = 0, end_written = 0;
-    for (const Span& sp : v) {
-        if (sp.lo < end_written || (sp.written && sp.lo < end_any)) return false;
-        end_any = std::max(end_any, sp.hi);
-        if (sp.written) end_written = std::max(end_written, sp.hi);
-    }
-    return true;
-}
 
 size_t dtype_bytes(int32_t dt) { return dt == DMUON_BF16 ? 2 : 4; }
 
