@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdmuon_ns.so")
 
 HIP_SOURCES = ["api.hip", "clip.hip", "head.hip", "k_adamw.hip", "k_diag.hip", "k_elementwise.hip", "k_gemm_bf16.hip",
-               "k_gemm_f32.hip", "k_head_gemm.hip", "k_head_rows.hip", "k_head_stream.hip",
+               "k_gemm_f32.hip", "k_head_gemm.hip", "k_head_probs.hip", "k_head_rows.hip", "k_head_stream.hip",
                "k_head_x3.hip", "k_resident.hip", "tune.hip"]
 CXX_SOURCES = ["head_layout.cpp", "plan.cpp"]
 ARCH = "gfx950"
@@ -49,7 +49,7 @@ def _run(cmd, verbose):
     return res
 
 
-HEADERS = ["dmuon_ns.h", "dmuon_head.h", "dmuon_clip.h"]
+HEADERS = ["dmuon_ns.h", "dmuon_head.h", "dmuon_logprobs.h", "dmuon_clip.h"]
 
 
 def exported_symbols(header: str = "dmuon_ns.h"):

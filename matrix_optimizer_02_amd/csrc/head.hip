@@ -2,6 +2,7 @@
 // (head_layout.cpp: tiles, splits and the workspace)
 //   forward   (teacher) rows -> pack H -> [pack W piece ->] tile statistics -> join
 //             (-> student logits and loss)
+//             (log probabilities: a chunk of the tokens at a time, -> logits -> outputs)
 //   backward  (teacher) rows -> pack H, coefficients -> per piece of the
 //             vocabulary: [pack W piece,] ds, (teacher's ids,) dH sums, dW -> dH
 // fp32 with W packed: behind statistics and ds the same from three bf16 parts, by a
@@ -15,6 +16,7 @@
 #include <new>
 #include <vector>
 
+#include "../../include/dmuon_logprobs.h"
 #include "head_internal.h"
 
 using namespace dmuon;
@@ -46,11 +48,14 @@ struct Buffers {
     }
 };
 
+enum Kind { kCrossEntropy, kDistill, kLogProbs };
+
 struct Call {
+    Kind kind;
     const dmuon_head_desc* desc;
     const void* hidden;
     const void* weight;
-    const int64_t* targets;  // cross entropy
+    const int64_t* targets;  // cross entropy; log probabilities, or null
     int64_t ignore_index;
     const int64_t* ids;      // distillation
     const float* teacher;
@@ -60,11 +65,16 @@ struct Call {
     hipStream_t stream;
 };
 
-dmuon_status check_call(const Call& c, bool distill, Buffers& b) {
-    const dmuon_status st = head_check_desc(c.desc);
+dmuon_status check_call(const Call& c, bool backward, Buffers& b) {
+    const bool distill = c.kind == kDistill;
+    const dmuon_status st = c.kind == kLogProbs ? probs_check_desc(c.desc, backward) : head_check_desc(c.desc);
     if (st != DMUON_OK) return st;
     const dmuon_head_desc& d = *c.desc;
-    if (distill ? d.top_k < 1 : d.top_k != 0) return DMUON_ERR_INVALID_ARG;
+    if (c.kind == kLogProbs) {
+        if (!(c.temp > 0.f && std::isnormal(c.temp) && std::isnormal(1.f / c.temp))) return DMUON_ERR_INVALID_ARG;
+    } else if (distill ? d.top_k < 1 : d.top_k != 0) {
+        return DMUON_ERR_INVALID_ARG;
+    }
     // the losses are multiplied by T^2, the logits by 1 / T
     if (distill && !(c.temp > 0.f && std::isnormal(c.temp * c.temp))) return DMUON_ERR_INVALID_ARG;
     const int64_t e = d.dtype == DMUON_BF16 ? 2 : 4;
@@ -73,18 +83,18 @@ dmuon_status check_call(const Call& c, bool distill, Buffers& b) {
     if (distill) {
         b.add(c.ids, 8 * d.tokens * d.top_k, false);
         b.add(c.teacher, 4 * d.tokens * d.top_k, false);
-    } else {
+    } else if (c.targets != nullptr || c.kind == kCrossEntropy) {
         b.add(c.targets, 8 * d.tokens, false);
     }
     return DMUON_OK;
 }
 
-dmuon_status check_rest(const Call& c, const HeadLayout& L, Buffers& b) {
+dmuon_status check_rest(const Call& c, size_t bytes, Buffers& b) {
     if (!b.good()) return DMUON_ERR_INVALID_ARG;
     if (c.workspace == nullptr || (reinterpret_cast<uintptr_t>(c.workspace) & (kAlign - 1)) != 0 ||
-        c.workspace_bytes < L.bytes)
+        c.workspace_bytes < bytes)
         return DMUON_ERR_WORKSPACE;
-    b.add(c.workspace, (int64_t)L.bytes, true);
+    b.add(c.workspace, (int64_t)bytes, true);
     return b.good() ? DMUON_OK : DMUON_ERR_INVALID_ARG;
 }
 
@@ -145,7 +155,7 @@ dmuon_status gather_rows(const Call& c, const Views& v, float* losses, float* ls
     HeadPrepareArgs a{};
     a.esize = L.esize;
     a.rows.targets = c.ids != nullptr ? nullptr : c.targets;
-    a.rows.flag = v.flag();
+    a.rows.flag = c.ids != nullptr ? v.flag() : nullptr;
     a.rows.ignore_index = c.ignore_index;
     a.rows.vocab = L.vocab;
     a.rows.tokens = (int32_t)L.tokens;
@@ -222,7 +232,7 @@ void logits_args(const Call& c, const Views& v, int64_t v0, int64_t rows, HeadGe
     a.v0 = v0;
     a.vocab = L.vocab;
     a.inv_temp = 1.f / c.temp;
-    a.target = c.ids != nullptr ? nullptr : v.target();
+    a.target = c.targets != nullptr ? v.target() : nullptr;
     a.t_pad = L.t_pad;
     a.first_tile = (int32_t)(v0 / L.s_tile.tp);
 }
@@ -249,9 +259,10 @@ hipError_t launch_logits(int mode, const Call& c, const Views& v, int64_t v0, in
     return launch_head_stream(mode, L.s_tile, b, a.tiles_i * ceil_div(token_rows, std::min(128, L.s_tile.tq)), c.stream);
 }
 
-dmuon_status forward(const Call& c, bool distill, float* losses, float* lse, float* student) {
+dmuon_status forward(const Call& c, float* losses, float* lse, float* student) {
+    const bool distill = c.kind == kDistill;
     Buffers b;
-    dmuon_status st = check_call(c, distill, b);
+    dmuon_status st = check_call(c, false, b);
     if (st != DMUON_OK) return st;
     const dmuon_head_desc& d = *c.desc;
     b.add(losses, 4 * d.tokens, true);
@@ -259,7 +270,7 @@ dmuon_status forward(const Call& c, bool distill, float* losses, float* lse, flo
     if (distill) b.add(student, 4 * d.tokens * d.top_k, true);
     const HeadLayout L = head_layout_of(d, false);
     if (d.tokens == 0) return b.good() ? DMUON_OK : DMUON_ERR_INVALID_ARG;
-    st = check_rest(c, L, b);
+    st = check_rest(c, L.bytes, b);
     if (st != DMUON_OK) return st;
 
     const Views v{static_cast<char*>(c.workspace), L};
@@ -313,36 +324,139 @@ dmuon_status forward(const Call& c, bool distill, float* losses, float* lse, flo
     return DMUON_OK;
 }
 
-dmuon_status backward(const Call& c, bool distill, const float* lse, const float* student, const float* grad_losses,
-                      const float* grad_lse, void* grad_hidden, void* grad_weight) {
+// What a chunk of the log probabilities writes.
+struct Probs {
+    float *logprobs, *entropy, *lse;
+    int64_t* top_ids;
+    float* top_logprobs;
+};
+
+dmuon_status probs_chunk_forward(const Call& c, const Probs& o) {
+    const ProbsLayout P = probs_layout_of(*c.desc, false);
+    const HeadLayout& L = P.head;
+    const Views v{static_cast<char*>(c.workspace), L};
+    dmuon_status st = gather_rows(c, v, nullptr, nullptr, nullptr, nullptr);
+    if (st != DMUON_OK) return st;
+    const int64_t step = L.pack_weight ? L.piece : round_up(L.vocab, kHeadTile);
+    for (int64_t v0 = 0; v0 < L.vocab; v0 += step) {
+        HeadGemmArgs a{};
+        st = weight_piece(c, v, false, v0, step, a);
+        if (st != DMUON_OK) return st;
+        logits_args(c, v, v0, step, a);
+        a.part = v.at<float2>(L.off_part);
+        a.target_logit = v.target_logit();
+        a.logits = v.at<float>(P.off_logits);
+        a.logits_ld = (int32_t)round_up(L.vocab, kHeadTile);
+        HEAD_TRY(launch_logits(kHeadLse, c, v, v0, step, a, L.tokens));
+    }
+    HeadProbsArgs r{};
+    r.count = v.count();
+    r.src = v.src();
+    r.target = c.targets != nullptr ? v.target() : nullptr;
+    r.tokens = L.tokens;
+    r.vocab = L.vocab;
+    r.inv_temp = 1.f / c.temp;
+    r.k = c.desc->top_k;
+    r.logits = v.at<float>(P.off_logits);
+    r.logits_ld = round_up(L.vocab, kHeadTile);
+    r.logprobs = o.logprobs;
+    r.entropy = o.entropy;
+    r.lse = o.lse;
+    r.top_ids = o.top_ids;
+    r.top_logprobs = o.top_logprobs;
+    HEAD_TRY(launch_head_probs(r, c.stream));
+    return DMUON_OK;
+}
+
+dmuon_status probs_forward(const Call& c, const Probs& o) {
     Buffers b;
-    dmuon_status st = check_call(c, distill, b);
+    dmuon_status st = check_call(c, false, b);
+    if (st != DMUON_OK) return st;
+    const dmuon_head_desc& d = *c.desc;
+    if (d.tokens > 0 && (c.targets == nullptr) != (o.logprobs == nullptr)) return DMUON_ERR_INVALID_ARG;
+    if (o.logprobs != nullptr) b.add(o.logprobs, 4 * d.tokens, true);
+    if (o.entropy != nullptr) b.add(o.entropy, 4 * d.tokens, true);
+    b.add(o.lse, 4 * d.tokens, true);
+    b.add(o.top_ids, 8 * d.tokens * d.top_k, true);
+    b.add(o.top_logprobs, 4 * d.tokens * d.top_k, true);
+    if (d.top_k == 0 && (o.top_ids != nullptr || o.top_logprobs != nullptr)) return DMUON_ERR_INVALID_ARG;
+    if (d.tokens == 0) return b.good() ? DMUON_OK : DMUON_ERR_INVALID_ARG;
+    const int64_t chunk = std::min(probs_chunk(d), d.tokens);
+    dmuon_head_desc part = d, last = d;
+    part.tokens = chunk;
+    last.tokens = d.tokens - (d.tokens - 1) / chunk * chunk;
+    st = check_rest(c, std::max(probs_layout_of(part, false).bytes, probs_layout_of(last, false).bytes), b);
+    if (st != DMUON_OK) return st;
+    const int64_t e = d.dtype == DMUON_BF16 ? 2 : 4;
+    for (int64_t t = 0; t < d.tokens; t += chunk) {
+        part.tokens = std::min(chunk, d.tokens - t);
+        Call k = c;
+        k.desc = &part;
+        k.hidden = static_cast<const char*>(c.hidden) + t * d.hidden * e;
+        if (c.targets != nullptr) k.targets = c.targets + t;
+        Probs p{};
+        if (o.logprobs != nullptr) p.logprobs = o.logprobs + t;
+        if (o.entropy != nullptr) p.entropy = o.entropy + t;
+        p.lse = o.lse + t;
+        if (d.top_k > 0) {
+            p.top_ids = o.top_ids + t * d.top_k;
+            p.top_logprobs = o.top_logprobs + t * d.top_k;
+        }
+        st = probs_chunk_forward(k, p);
+        if (st != DMUON_OK) return st;
+    }
+    return DMUON_OK;
+}
+
+// What a backward call is given beside its Call.
+struct Upstream {
+    const float *lse, *student;
+    const float *grad_losses, *grad_lse;
+    const float *entropy, *grad_entropy;
+};
+
+dmuon_status backward(const Call& c, const Upstream& u, void* grad_hidden, void* grad_weight) {
+    const bool distill = c.kind == kDistill, probs = c.kind == kLogProbs;
+    Buffers b;
+    dmuon_status st = check_call(c, true, b);
     if (st != DMUON_OK) return st;
     const dmuon_head_desc& d = *c.desc;
     const int64_t e = d.dtype == DMUON_BF16 ? 2 : 4;
     if (grad_hidden == nullptr && grad_weight == nullptr && (d.tokens > 0)) return DMUON_ERR_INVALID_ARG;
-    b.add(lse, 4 * d.tokens, false);
-    b.add(grad_losses, 4 * d.tokens, false);
-    if (grad_lse != nullptr) b.add(grad_lse, 4 * d.tokens, false);
-    if (distill) b.add(student, 4 * d.tokens * d.top_k, false);
+    if (probs && d.tokens > 0) {
+        if (u.grad_losses == nullptr && u.grad_entropy == nullptr) return DMUON_ERR_INVALID_ARG;
+        if (u.grad_losses != nullptr && c.targets == nullptr) return DMUON_ERR_INVALID_ARG;
+        if (u.grad_entropy != nullptr) b.add(u.entropy, 4 * d.tokens, false);
+    }
+    b.add(u.lse, 4 * d.tokens, false);
+    if (!probs || u.grad_losses != nullptr) b.add(u.grad_losses, 4 * d.tokens, false);
+    if (u.grad_lse != nullptr) b.add(u.grad_lse, 4 * d.tokens, false);
+    if (u.grad_entropy != nullptr) b.add(u.grad_entropy, 4 * d.tokens, false);
+    if (distill) b.add(u.student, 4 * d.tokens * d.top_k, false);
     if (grad_hidden != nullptr) b.add(grad_hidden, d.tokens * d.hidden * e, true);
     if (grad_weight != nullptr) b.add(grad_weight, d.vocab * d.hidden * e, true);
-    const HeadLayout L = head_layout_of(d, true);
+    const ProbsLayout P = probs ? probs_layout_of(d, true) : ProbsLayout{head_layout_of(d, true), 0, 0, 0};
+    const HeadLayout& L = P.head;
     if (d.tokens == 0) {
         if (!b.good()) return DMUON_ERR_INVALID_ARG;
         if (grad_weight != nullptr) HEAD_TRY(launch_head_zero(grad_weight, d.vocab * d.hidden * e, c.stream));
         return DMUON_OK;
     }
-    st = check_rest(c, L, b);
+    st = check_rest(c, probs ? P.bytes : L.bytes, b);
     if (st != DMUON_OK) return st;
 
     const Views v{static_cast<char*>(c.workspace), L};
+    const bool entropy = u.grad_entropy != nullptr;
     HeadCoefArgs k{};
     k.q = distill ? v.q() : nullptr;
-    k.lse = lse;
-    k.grad_losses = grad_losses;
-    k.grad_lse = grad_lse;
-    k.temp = c.temp;
+    k.lse = u.lse;
+    k.grad_losses = u.grad_losses;
+    k.grad_lse = u.grad_lse;
+    k.entropy = u.entropy;
+    k.grad_entropy = u.grad_entropy;
+    // the losses: g p - g at the target; log probabilities the other way round, over T
+    k.temp = probs ? -1.f / c.temp : c.temp;
+    k.ce = v.at<float>(P.off_ce);
     k.lse_c = v.lse();
     k.cp = v.cp();
     k.ct = v.ct();
@@ -362,19 +476,20 @@ dmuon_status backward(const Call& c, bool distill, const float* lse, const float
         a.lse = v.lse();
         a.cp = v.cp();
         a.ct = v.ct();
+        a.ce = v.at<float>(P.off_ce);
         a.norm = v.norm();
         a.low = L.low;
         a.g = v.ws + L.off_g;
         a.g_plane = 2 * L.t_pad * L.piece;
         a.g_ld = (int32_t)L.piece;
-        HEAD_TRY(launch_logits(kHeadGrad, c, v, v0, L.piece, a, round_up(L.tokens, kHeadSlab)));
+        HEAD_TRY(launch_logits(entropy ? kHeadGradEntropy : kHeadGrad, c, v, v0, L.piece, a, round_up(L.tokens, kHeadSlab)));
         if (distill) {
             HeadFixArgs f{};
             f.count = v.count();
             f.src = v.src();
             f.t = teacher_of(c);
             f.q = v.q();
-            f.student = student;
+            f.student = u.student;
             f.lse_c = v.lse();
             f.cp = v.cp();
             f.norm = v.norm();
@@ -482,9 +597,9 @@ extern "C" dmuon_status head_cross_entropy_forward(const dmuon_head_desc* desc, 
                                                    const int64_t* targets, int64_t ignore_index, float* losses,
                                                    float* lse, void* workspace, size_t workspace_bytes, void* stream) {
     try {
-        const Call c{desc, hidden, weight, targets, ignore_index, nullptr, nullptr, 1.f, workspace, workspace_bytes,
-                     static_cast<hipStream_t>(stream)};
-        return forward(c, false, losses, lse, nullptr);
+        const Call c{kCrossEntropy, desc, hidden, weight, targets, ignore_index, nullptr, nullptr, 1.f, workspace,
+                     workspace_bytes, static_cast<hipStream_t>(stream)};
+        return forward(c, losses, lse, nullptr);
     } catch (...) {
         return DMUON_ERR_ALLOC;
     }
@@ -496,9 +611,9 @@ extern "C" dmuon_status head_cross_entropy_backward(const dmuon_head_desc* desc,
                                                     void* grad_hidden, void* grad_weight, void* workspace,
                                                     size_t workspace_bytes, void* stream) {
     try {
-        const Call c{desc, hidden, weight, targets, ignore_index, nullptr, nullptr, 1.f, workspace, workspace_bytes,
-                     static_cast<hipStream_t>(stream)};
-        return backward(c, false, lse, nullptr, grad_losses, grad_lse, grad_hidden, grad_weight);
+        const Call c{kCrossEntropy, desc, hidden, weight, targets, ignore_index, nullptr, nullptr, 1.f, workspace,
+                     workspace_bytes, static_cast<hipStream_t>(stream)};
+        return backward(c, Upstream{lse, nullptr, grad_losses, grad_lse, nullptr, nullptr}, grad_hidden, grad_weight);
     } catch (...) {
         return DMUON_ERR_ALLOC;
     }
@@ -509,9 +624,9 @@ extern "C" dmuon_status head_distill_forward(const dmuon_head_desc* desc, const 
                                              float temperature, float* losses, float* lse, float* student_logits,
                                              void* workspace, size_t workspace_bytes, void* stream) {
     try {
-        const Call c{desc, hidden, weight, nullptr, 0, teacher_ids, teacher_logits, temperature, workspace,
+        const Call c{kDistill, desc, hidden, weight, nullptr, 0, teacher_ids, teacher_logits, temperature, workspace,
                      workspace_bytes, static_cast<hipStream_t>(stream)};
-        return forward(c, true, losses, lse, student_logits);
+        return forward(c, losses, lse, student_logits);
     } catch (...) {
         return DMUON_ERR_ALLOC;
     }
@@ -523,9 +638,56 @@ extern "C" dmuon_status head_distill_backward(const dmuon_head_desc* desc, const
                                               const float* grad_losses, void* grad_hidden, void* grad_weight,
                                               void* workspace, size_t workspace_bytes, void* stream) {
     try {
-        const Call c{desc, hidden, weight, nullptr, 0, teacher_ids, teacher_logits, temperature, workspace,
+        const Call c{kDistill, desc, hidden, weight, nullptr, 0, teacher_ids, teacher_logits, temperature, workspace,
                      workspace_bytes, static_cast<hipStream_t>(stream)};
-        return backward(c, true, lse, student_logits, grad_losses, nullptr, grad_hidden, grad_weight);
+        return backward(c, Upstream{lse, student_logits, grad_losses, nullptr, nullptr, nullptr}, grad_hidden,
+                        grad_weight);
+    } catch (...) {
+        return DMUON_ERR_ALLOC;
+    }
+}
+
+extern "C" dmuon_status head_log_probs_workspace_bytes(const dmuon_head_desc* desc, int32_t backward, size_t* bytes) {
+    if (bytes == nullptr) return DMUON_ERR_INVALID_ARG;
+    const dmuon_status st = probs_check_desc(desc, backward != 0);
+    if (st != DMUON_OK) return st;
+    // the largest over all calls of at most these tokens, as for the losses
+    dmuon_head_desc d = *desc;
+    const int64_t tokens = backward ? desc->tokens : std::min(desc->tokens, probs_chunk(d));
+    size_t most = 0;
+    for (int64_t t = std::min<int64_t>(64, tokens);; t = std::min(round_up(t + 1, 64), tokens)) {
+        d.tokens = t;
+        most = std::max(most, probs_layout_of(d, backward != 0).bytes);
+        if (t == tokens) break;
+    }
+    *bytes = most;
+    return DMUON_OK;
+}
+
+extern "C" dmuon_status head_log_probs_forward(const dmuon_head_desc* desc, const void* hidden, const void* weight,
+                                               const int64_t* targets, int64_t ignore_index, float temperature,
+                                               float* logprobs, float* entropy, float* lse, int64_t* top_ids,
+                                               float* top_logprobs, void* workspace, size_t workspace_bytes,
+                                               void* stream) {
+    try {
+        const Call c{kLogProbs, desc, hidden, weight, targets, ignore_index, nullptr, nullptr, temperature, workspace,
+                     workspace_bytes, static_cast<hipStream_t>(stream)};
+        return probs_forward(c, Probs{logprobs, entropy, lse, top_ids, top_logprobs});
+    } catch (...) {
+        return DMUON_ERR_ALLOC;
+    }
+}
+
+extern "C" dmuon_status head_log_probs_backward(const dmuon_head_desc* desc, const void* hidden, const void* weight,
+                                                const int64_t* targets, int64_t ignore_index, float temperature,
+                                                const float* lse, const float* entropy, const float* grad_logprobs,
+                                                const float* grad_entropy, void* grad_hidden, void* grad_weight,
+                                                void* workspace, size_t workspace_bytes, void* stream) {
+    try {
+        const Call c{kLogProbs, desc, hidden, weight, targets, ignore_index, nullptr, nullptr, temperature, workspace,
+                     workspace_bytes, static_cast<hipStream_t>(stream)};
+        return backward(c, Upstream{lse, nullptr, grad_logprobs, nullptr, entropy, grad_entropy}, grad_hidden,
+                        grad_weight);
     } catch (...) {
         return DMUON_ERR_ALLOC;
     }

@@ -23,7 +23,8 @@ enum HeadMode : int32_t {
     kHeadGrad = 1,  // P = W rows, Q = H rows: ds as bf16 parts
     kHeadDh = 2,    // P = W (k = vocab rows, columns of hidden), Q = ds rows: fp32 sums, added per piece
     kHeadDw = 3,    // P = H (k = tokens, columns of hidden), Q = ds (k = tokens, columns of vocab): dW rows
-    kHeadDwSum = 4  // the same in splits of the tokens: fp32 sums
+    kHeadDwSum = 4,  // the same in splits of the tokens: fp32 sums
+    kHeadGradEntropy = 5  // as Grad, with the entropy's gradient
 };
 
 struct HeadGemmArgs {
@@ -57,6 +58,7 @@ struct HeadGemmArgs {
     const float* lse;            // per compact row
     const float* cp;             // coefficient of p
     const float* ct;             // coefficient at the target
+    const float* ce;             // coefficient of p log p (GradEntropy)
     const float* norm;           // the largest coefficient: ds is held as multiples of it
     int32_t low;                 // Grad: the rows' low parts go to head_low_row(n) rows further
     char* g;                     // ds out
@@ -94,7 +96,7 @@ hipError_t launch_head_teacher(const HeadTeacher& t, int64_t tokens, float2* q, 
 // padding, -2 where out of range); zeros losses and lse (null: not) of the others.
 struct HeadRowsArgs {
     const int64_t* targets;  // null: flag decides
-    const int32_t* flag;
+    const int32_t* flag;     // null: every row
     int64_t ignore_index, vocab;
     int32_t tokens, t_pad;
     int32_t* count;          // the rows, then the rows of ds
@@ -154,15 +156,36 @@ struct HeadMergeArgs {
     float* lse;
 };
 hipError_t launch_head_merge(const HeadMergeArgs& a, hipStream_t stream);
-// Backward coefficients per compact row (zero in the padding).
+// Log probabilities, entropies and alternatives of the rows.
+struct HeadProbsArgs {
+    const int32_t* count;
+    const int32_t* src;
+    const int32_t* target;  // per compact row, or null
+    int64_t tokens, vocab;
+    float inv_temp;
+    int32_t k;
+    const float* logits;    // of the compact rows
+    int64_t logits_ld;
+    float* logprobs;        // or null
+    float* entropy;         // or null
+    float* lse;
+    int64_t* top_ids;
+    float* top_logprobs;
+};
+hipError_t launch_head_probs(const HeadProbsArgs& a, hipStream_t stream);
+// Backward coefficients per compact row (zero in the padding): ds = exp(x - lse)
+// (cp + ce (x - lse)) - ct at the target.
 struct HeadCoefArgs {
     const float2* q;        // distillation, else null
     const float* lse;
-    const float* grad_losses;
-    const float* grad_lse;  // or null
-    float temp;
+    const float* grad_losses;   // or null
+    const float* grad_lse;      // or null
+    const float* entropy;
+    const float* grad_entropy;  // or null
+    float temp;             // what the upstream gradients are multiplied by
     float *lse_c, *cp, *ct;
-    float* norm;            // the largest |cp|, |ct|, within 2^100 either way
+    float* ce;              // with grad_entropy
+    float* norm;            // the largest |cp|, |ct|, |ce|, within 2^100 either way
     int64_t t_pad;
 };
 // The rows that carry a loss (rows.tokens 0: found before), then up to three

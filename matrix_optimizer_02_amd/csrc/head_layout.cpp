@@ -14,6 +14,8 @@ namespace {
 // cache next to what those stream.
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
 constexpr int64_t kLowTokens = 128;
+// Bytes of logits that a forward call of the log probabilities holds.
+constexpr int64_t kProbsBytes = int64_t(1) << 30;
 constexpr int64_t kPieceMin = 8192;  // vocab rows: fewer would leave dW's launch short of tiles
 
 // Tiles with the time a workgroup takes for 64 of K, in microseconds, when it has
@@ -185,6 +187,35 @@ HeadLayout head_layout_of(dmuon_head_desc d, bool backward) {
         if (L.keep_logits) L.off_logits = take(kept);
         L.off_part = take(8 * (v_pad / L.s_tile.tp) * head_wave_rows(L.s_tile.tp, L.s_tile.tq) * L.t_pad);
     }
+    L.bytes = at;
+    return L;
+}
+
+dmuon_status probs_check_desc(const dmuon_head_desc* d, bool backward) {
+    const dmuon_status st = head_check_desc(d);
+    if (st != DMUON_OK) return st;
+    if (backward ? d->top_k != 0 : d->top_k > d->vocab) return DMUON_ERR_INVALID_ARG;
+    return d->top_k > kHeadMaxAlternatives ? DMUON_ERR_UNSUPPORTED : DMUON_OK;
+}
+
+int64_t probs_chunk(const dmuon_head_desc& d) {
+    const int64_t row = 4 * round_up(d.vocab, kHeadTile);
+    return std::max<int64_t>(kProbsBytes / row / kHeadTile, 1) * kHeadTile;
+}
+
+ProbsLayout probs_layout_of(const dmuon_head_desc& d, bool backward) {
+    ProbsLayout L{};
+    dmuon_head_desc h = d;
+    h.top_k = 0;
+    L.head = head_layout_of(h, backward);
+    size_t at = L.head.bytes;
+    auto take = [&](int64_t bytes) {
+        const size_t o = at;
+        at += align_up((size_t)bytes);
+        return o;
+    };
+    if (backward) L.off_ce = take(4 * L.head.t_pad);
+    else L.off_logits = take(4 * L.head.t_pad * round_up(d.vocab, kHeadTile));
     L.bytes = at;
     return L;
 }

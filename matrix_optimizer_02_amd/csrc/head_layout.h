@@ -15,6 +15,7 @@ constexpr int64_t kHeadMaxTokens = (int64_t(1) << 24) - 1;
 constexpr int64_t kHeadMaxHidden = 65536;
 constexpr int64_t kHeadMaxVocab = (int64_t(1) << 27) - 1;
 constexpr int32_t kHeadMaxTopK = 1024;
+constexpr int32_t kHeadMaxAlternatives = 128;
 constexpr int64_t kHeadMaxLogits = int64_t(1) << 42;  // tokens x vocab: keeps every launch's tile count in 31 bits
 
 constexpr int kHeadTile = 256;  // every tile edge divides it: arrays are padded to it
@@ -79,5 +80,20 @@ inline int64_t ceil_div(int64_t x, int64_t a) { return (x + a - 1) / a; }
 dmuon_status head_check_desc(const dmuon_head_desc* d);
 // The cut of one call (a descriptor that head_check_desc accepts).
 HeadLayout head_layout_of(dmuon_head_desc d, bool backward);
+
+// The log probabilities: arrays beside those of a head loss.  The forward call takes a
+// chunk of the tokens at a time.
+struct ProbsLayout {
+    HeadLayout head;
+    size_t off_logits;  // forward
+    size_t off_ce;      // backward
+    size_t bytes;
+};
+// INVALID_ARG or UNSUPPORTED for sizes out of range.
+dmuon_status probs_check_desc(const dmuon_head_desc* d, bool backward);
+// Tokens of a forward call's chunk, and the cut of one of d.tokens <= that (or of a
+// whole backward call).
+int64_t probs_chunk(const dmuon_head_desc& d);
+ProbsLayout probs_layout_of(const dmuon_head_desc& d, bool backward);
 
 }  // namespace dmuon

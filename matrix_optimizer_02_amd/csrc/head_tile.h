@@ -100,6 +100,7 @@ __device__ __forceinline__ void weave() {
 }
 
 constexpr bool is_dw(int mode) { return mode == kHeadDw || mode == kHeadDwSum; }
+constexpr bool is_grad(int mode) { return mode == kHeadGrad || mode == kHeadGradEntropy; }
 
 // The tiles of a launch and this workgroup's share of them: XCD x takes one
 // contiguous run of the tiles (neighbours share operand rows in its L2), its
@@ -110,7 +111,7 @@ struct Share {
 template <int TQ, int MODE>
 __device__ __forceinline__ Share share_of(const HeadGemmArgs& args, int n, int n_k) {
     Share s;
-    s.tiles_j = is_dw(MODE) ? args.tiles_j : ((MODE == kHeadGrad ? n_k : n) + TQ - 1) / TQ;
+    s.tiles_j = is_dw(MODE) ? args.tiles_j : ((is_grad(MODE) ? n_k : n) + TQ - 1) / TQ;
     s.per_split = args.tiles_i * s.tiles_j;
     const int total = s.per_split * (MODE == kHeadDh || MODE == kHeadDwSum ? args.splits : 1);
     const int x = (int)(blockIdx.x % kXcds);
@@ -285,9 +286,10 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
                     *p = o;
                 }
     } else {
-        if constexpr (MODE == kHeadGrad) {
+        if constexpr (is_grad(MODE)) {
             const float inv_norm = 1.f / norm_of(args.norm);
             float row_lse[C::FJ], row_cp[C::FJ], row_ct[C::FJ];
+            [[maybe_unused]] float row_ce[C::FJ];
             int row_target[C::FJ];
             #pragma unroll
             for (int j = 0; j < C::FJ; ++j) {
@@ -298,6 +300,10 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
                 row_target[j] = -1;
                 if (args.target != nullptr) row_target[j] = args.target[row];
                 asm volatile("" : "+v"(row_lse[j]), "+v"(row_cp[j]), "+v"(row_ct[j]), "+v"(row_target[j]));
+                if constexpr (MODE == kHeadGradEntropy) {
+                    row_ce[j] = args.ce[row] * inv_norm;
+                    asm volatile("" : "+v"(row_ce[j]));
+                }
             }
             __syncthreads();
             prefetch();
@@ -314,7 +320,11 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
                     #pragma unroll
                     for (int v = 0; v < 16; ++v) {
                         const int r = 32 * i + 8 * (v / 4) + v % 4;  // less 4 khalf
-                        float g = cp * __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], args.inv_temp, -lse) * kLog2e);
+                        const float x = fmaf(acc[i][j][v], args.inv_temp, -lse);
+                        float g = __builtin_amdgcn_exp2f(x * kLog2e);
+                        // (p is 0 long before x is -200, and 0 times the logarithm has to be 0)
+                        if constexpr (MODE == kHeadGradEntropy) g *= fmaf(row_ce[j], fmaxf(x, -200.f), cp);
+                        else g *= cp;
                         if (r == at - 4 * khalf) g -= ct;
                         acc[i][j][v] = r < limit - 4 * khalf ? g : 0.f;
                     }
@@ -360,7 +370,7 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
         } else {
             // bf16 rows: staged through LDS as E[c][r], stored in whole 16-byte chunks
             // (256 token rows: never in two parts)
-            constexpr bool kSplit = MODE == kHeadGrad && (PARTS > 1 || TQ <= 128);
+            constexpr bool kSplit = is_grad(MODE) && (PARTS > 1 || TQ <= 128);
             const int kOut = !kSplit ? 1 : PARTS > 1 ? PARTS : args.low + 1;
             constexpr int kEBytes = 2 * TP, kEChunks = TP / 8, kRows = TQ / PIECES;
             const int low_row = kSplit && PARTS == 1 && args.low ? head_low_row(*args.count) : 0;
@@ -395,7 +405,7 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
                     const int cp = q / kEChunks, ch = q % kEChunks, c = first + cp;
                     const uint4 v = *reinterpret_cast<const uint4*>(smem + cp * kEBytes +
                                                                     ((ch ^ (cp & (kEChunks - 1))) << 4));
-                    if (MODE == kHeadGrad) {
+                    if (is_grad(MODE)) {
                         // the low parts' rows begin where this tile's padding may reach
                         if (low_row != 0 && t.J * TQ + c >= low_row) continue;
                         const int64_t row = t.J * TQ + c + part * low_row;

@@ -180,7 +180,7 @@ __global__ __launch_bounds__(C::NT) __attribute__((
     // Stores that every wave issues behind that slab's loads, at least: they need not
     // have completed for the slab to be there.
     constexpr int kStores = MODE == kHeadLse ? C::FJ
-                            : MODE == kHeadGrad && TQ == 256 ? TQ * TP / 8 / C::NT
+                            : is_grad(MODE) && TQ == 256 ? TQ * TP / 8 / C::NT
                             : MODE == kHeadDh ? C::FI * C::FJ * 4 : 0;
     bool behind = false;
     Plan pl;
@@ -430,6 +430,9 @@ hipError_t launch_config(int mode, const HeadGemmArgs& a, int64_t max_tiles, hip
         case kHeadGrad:
             return f32 ? launch<C, kHeadGrad, kHeadHalf2>(a, max_tiles, stream)
                        : launch<C, kHeadGrad, kHeadBf16>(a, max_tiles, stream);
+        case kHeadGradEntropy:
+            return f32 ? launch<C, kHeadGradEntropy, kHeadHalf2>(a, max_tiles, stream)
+                       : launch<C, kHeadGradEntropy, kHeadBf16>(a, max_tiles, stream);
         case kHeadDh:
             return launch<C, kHeadDh, kHeadBf16>(a, max_tiles, stream);
         case kHeadDw:
@@ -445,7 +448,7 @@ hipError_t launch_config(int mode, const HeadGemmArgs& a, int64_t max_tiles, hip
 hipError_t launch_head_gemm(int mode, HeadTile tile, const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream) {
     if (max_tiles <= 0) return hipSuccess;
     if (max_tiles > (int64_t)0x3fffffff) return hipErrorInvalidValue;
-    if (a.parts > 1 && mode != kHeadLse && mode != kHeadGrad) return launch_head_x3(mode, tile, a, max_tiles, stream);
+    if (a.parts > 1 && (mode == kHeadDh || mode == kHeadDw || mode == kHeadDwSum)) return launch_head_x3(mode, tile, a, max_tiles, stream);
     if (tile.tp == 64) return launch_config<Config<64, 64, 4>>(mode, a, max_tiles, stream);
     if (tile.tq == 64) return launch_config<Config<256, 64, 2>>(mode, a, max_tiles, stream);
     if (tile.tq == 128) return launch_config<Config<256, 128, 3>>(mode, a, max_tiles, stream);

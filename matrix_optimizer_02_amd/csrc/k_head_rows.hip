@@ -81,7 +81,7 @@ __device__ __forceinline__ int scan_rows(const HeadRowsArgs& a, bool writer, int
         const int t = t0 + threadIdx.x;
         const bool in = t < a.tokens;
         const int64_t target = in && a.targets != nullptr ? a.targets[t] : 0;
-        const bool live = in && (a.targets != nullptr ? target != a.ignore_index : a.flag[t] != 0);
+        const bool live = in && (a.targets != nullptr ? target != a.ignore_index : a.flag == nullptr || a.flag[t] != 0);
         const uint64_t b = __builtin_amdgcn_ballot_w64(live);
         if (lane == 0) wave_n[wave] = __popcll(b);
         __syncthreads();
@@ -379,12 +379,19 @@ __global__ __launch_bounds__(kRowThreads) void head_student_kernel(HeadStudentAr
 // The coefficients of compact row c < n, of token t; the larger one's magnitude, for
 // the largest of all, by which ds is divided.
 __device__ __forceinline__ float coefficients(const HeadCoefArgs& a, int64_t c, int t, bool bad) {
-    const float ct = a.temp * a.grad_losses[t];
-    const float cp = a.grad_lse != nullptr ? ct + a.grad_lse[t] : ct;
+    const float ct = a.grad_losses != nullptr ? a.temp * a.grad_losses[t] : 0.f;
+    float cp = a.grad_lse != nullptr ? ct + a.grad_lse[t] : ct;
+    float m = fabsf(ct);
+    if (a.grad_entropy != nullptr) {
+        const float ce = a.temp * a.grad_entropy[t];
+        cp = fmaf(ce, a.entropy[t], cp);
+        a.ce[c] = ce;
+        m = fmaxf(m, fabsf(ce));
+    }
     a.lse_c[c] = a.lse[t];
     a.cp[c] = bad ? nan_f() : cp;
     a.ct[c] = ct;
-    const float m = fmaxf(fabsf(cp), fabsf(ct));
+    m = fmaxf(fabsf(cp), m);
     // (within 2^100 either way, so that its inverse is a normal number)
     return m > 0.f && m < INFINITY ? fminf(fmaxf(m, 0x1p-100f), 0x1p100f) : 0.f;
 }
@@ -392,6 +399,7 @@ __device__ __forceinline__ void no_coefficients(const HeadCoefArgs& a, int64_t c
     a.lse_c[c] = 0.f;
     a.cp[c] = 0.f;
     a.ct[c] = 0.f;
+    if (a.grad_entropy != nullptr) a.ce[c] = 0.f;
 }
 
 // After head_rows_kernel.
@@ -415,7 +423,7 @@ __global__ __launch_bounds__(kRowThreads) void head_prepare_kernel(HeadPrepareAr
         return;
     }
     const int t = a.rows.src[c];
-    const float m = coefficients(k, c, t, k.q != nullptr ? k.q[t].x != k.q[t].x : a.rows.target[c] < 0);
+    const float m = coefficients(k, c, t, k.q != nullptr ? k.q[t].x != k.q[t].x : a.rows.targets != nullptr && a.rows.target[c] < 0);
     // (integer order is float order for these bits; the maximum does not depend on the order)
     atomicMax(reinterpret_cast<unsigned int*>(k.norm), __float_as_uint(m));
 }
@@ -449,7 +457,7 @@ __global__ __launch_bounds__(kRowThreads) void head_scan_prepare_kernel(HeadPrep
         if (k.q != nullptr) {
             bad = k.q[t].x != k.q[t].x;
         } else {
-            const int64_t target = a.rows.targets[t];
+            const int64_t target = a.rows.targets != nullptr ? a.rows.targets[t] : 0;
             bad = target < 0 || target >= a.rows.vocab;
         }
         m = fmaxf(m, coefficients(k, c, t, bad));
