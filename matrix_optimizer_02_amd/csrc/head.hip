@@ -345,10 +345,15 @@ dmuon_status probs_chunk_forward(const Call& c, const Probs& o) {
         logits_args(c, v, v0, step, a);
         a.part = v.at<float2>(L.off_part);
         a.target_logit = v.target_logit();
-        a.logits = v.at<float>(P.off_logits);
+        if (P.keep_logits) a.logits = v.at<float>(P.off_logits);
         a.logits_ld = (int32_t)round_up(L.vocab, kHeadTile);
-        HEAD_TRY(launch_logits(kHeadLse, c, v, v0, step, a, L.tokens));
+        a.part_e = v.at<float>(P.off_part_e);
+        a.top = v.at<float2>(P.off_top);
+        a.top_at = v.at<uint8_t>(P.off_top_at);
+        const bool top = c.desc->top_k > 0 && !P.keep_logits;
+        HEAD_TRY(launch_logits(top ? kHeadTop : kHeadProbs, c, v, v0, step, a, L.tokens));
     }
+    const int wave_rows = head_wave_rows(L.s_tile.tp, L.s_tile.tq);
     HeadProbsArgs r{};
     r.count = v.count();
     r.src = v.src();
@@ -357,8 +362,20 @@ dmuon_status probs_chunk_forward(const Call& c, const Probs& o) {
     r.vocab = L.vocab;
     r.inv_temp = 1.f / c.temp;
     r.k = c.desc->top_k;
-    r.logits = v.at<float>(P.off_logits);
+    if (P.keep_logits) r.logits = v.at<float>(P.off_logits);
     r.logits_ld = round_up(L.vocab, kHeadTile);
+    r.part = v.at<float2>(L.off_part);
+    r.part_e = v.at<float>(P.off_part_e);
+    r.parts = (int32_t)ceil_div(L.vocab, L.s_tile.tp) * wave_rows;
+    r.part_rows = L.s_tile.tp / wave_rows;
+    r.t_pad = L.t_pad;
+    r.target_logit = v.target_logit();
+    r.top = v.at<float2>(P.off_top);
+    r.top_at = v.at<uint8_t>(P.off_top_at);
+    r.hidden = c.hidden;
+    r.weight = c.weight;
+    r.esize = L.esize;
+    r.cols = L.hidden;
     r.logprobs = o.logprobs;
     r.entropy = o.entropy;
     r.lse = o.lse;
@@ -435,7 +452,7 @@ dmuon_status backward(const Call& c, const Upstream& u, void* grad_hidden, void*
     if (distill) b.add(u.student, 4 * d.tokens * d.top_k, false);
     if (grad_hidden != nullptr) b.add(grad_hidden, d.tokens * d.hidden * e, true);
     if (grad_weight != nullptr) b.add(grad_weight, d.vocab * d.hidden * e, true);
-    const ProbsLayout P = probs ? probs_layout_of(d, true) : ProbsLayout{head_layout_of(d, true), 0, 0, 0};
+    const ProbsLayout P = probs ? probs_layout_of(d, true) : ProbsLayout{head_layout_of(d, true), 0, 0, 0, 0, 0, 0, 0};
     const HeadLayout& L = P.head;
     if (d.tokens == 0) {
         if (!b.good()) return DMUON_ERR_INVALID_ARG;

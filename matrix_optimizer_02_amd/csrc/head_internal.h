@@ -24,7 +24,9 @@ enum HeadMode : int32_t {
     kHeadDh = 2,    // P = W (k = vocab rows, columns of hidden), Q = ds rows: fp32 sums, added per piece
     kHeadDw = 3,    // P = H (k = tokens, columns of hidden), Q = ds (k = tokens, columns of vocab): dW rows
     kHeadDwSum = 4,  // the same in splits of the tokens: fp32 sums
-    kHeadGradEntropy = 5  // as Grad, with the entropy's gradient
+    kHeadGradEntropy = 5, // as Grad, with the entropy's gradient
+    kHeadProbs = 6,  // as Lse, with the sum that the entropy takes
+    kHeadTop = 7     // ... and the two largest logits of every group of 16 words
 };
 
 struct HeadGemmArgs {
@@ -55,6 +57,9 @@ struct HeadGemmArgs {
     float* target_logit;
     float* logits;               // Lse: the logits too (row stride logits_ld), or null
     int32_t logits_ld;
+    float* part_e;               // Probs: sum of p log2 p' per part (p' relative to the part's largest)
+    float2* top;                 // Top: top[group * t_pad + row], see k_head_probs.hip
+    uint8_t* top_at;             // ... and where in their group they are, 4 bits each
     const float* lse;            // per compact row
     const float* cp;             // coefficient of p
     const float* ct;             // coefficient at the target
@@ -164,8 +169,20 @@ struct HeadProbsArgs {
     int64_t tokens, vocab;
     float inv_temp;
     int32_t k;
-    const float* logits;    // of the compact rows
+    const float* logits;    // of the compact rows, or null:
     int64_t logits_ld;
+    const float2* part;     // statistics of the rows' parts
+    const float* part_e;
+    int32_t parts;
+    int32_t part_rows;      // words of a part
+    int64_t t_pad;
+    const float* target_logit;
+    const float2* top;      // k > 0: the parts' groups
+    const uint8_t* top_at;
+    const void* hidden;     // ... and the operands, for words that a group does not show
+    const void* weight;
+    int32_t esize;
+    int64_t cols;
     float* logprobs;        // or null
     float* entropy;         // or null
     float* lse;

@@ -14,7 +14,7 @@ namespace {
 // cache next to what those stream.
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
 constexpr int64_t kLowTokens = 128;
-// Bytes of logits that a forward call of the log probabilities holds.
+// Bytes that a forward call of the log probabilities holds for its alternatives.
 constexpr int64_t kProbsBytes = int64_t(1) << 30;
 constexpr int64_t kPieceMin = 8192;  // vocab rows: fewer would leave dW's launch short of tiles
 
@@ -198,8 +198,19 @@ dmuon_status probs_check_desc(const dmuon_head_desc* d, bool backward) {
     return d->top_k > kHeadMaxAlternatives ? DMUON_ERR_UNSUPPORTED : DMUON_OK;
 }
 
+namespace {
+
+// Alternatives come from the two largest logits of every group of 16 words, which the
+// products' epilogue leaves; where a row's alternatives share a group, the group's other
+// logits are formed again.  With K alternatives spread over V / 16 groups that are
+// 8 K^2 / V groups: from one in eight alternatives on, the logits themselves are kept.
+bool probs_keep(const dmuon_head_desc& d) { return d.top_k > 0 && d.vocab < 64 * (int64_t)d.top_k; }
+
+}  // namespace
+
 int64_t probs_chunk(const dmuon_head_desc& d) {
-    const int64_t row = 4 * round_up(d.vocab, kHeadTile);
+    if (d.top_k == 0) return std::max<int64_t>(d.tokens, 1);
+    const int64_t v_pad = round_up(d.vocab, kHeadTile), row = probs_keep(d) ? 4 * v_pad : v_pad / 16 * 9;
     return std::max<int64_t>(kProbsBytes / row / kHeadTile, 1) * kHeadTile;
 }
 
@@ -214,8 +225,19 @@ ProbsLayout probs_layout_of(const dmuon_head_desc& d, bool backward) {
         at += align_up((size_t)bytes);
         return o;
     };
-    if (backward) L.off_ce = take(4 * L.head.t_pad);
-    else L.off_logits = take(4 * L.head.t_pad * round_up(d.vocab, kHeadTile));
+    const int64_t v_pad = round_up(d.vocab, kHeadTile), t_pad = L.head.t_pad;
+    const HeadTile s = L.head.s_tile;
+    L.keep_logits = !backward && probs_keep(d);
+    if (backward) {
+        L.off_ce = take(4 * t_pad);
+    } else {
+        L.off_part_e = take(4 * (v_pad / s.tp) * head_wave_rows(s.tp, s.tq) * t_pad);
+        if (L.keep_logits) L.off_logits = take(4 * t_pad * v_pad);
+        else if (d.top_k > 0) {
+            L.off_top = take(8 * (v_pad / 16) * t_pad);
+            L.off_top_at = take((v_pad / 16) * t_pad);
+        }
+    }
     L.bytes = at;
     return L;
 }

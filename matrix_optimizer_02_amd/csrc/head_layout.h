@@ -85,7 +85,10 @@ HeadLayout head_layout_of(dmuon_head_desc d, bool backward);
 // chunk of the tokens at a time.
 struct ProbsLayout {
     HeadLayout head;
-    size_t off_logits;  // forward
+    int32_t keep_logits;  // forward: the logits lie in memory
+    size_t off_logits;
+    size_t off_part_e;    // forward otherwise: sums for the entropy, the groups' largest
+    size_t off_top, off_top_at;
     size_t off_ce;      // backward
     size_t bytes;
 };

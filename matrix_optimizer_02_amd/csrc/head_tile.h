@@ -100,6 +100,8 @@ __device__ __forceinline__ void weave() {
 }
 
 constexpr bool is_dw(int mode) { return mode == kHeadDw || mode == kHeadDwSum; }
+constexpr bool is_probs(int mode) { return mode == kHeadProbs || mode == kHeadTop; }
+constexpr bool is_stats(int mode) { return mode == kHeadLse || is_probs(mode); }
 constexpr bool is_grad(int mode) { return mode == kHeadGrad || mode == kHeadGradEntropy; }
 
 // The tiles of a launch and this workgroup's share of them: XCD x takes one
@@ -148,7 +150,7 @@ __device__ __forceinline__ float norm_of(const float* norm) {
 // the backward modes (3687 x 3584 x 128256 9.06 / 9.25 ms).
 template <typename C, int MODE>
 constexpr bool plain_loop(bool scaled) {
-    return MODE == kHeadLse && !scaled && C::TQ == 256;
+    return is_stats(MODE) && !scaled && C::TQ == 256;
 }
 
 // Writes a finished tile.  acc[i][j][v]: P row wr RW + 32 i + 8 (v / 4) + 4 khalf
@@ -195,7 +197,7 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
             __builtin_amdgcn_sched_barrier(0);  // no more of the scales in registers at once
         }
     }
-    if constexpr (MODE == kHeadLse) {
+    if constexpr (is_stats(MODE)) {
         const int64_t v_base = args.v0 + (int64_t)t.I * TP + wr * C::RW;  // vocab row of the wave's row 0
         const int64_t left = args.vocab - v_base;
         const int limit = left < C::RW ? (int)(left < 0 ? 0 : left) : C::RW;  // rows inside the vocabulary
@@ -254,16 +256,49 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
             m = fmaxf(m, __shfl_xor(m, 32, 64));
             const float m0 = m == -INFINITY ? 0.f : m;
             float ls[4] = {0.f, 0.f, 0.f, 0.f};  // four chains: an addition need not wait for the one before
+            [[maybe_unused]] float es[4] = {0.f, 0.f, 0.f, 0.f};
             #pragma unroll
             for (int i = 0; i < C::FI; ++i) {
                 #pragma unroll
-                for (int v = 0; v < 16; ++v) ls[v & 3] += __builtin_amdgcn_exp2f((acc[i][j][v] - m0) * scale);
+                for (int v = 0; v < 16; ++v) {
+                    const float x = (acc[i][j][v] - m0) * scale;
+                    const float p = __builtin_amdgcn_exp2f(x);
+                    ls[v & 3] += p;
+                    // (p is 0 long before x is -200, and 0 times the logarithm has to be 0)
+                    if constexpr (is_probs(MODE)) es[v & 3] = fmaf(p, fmaxf(x, -200.f), es[v & 3]);
+                }
                 if (!kRowNumbers) __builtin_amdgcn_sched_barrier(0);  // no more of the differences in registers at once
             }
             float l = (ls[0] + ls[1]) + (ls[2] + ls[3]);
             l += __shfl_xor(l, 32, 64);
-            if (khalf == 0)
-                args.part[((int64_t)(args.first_tile + t.I) * C::WR + wr) * args.t_pad + row] = make_float2(m, l);
+            const int64_t at = ((int64_t)(args.first_tile + t.I) * C::WR + wr) * args.t_pad + row;
+            if (khalf == 0) args.part[at] = make_float2(m, l);
+            if constexpr (is_probs(MODE)) {
+                float e = (es[0] + es[1]) + (es[2] + es[3]);
+                e += __shfl_xor(e, 32, 64);
+                if (khalf == 0) args.part_e[at] = e;
+            }
+            if constexpr (MODE == kHeadTop) {
+                // The two largest of the lane's 16 words of each block of 32, equal ones in order.
+                // The third and further ones are rarely asked for (k_head_probs.hip).
+                #pragma unroll
+                for (int i = 0; i < C::FI; ++i) {
+                    float m1 = -INFINITY, m2 = -INFINITY;
+                    int at1 = 0, at2 = 0;
+                    #pragma unroll
+                    for (int v = 0; v < 16; ++v) {
+                        const float x = acc[i][j][v];
+                        const bool first = x > m1, second = x > m2;
+                        at2 = first ? at1 : second ? v : at2;
+                        at1 = first ? v : at1;
+                        m2 = __builtin_amdgcn_fmed3f(m1, m2, x);
+                        m1 = fmaxf(m1, x);
+                    }
+                    const int64_t group = 2 * (v_base / 32 + i) + khalf;
+                    args.top[group * args.t_pad + row] = make_float2(m1, m2);
+                    args.top_at[group * args.t_pad + row] = (uint8_t)(at1 | at2 << 4);
+                }
+            }
         }
     } else if constexpr (MODE == kHeadDh || MODE == kHeadDwSum) {
         __syncthreads();

@@ -179,7 +179,7 @@ __global__ __launch_bounds__(C::NT) __attribute__((
     static_assert(TQ % kPieces == 0 && TQ / kPieces % C::CW == 0, "a wave's columns lie in one piece");
     // Stores that every wave issues behind that slab's loads, at least: they need not
     // have completed for the slab to be there.
-    constexpr int kStores = MODE == kHeadLse ? C::FJ
+    constexpr int kStores = is_stats(MODE) ? C::FJ
                             : is_grad(MODE) && TQ == 256 ? TQ * TP / 8 / C::NT
                             : MODE == kHeadDh ? C::FI * C::FJ * 4 : 0;
     bool behind = false;
@@ -433,6 +433,12 @@ hipError_t launch_config(int mode, const HeadGemmArgs& a, int64_t max_tiles, hip
         case kHeadGradEntropy:
             return f32 ? launch<C, kHeadGradEntropy, kHeadHalf2>(a, max_tiles, stream)
                        : launch<C, kHeadGradEntropy, kHeadBf16>(a, max_tiles, stream);
+        case kHeadProbs:
+            return f32 ? launch<C, kHeadProbs, kHeadHalf2>(a, max_tiles, stream)
+                       : launch<C, kHeadProbs, kHeadBf16>(a, max_tiles, stream);
+        case kHeadTop:
+            return f32 ? launch<C, kHeadTop, kHeadHalf2>(a, max_tiles, stream)
+                       : launch<C, kHeadTop, kHeadBf16>(a, max_tiles, stream);
         case kHeadDh:
             return launch<C, kHeadDh, kHeadBf16>(a, max_tiles, stream);
         case kHeadDw:

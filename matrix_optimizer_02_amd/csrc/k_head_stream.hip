@@ -338,6 +338,10 @@ hipError_t launch_config(int mode, const HeadGemmArgs& a, int64_t max_tiles, hip
             return f32 ? launch<F, kHeadGrad>(a, max_tiles, stream) : launch<B, kHeadGrad>(a, max_tiles, stream);
         case kHeadGradEntropy:
             return f32 ? launch<F, kHeadGradEntropy>(a, max_tiles, stream) : launch<B, kHeadGradEntropy>(a, max_tiles, stream);
+        case kHeadProbs:
+            return f32 ? launch<F, kHeadProbs>(a, max_tiles, stream) : launch<B, kHeadProbs>(a, max_tiles, stream);
+        case kHeadTop:
+            return f32 ? launch<F, kHeadTop>(a, max_tiles, stream) : launch<B, kHeadTop>(a, max_tiles, stream);
         case kHeadDh:
             return f32 ? launch<F, kHeadDh>(a, max_tiles, stream) : launch<B, kHeadDh>(a, max_tiles, stream);
         default: return hipErrorInvalidValue;
@@ -353,9 +357,14 @@ hipError_t launch_head_stream(int mode, HeadTile tile, const HeadGemmArgs& a, in
         // in the place of a 256 x 256 tile: half of one, its statistics laid out as the whole one's
         using F = Stream<Config<256, 128, 3, head_wave_rows(256, 256)>, true>;
         if (a.parts == 1) return hipErrorInvalidValue;
-        if (mode == kHeadLse) return launch<F, kHeadLse>(a, max_tiles, stream);
-        if (mode == kHeadGradEntropy) return launch<F, kHeadGradEntropy>(a, max_tiles, stream);
-        return mode == kHeadGrad ? launch<F, kHeadGrad>(a, max_tiles, stream) : hipErrorInvalidValue;
+        switch (mode) {
+            case kHeadLse: return launch<F, kHeadLse>(a, max_tiles, stream);
+            case kHeadProbs: return launch<F, kHeadProbs>(a, max_tiles, stream);
+            case kHeadTop: return launch<F, kHeadTop>(a, max_tiles, stream);
+            case kHeadGrad: return launch<F, kHeadGrad>(a, max_tiles, stream);
+            case kHeadGradEntropy: return launch<F, kHeadGradEntropy>(a, max_tiles, stream);
+            default: return hipErrorInvalidValue;
+        }
     }
     if (tile.tp == 64) return launch_config<Config<64, 64, 4>>(mode, a, max_tiles, stream);
     if (tile.tq == 64) return launch_config<Config<256, 64, 2>>(mode, a, max_tiles, stream);
