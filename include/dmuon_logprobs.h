@@ -38,10 +38,10 @@
  * row's largest one, not from lse; ds in the gradients' products is held as there
  * (bf16 calls round it to bf16 once, relative to the largest of |g|, |e| and
  * |g + e entropy|; entries below 2^-126 of that count as 0), fp32 calls multiply in
- * parts.  An alternative is found by the logit that its product formed; where a
- * group of 16 words holds three or more of a row's alternatives, the third and later
- * ones' logits are formed again by another order of summation, which may differ in
- * the last bits and so order what those bits decide otherwise.
+ * parts.  An alternative is found by the logit that its product formed; where several of
+ * a row's alternatives lie in one group of 16 words, all but the first of them are by
+ * logits formed again in another order of summation, which may differ in the last bits
+ * and so order what those bits decide otherwise.
  *
  * Conventions are those of dmuon_head.h: status codes, dense row-major arrays,
  * 16-byte aligned device pointers of the current device, a 256-byte aligned

@@ -349,7 +349,6 @@ dmuon_status probs_chunk_forward(const Call& c, const Probs& o) {
         a.logits_ld = (int32_t)round_up(L.vocab, kHeadTile);
         a.part_e = v.at<float>(P.off_part_e);
         a.top = v.at<float2>(P.off_top);
-        a.top_at = v.at<uint8_t>(P.off_top_at);
         const bool top = c.desc->top_k > 0 && !P.keep_logits;
         HEAD_TRY(launch_logits(top ? kHeadTop : kHeadProbs, c, v, v0, step, a, L.tokens));
     }
@@ -371,7 +370,6 @@ dmuon_status probs_chunk_forward(const Call& c, const Probs& o) {
     r.t_pad = L.t_pad;
     r.target_logit = v.target_logit();
     r.top = v.at<float2>(P.off_top);
-    r.top_at = v.at<uint8_t>(P.off_top_at);
     r.hidden = c.hidden;
     r.weight = c.weight;
     r.esize = L.esize;
@@ -452,7 +450,7 @@ dmuon_status backward(const Call& c, const Upstream& u, void* grad_hidden, void*
     if (distill) b.add(u.student, 4 * d.tokens * d.top_k, false);
     if (grad_hidden != nullptr) b.add(grad_hidden, d.tokens * d.hidden * e, true);
     if (grad_weight != nullptr) b.add(grad_weight, d.vocab * d.hidden * e, true);
-    const ProbsLayout P = probs ? probs_layout_of(d, true) : ProbsLayout{head_layout_of(d, true), 0, 0, 0, 0, 0, 0, 0};
+    const ProbsLayout P = probs ? probs_layout_of(d, true) : ProbsLayout{head_layout_of(d, true), 0, 0, 0, 0, 0, 0};
     const HeadLayout& L = P.head;
     if (d.tokens == 0) {
         if (!b.good()) return DMUON_ERR_INVALID_ARG;

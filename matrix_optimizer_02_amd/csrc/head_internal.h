@@ -26,7 +26,7 @@ enum HeadMode : int32_t {
     kHeadDwSum = 4,  // the same in splits of the tokens: fp32 sums
     kHeadGradEntropy = 5, // as Grad, with the entropy's gradient
     kHeadProbs = 6,  // as Lse, with the sum that the entropy takes
-    kHeadTop = 7     // ... and the two largest logits of every group of 16 words
+    kHeadTop = 7     // ... and what every group of 16 words shows of its largest logits
 };
 
 struct HeadGemmArgs {
@@ -59,7 +59,6 @@ struct HeadGemmArgs {
     int32_t logits_ld;
     float* part_e;               // Probs: sum of p log2 p' per part (p' relative to the part's largest)
     float2* top;                 // Top: top[group * t_pad + row], see k_head_probs.hip
-    uint8_t* top_at;             // ... and where in their group they are, 4 bits each
     const float* lse;            // per compact row
     const float* cp;             // coefficient of p
     const float* ct;             // coefficient at the target
@@ -178,7 +177,6 @@ struct HeadProbsArgs {
     int64_t t_pad;
     const float* target_logit;
     const float2* top;      // k > 0: the parts' groups
-    const uint8_t* top_at;
     const void* hidden;     // ... and the operands, for words that a group does not show
     const void* weight;
     int32_t esize;

@@ -200,9 +200,9 @@ dmuon_status probs_check_desc(const dmuon_head_desc* d, bool backward) {
 
 namespace {
 
-// Alternatives come from the two largest logits of every group of 16 words, which the
-// products' epilogue leaves; where a row's alternatives share a group, the group's other
-// logits are formed again.  With K alternatives spread over V / 16 groups that are
+// Alternatives come from the largest logit of every group of 16 words, which the
+// products' epilogue leaves (8 bytes a group); where a row's alternatives share a group, the
+// group's other logits are formed again.  With K alternatives spread over V / 16 groups that are
 // 8 K^2 / V groups: from one in eight alternatives on, the logits themselves are kept.
 bool probs_keep(const dmuon_head_desc& d) { return d.top_k > 0 && d.vocab < 64 * (int64_t)d.top_k; }
 
@@ -210,7 +210,7 @@ bool probs_keep(const dmuon_head_desc& d) { return d.top_k > 0 && d.vocab < 64 *
 
 int64_t probs_chunk(const dmuon_head_desc& d) {
     if (d.top_k == 0) return std::max<int64_t>(d.tokens, 1);
-    const int64_t v_pad = round_up(d.vocab, kHeadTile), row = probs_keep(d) ? 4 * v_pad : v_pad / 16 * 9;
+    const int64_t v_pad = round_up(d.vocab, kHeadTile), row = probs_keep(d) ? 4 * v_pad : v_pad / 2;
     return std::max<int64_t>(kProbsBytes / row / kHeadTile, 1) * kHeadTile;
 }
 
@@ -233,10 +233,7 @@ ProbsLayout probs_layout_of(const dmuon_head_desc& d, bool backward) {
     } else {
         L.off_part_e = take(4 * (v_pad / s.tp) * head_wave_rows(s.tp, s.tq) * t_pad);
         if (L.keep_logits) L.off_logits = take(4 * t_pad * v_pad);
-        else if (d.top_k > 0) {
-            L.off_top = take(8 * (v_pad / 16) * t_pad);
-            L.off_top_at = take((v_pad / 16) * t_pad);
-        }
+        else if (d.top_k > 0) L.off_top = take(v_pad / 2 * t_pad);
     }
     L.bytes = at;
     return L;

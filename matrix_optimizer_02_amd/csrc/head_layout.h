@@ -88,7 +88,7 @@ struct ProbsLayout {
     int32_t keep_logits;  // forward: the logits lie in memory
     size_t off_logits;
     size_t off_part_e;    // forward otherwise: sums for the entropy, the groups' largest
-    size_t off_top, off_top_at;
+    size_t off_top;
     size_t off_ce;      // backward
     size_t bytes;
 };

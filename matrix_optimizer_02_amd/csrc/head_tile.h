@@ -165,14 +165,17 @@ template <typename C, int MODE, bool SCALED, int PARTS, int PIECES = 1, typename
 __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile& t, int tiles_j, char* smem,
                                            floatx16 (&acc)[C::FI][C::FJ], F&& prefetch) {
     constexpr int TP = C::TP, TQ = C::TQ;
-    const int tid = threadIdx.x, lane = tid & 63;
+    int tid = threadIdx.x;
+    // (nothing of a lane's own numbers is kept in registers through the main loop, which would spill)
+    if constexpr (is_probs(MODE)) asm volatile("" : "+v"(tid));
+    const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave % C::WR, wc = wave / C::WR;
     const int lrow = lane & 31;
     // Rows are compared as (constant) against (bound - 4 khalf), the lane's part on the one
     // side that is not a constant: 64 row numbers would otherwise be kept in registers.
     // (The plain loop leaves room for them, and is compiled to the shorter code with them.)
-    constexpr bool kRowNumbers = plain_loop<C, MODE>(SCALED);
+    constexpr bool kRowNumbers = plain_loop<C, MODE>(SCALED) && !is_probs(MODE);
     int khalf = lane >> 5;
     if constexpr (!kRowNumbers) asm volatile("" : "+v"(khalf));
     if constexpr (SCALED) {
@@ -267,36 +270,40 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
                     // (p is 0 long before x is -200, and 0 times the logarithm has to be 0)
                     if constexpr (is_probs(MODE)) es[v & 3] = fmaf(p, fmaxf(x, -200.f), es[v & 3]);
                 }
-                if (!kRowNumbers) __builtin_amdgcn_sched_barrier(0);  // no more of the differences in registers at once
+                if (!kRowNumbers || is_probs(MODE)) __builtin_amdgcn_sched_barrier(0);  // no more of the differences in registers at once
             }
             float l = (ls[0] + ls[1]) + (ls[2] + ls[3]);
             l += __shfl_xor(l, 32, 64);
-            const int64_t at = ((int64_t)(args.first_tile + t.I) * C::WR + wr) * args.t_pad + row;
-            if (khalf == 0) args.part[at] = make_float2(m, l);
+            [[maybe_unused]] float e = (es[0] + es[1]) + (es[2] + es[3]);
             if constexpr (is_probs(MODE)) {
-                float e = (es[0] + es[1]) + (es[2] + es[3]);
                 e += __shfl_xor(e, 32, 64);
-                if (khalf == 0) args.part_e[at] = e;
+                asm volatile("" : "+v"(e));  // formed here, or every exponential is kept for it
+            }
+            if (khalf == 0) {
+                const int64_t at = ((int64_t)(args.first_tile + t.I) * C::WR + wr) * args.t_pad + row;
+                args.part[at] = make_float2(m, l);
+                if constexpr (is_probs(MODE)) args.part_e[at] = e;
             }
             if constexpr (MODE == kHeadTop) {
-                // The two largest of the lane's 16 words of each block of 32, equal ones in order.
-                // The third and further ones are rarely asked for (k_head_probs.hip).
+                // Of the lane's 16 words of each block of 32: the largest (the first of equal ones), where
+                // it is, and the second.  Where the second is among a row's alternatives, the others
+                // are formed again (k_head_probs.hip): four instructions a logit here, where keeping
+                // two with their places took seven.
                 #pragma unroll
                 for (int i = 0; i < C::FI; ++i) {
                     float m1 = -INFINITY, m2 = -INFINITY;
-                    int at1 = 0, at2 = 0;
+                    uint32_t at1 = 0;
                     #pragma unroll
                     for (int v = 0; v < 16; ++v) {
                         const float x = acc[i][j][v];
-                        const bool first = x > m1, second = x > m2;
-                        at2 = first ? at1 : second ? v : at2;
-                        at1 = first ? v : at1;
+                        const bool larger = x > m1;
+                        at1 = larger ? v : at1;
                         m2 = __builtin_amdgcn_fmed3f(m1, m2, x);
-                        m1 = fmaxf(m1, x);
+                        m1 = larger ? x : m1;  // (fmaxf would take a quieted copy of every x)
                     }
-                    const int64_t group = 2 * (v_base / 32 + i) + khalf;
-                    args.top[group * args.t_pad + row] = make_float2(m1, m2);
-                    args.top_at[group * args.t_pad + row] = (uint8_t)(at1 | at2 << 4);
+                    const uint32_t second = (__float_as_uint(m2) & ~15u) | at1;
+                    args.top[(2 * (v_base / 32 + i) + khalf) * args.t_pad + row] = make_float2(m1, __uint_as_float(second));
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
