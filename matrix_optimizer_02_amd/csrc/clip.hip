@@ -123,9 +123,8 @@ __device__ __forceinline__ double block_sum64(double v) {
 
 __global__ __launch_bounds__(kThreads) void norm_squares_kernel(NormArgs a) {
     double s[2] = {0.0, 0.0};
-    int i = 0;
     for (int c = (int)blockIdx.x; c < a.pieces; c += (int)gridDim.x) {
-        while (i + 1 < a.count && a.rec[i + 1].first <= c) ++i;
+        const int i = upper_index(a.count, c, [&](int k) { return a.rec[k].first; });
         const char* const in = a.rec[i].in;
         const int64_t at = (int64_t)(c - a.rec[i].first) * kPiece - low4(in);  // of the piece in the tensor
         if (a.rec[i].bf16) piece_squares<true>(s, in + at, -at, a.rec[i].bytes - at);
@@ -193,9 +192,8 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(ClipArgs a) {
     const double ratio = a.max_norm / ((double)norm + a.eps);
     // (a ratio that is NaN: both infinite, and nothing is to be clipped)
     const float f = norm != norm ? norm : ratio < 1.0 ? (float)ratio : 1.f;
-    int i = a.count - 1;
     for (int c = a.pieces - 1 - (int)blockIdx.x; c >= 0; c -= (int)gridDim.x) {
-        while (a.rec[i].first > c) --i;
+        const int i = upper_index(a.count, c, [&](int k) { return a.rec[k].first; });
         const char* const in = a.rec[i].in;
         char* const out = a.rec[i].out;
         if (in == out && f == 1.f) continue;

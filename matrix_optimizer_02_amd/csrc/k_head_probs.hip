@@ -17,7 +17,7 @@
 // words, once for K = 128.
 //
 // What bounds it: latency.  The largest of n values are found by counting how many reach
-// a threshold, two bits of it a round, with the values in registers.
+// a threshold, two bits of it a round.
 #include "head_internal.h"
 #include "kcommon.h"
 
@@ -27,6 +27,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kK = kHeadMaxAlternatives;
+constexpr int kSorted = kK;  // candidates that are sorted, at most
 
 __device__ __forceinline__ float nan_f() { return __uint_as_float(0x7fc00000u); }
 
@@ -77,92 +78,85 @@ __device__ __forceinline__ float block_add(float v, Joins& red) {
     return (red.f[0] + red.f[1]) + (red.f[2] + red.f[3]);
 }
 
-// The k largest of up to PER values a thread (orders o, 0 where there is none, at places
-// p), in any order; returns their number (fewer than k where there are not as many).
-template <int PER, typename P>
-__device__ __forceinline__ int largest(const uint32_t (&o)[PER], P&& place, int k, uint64_t* out, int* taken,
-                                       Joins& red) {
+// At least the k largest and at most `most` (>= k) of n values in LDS (orders o, 0 where
+// there is none; at places p, or INDEX: at their own), equal ones by the lower place, in any order; returns their
+// number (fewer than k where there are not as many).  Counting how many reach a threshold,
+// two bits of it a round: a few rounds leave few enough of them.
+template <bool INDEX = false>
+__device__ __forceinline__ int largest(const uint32_t* o, const uint32_t* p, int n, int k, int most, uint64_t* out,
+                                       int* taken, Joins& red) {
     int turn = 0;
-    // how many of the values are at least a, b and c, by `at`
-    auto count = [&](auto&& at, uint32_t a, uint32_t b, uint32_t c) {
-        int4 n = make_int4(0, 0, 0, 0);
-        #pragma unroll
-        for (int u = 0; u < PER; ++u) {
-            const uint32_t x = at(u);
-            n.x += __popcll(__builtin_amdgcn_ballot_w64(x >= a));
-            n.y += __popcll(__builtin_amdgcn_ballot_w64(x >= b));
-            n.z += __popcll(__builtin_amdgcn_ballot_w64(x >= c));
+    // how many of the values are at least a, b and c: of all, or of the places (from the
+    // last on) of those that equal `only`
+    auto count = [&](uint32_t only, uint32_t a, uint32_t b, uint32_t c) {
+        int4 s = make_int4(0, 0, 0, 0);
+        for (int i0 = 0; i0 < n; i0 += 4 * kThreads) {
+            uint32_t x[4];
+            #pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int i = i0 + q * kThreads + (int)threadIdx.x;
+                x[q] = i < n ? o[i] : 0;
+                if (only != 0) x[q] = i < n && x[q] == only ? ~(INDEX ? (uint32_t)i : p[i]) : 0;
+            }
+            #pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                s.x += __popcll(__builtin_amdgcn_ballot_w64(x[q] >= a));
+                s.y += __popcll(__builtin_amdgcn_ballot_w64(x[q] >= b));
+                s.z += __popcll(__builtin_amdgcn_ballot_w64(x[q] >= c));
+            }
         }
         turn ^= 1;  // (the counts of the round before may still be read)
-        if ((threadIdx.x & 63) == 0) red.counts[turn][threadIdx.x >> 6] = n;
+        if ((threadIdx.x & 63) == 0) red.counts[turn][threadIdx.x >> 6] = s;
         __syncthreads();
-        n = red.counts[turn][0];
+        s = red.counts[turn][0];
         #pragma unroll
         for (int w = 1; w < kWaves; ++w) {
             const int4 m = red.counts[turn][w];
-            n.x += m.x, n.y += m.y, n.z += m.z;
+            s.x += m.x, s.y += m.y, s.z += m.z;
         }
-        return n;
+        return s;
     };
-    // The largest threshold that k values reach: two bits a round.
-    auto threshold = [&](auto&& at, int top, int want, int& reach) {
-        uint32_t least = 0;
-        for (int bit = top; bit >= 0 && reach != want; bit -= 2) {
-            const uint32_t a = least | 1u << bit, b = least | 2u << bit, c = least | 3u << bit;
-            const int4 n = count(at, a, b, c);
-            if (n.z >= want) least = c, reach = n.z;
-            else if (n.y >= want) least = b, reach = n.y;
-            else if (n.x >= want) least = a, reach = n.x;
-        }
-        return least;
-    };
-    __syncthreads();
-    const int held = count([&](int u) { return o[u]; }, 1u, 1u, 1u).x;
+    __syncthreads();  // (the last call's number has been read)
     if (threadIdx.x == 0) *taken = 0;
-    if (k > held) k = held;
-    int reach = held;
-    const uint32_t least = threshold([&](int u) { return o[u]; }, 30, k, reach);
-    // of values equal to the least one, those at the lowest places
-    uint32_t low = 0;
-    if (reach > k) {
-        const int above = least == 0xffffffffu ? 0 : count([&](int u) { return o[u]; }, least + 1, 1u, 1u).x;
-        int equal = reach - above;
-        low = threshold([&](int u) { return o[u] == least ? ~place(u) : 0u; }, 30, k - above, equal);
+    __syncthreads();
+    // The largest threshold that k values reach; then, of too many that equal it, the one of
+    // their places.
+    uint32_t least = 0, low = 0;
+    int reach = n;  // values at the threshold, or more than there are
+    #pragma unroll 1
+    for (int pass = 0; pass < 2 && reach > most; ++pass) {
+        uint32_t& at = pass == 0 ? least : low;
+        const int above = pass == 0 ? 0 : count(0, least + 1, 1u, 1u).x;  // (no order is the largest integer)
+        #pragma unroll 1
+        for (int bit = 30; bit >= 0 && reach > most; bit -= 2) {
+            const uint32_t a = at | 1u << bit, b = at | 2u << bit, c = at | 3u << bit;
+            const int4 s = count(pass == 0 ? 0 : least, a, b, c);
+            if (above + s.z >= k) at = c, reach = above + s.z;
+            else if (above + s.y >= k) at = b, reach = above + s.y;
+            else if (above + s.x >= k) at = a, reach = above + s.x;
+        }
+        if (least == 0) break;  // fewer than k: all of them
+    }
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint32_t x = o[i], place = INDEX ? (uint32_t)i : p[i];
+        if (x != 0 && (x > least || (x == least && ~place >= low)))
+            out[atomicAdd(taken, 1)] = key_of(x, place);  // (places in a list that is sorted)
     }
     __syncthreads();
-    if (k > 0) {
-        #pragma unroll
-        for (int u = 0; u < PER; ++u)
-            if (o[u] != 0 && (o[u] > least || (o[u] == least && ~place(u) >= low)))
-                out[atomicAdd(taken, 1)] = key_of(o[u], place(u));  // (places in a list that is sorted next)
-    }
-    __syncthreads();
-    return k;
+    return *taken;
 }
 
-// The same of n keys in LDS.
-template <int PER>
-__device__ __forceinline__ int largest_keys(const uint64_t* keys, int n, int k, uint64_t* out, int* taken, Joins& red) {
-    uint32_t o[PER], p[PER];
-    #pragma unroll
-    for (int u = 0; u < PER; ++u) {
-        const int i = u * kThreads + (int)threadIdx.x;
-        const uint64_t x = i < n ? keys[i] : 0;
-        o[u] = order_in(x);
-        p[u] = place_of(x);
-    }
-    return largest<PER>(o, [&](int u) { return p[u]; }, k, out, taken, red);
-}
-
-// n different keys in descending order.
-__device__ __forceinline__ void sort_keys(const uint64_t* keys, int n, uint64_t* sorted) {
+// The k first of n different keys in descending order.
+__device__ __forceinline__ int sort_keys(const uint64_t* keys, int n, int k, uint64_t* sorted) {
     for (int i = threadIdx.x; i < n; i += kThreads) {
         const uint64_t mine = keys[i];
         int rank = 0;
+        #pragma unroll 4
         for (int j = 0; j < n; ++j) rank += keys[j] > mine ? 1 : 0;
-        sorted[rank] = mine;
+        if (rank < k) sorted[rank] = mine;
     }
     __syncthreads();
+    return n < k ? n : k;
 }
 
 // A token that takes no part.
@@ -215,37 +209,52 @@ __device__ __forceinline__ void write_top(const HeadProbsArgs& a, int64_t t, con
     }
 }
 
-// The parts' statistics in registers, PER a thread (more parts: joined as they are read).
-template <int PER>
-struct Parts {
-    uint32_t order[PER];  // of the parts' maxima
-};
-template <int PER>
-__device__ __forceinline__ Row join_parts(const HeadProbsArgs& a, int64_t c, int64_t t, Parts<PER>& parts, Joins& red) {
-    const float2* const part = a.part + c;
-    const float* const part_e = a.part_e + c;
-    float2 p[PER];
-    float pe[PER];
+// Parts a thread takes, one after the other.
+__device__ __forceinline__ int share_of_parts(const HeadProbsArgs& a) { return (a.parts + kThreads - 1) / kThreads; }
+
+// The row's outputs from its parts; orders (null: not) receives those of each thread's
+// largest maximum.
+__device__ __forceinline__ Row join_parts(const HeadProbsArgs& a, int64_t c, int64_t t, uint32_t* orders, Joins& red) {
+    const int per = share_of_parts(a), first = (int)threadIdx.x * per;
+    const int mine = max(0, min(per, a.parts - first));
+    const float2* const part = a.part + (int64_t)first * a.t_pad + c;
+    const float* const part_e = a.part_e + (int64_t)first * a.t_pad + c;
+    constexpr int kAhead = 8;  // loads on their way at once; the first ones' results are kept
+    float2 x[kAhead];
+    float y[kAhead];
     #pragma unroll
-    for (int u = 0; u < PER; ++u) {
-        const int i = u * kThreads + (int)threadIdx.x;
-        const bool in = i < a.parts;
-        p[u] = in ? part[i * a.t_pad] : make_float2(-INFINITY, 0.f);
-        pe[u] = in ? part_e[i * a.t_pad] : 0.f;
+    for (int u = 0; u < kAhead; ++u) {
+        x[u] = u < mine ? part[u * a.t_pad] : make_float2(-INFINITY, 0.f);
+        y[u] = u < mine ? part_e[u * a.t_pad] : 0.f;
     }
     float m = -INFINITY;
     #pragma unroll
-    for (int u = 0; u < PER; ++u) m = fmaxf(m, p[u].x);
-    for (int i = PER * kThreads + (int)threadIdx.x; i < a.parts; i += kThreads) m = fmaxf(m, part[i * a.t_pad].x);
+    for (int u = 0; u < kAhead; ++u) m = fmaxf(m, x[u].x);
+    #pragma unroll 1
+    for (int i = kAhead; i < mine; i += kAhead) {
+        float z[kAhead];
+        #pragma unroll
+        for (int u = 0; u < kAhead; ++u) z[u] = part[min(i + u, mine - 1) * a.t_pad].x;
+        #pragma unroll
+        for (int u = 0; u < kAhead; ++u) m = fmaxf(m, z[u]);
+    }
+    if (orders != nullptr) orders[threadIdx.x] = order_of(m);
     m = block_max(m, red);
     float l = 0.f, e = 0.f;
-    #pragma unroll
-    for (int u = 0; u < PER; ++u) {
-        add_part(a, m, p[u], pe[u], l, e);
-        parts.order[u] = order_of(p[u].x);
+    #pragma unroll 1
+    for (int i = 0;;) {
+        #pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (i + u < mine) add_part(a, m, x[u], y[u], l, e);
+        i += kAhead;
+        if (i >= mine) break;
+        #pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int at = min(i + u, mine - 1);
+            x[u] = part[at * a.t_pad];
+            y[u] = part_e[at * a.t_pad];
+        }
     }
-    for (int i = PER * kThreads + (int)threadIdx.x; i < a.parts; i += kThreads)
-        add_part(a, m, part[i * a.t_pad], part_e[i * a.t_pad], l, e);
     l = block_add(l, red);
     e = block_add(e, red);
     return row_of(a, c, t, m, l, e, threadIdx.x == 0);
@@ -269,18 +278,21 @@ __global__ __launch_bounds__(kThreads) void probs_join_kernel(HeadProbsArgs a) {
     const float2* const part = a.part + c;
     const float* const part_e = a.part_e + c;
     float m = -INFINITY;
-    #pragma unroll 4
+    #pragma unroll 8
     for (int i = g; i < a.parts; i += 16) m = fmaxf(m, part[i * a.t_pad].x);
     #pragma unroll
     for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 16));
+    const int per = share_of_parts(a);
     float l[kWaves], e[kWaves];
     #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
         float pl[4] = {0.f, 0.f, 0.f, 0.f}, pe[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int i = 64 * w + g; i < a.parts; i += kThreads) {
+        for (int j = 0; j < per; ++j) {
             #pragma unroll
-            for (int b = 0; b < 4; ++b)
-                if (i + 16 * b < a.parts) add_part(a, m, part[(i + 16 * b) * a.t_pad], part_e[(i + 16 * b) * a.t_pad], pl[b], pe[b]);
+            for (int b = 0; b < 4; ++b) {
+                const int i = (64 * w + 16 * b + g) * per + j;
+                if (i < a.parts) add_part(a, m, part[i * a.t_pad], part_e[i * a.t_pad], pl[b], pe[b]);
+            }
         }
         l[w] = (pl[0] + pl[2]) + (pl[1] + pl[3]);
         e[w] = (pe[0] + pe[2]) + (pe[1] + pe[3]);
@@ -293,44 +305,47 @@ __global__ __launch_bounds__(kThreads) void probs_join_kernel(HeadProbsArgs a) {
     row_of(a, c, t, m, (l[0] + l[1]) + (l[2] + l[3]), (e[0] + e[1]) + (e[2] + e[3]), g == 0);
 }
 
+// The row of a block: each XCD takes neighbouring rows, whose parts share lines of its L2.
+__device__ __forceinline__ int64_t row_of_block() {
+    const int64_t each = gridDim.x / 8;
+    return (int64_t)(blockIdx.x % 8) * each + blockIdx.x / 8;
+}
+
 // Statistics alone, of few rows.
 __global__ __launch_bounds__(kThreads) void probs_row_kernel(HeadProbsArgs a) {
     __shared__ Joins red;
-    const int64_t c = blockIdx.x;
+    const int64_t c = row_of_block();
+    if (c >= a.tokens) return;
     const int64_t t = a.src[c];
     if (c >= *a.count) {
         idle_row(a, t, threadIdx.x, kThreads);
         return;
     }
-    Parts<8> parts;
-    join_parts<8>(a, c, t, parts, red);
+    join_parts(a, c, t, nullptr, red);
 }
 
-// Alternatives from the row's kept logits (at most 64 kK words).
-constexpr int kKeptPer = 64 * kK / kThreads;
+// Alternatives from the row's kept logits.
+constexpr int kKept = 64 * kK;
 __global__ __launch_bounds__(kThreads) void probs_logits_kernel(HeadProbsArgs a) {
     __shared__ Joins red;
-    __shared__ uint64_t keys[kK], sorted[kK];
+    __shared__ uint32_t orders[kKept];
+    __shared__ uint64_t keys[kSorted], sorted[kK];
     __shared__ int taken;
-    const int64_t c = blockIdx.x;
+    const int64_t c = row_of_block();
+    if (c >= a.tokens) return;
     const int64_t t = a.src[c];
     if (c >= *a.count) {
         idle_row(a, t, threadIdx.x, kThreads);
         return;
     }
-    Parts<1> parts;
-    const Row r = join_parts<1>(a, c, t, parts, red);
+    const Row r = join_parts(a, c, t, nullptr, red);
     int held = 0;
     if (r.fine) {
         const float* const row = a.logits + c * a.logits_ld;
-        uint32_t o[kKeptPer];
-        #pragma unroll
-        for (int u = 0; u < kKeptPer; ++u) {
-            const int i = u * kThreads + (int)threadIdx.x;
-            o[u] = i < a.vocab ? order_of(row[i]) : 0;
-        }
-        held = largest<kKeptPer>(o, [&](int u) { return (uint32_t)(u * kThreads + (int)threadIdx.x); }, a.k, keys, &taken, red);
-        sort_keys(keys, held, sorted);
+        const int n = (int)a.vocab;  // at most kKept (head_layout.cpp)
+        #pragma unroll 8
+        for (int i = threadIdx.x; i < n; i += kThreads) orders[i] = order_of(row[i]);
+        held = sort_keys(keys, largest<true>(orders, nullptr, n, a.k, kSorted, keys, &taken, red), a.k, sorted);
     }
     write_top(a, t, sorted, held, r);
 }
@@ -401,113 +416,133 @@ __device__ __forceinline__ uint32_t second_order(float shown) {
     return order_of(__uint_as_float(u >> 31 ? u & ~15u : u | 15u));
 }
 
-constexpr int kShown = kK * 8;                // largest logits of the groups of kK parts of 128 words
-constexpr int kPool = kK + kK * 16;           // ... and after groups are opened
-constexpr int kPoolPer = (kPool + kThreads - 1) / kThreads;
+constexpr int kList = 512;           // of threads, then parts, that may hold alternatives
+constexpr int kShown = kK * 8;       // largest logits of the groups of kK parts of 128 words
+constexpr int kPool = kK + kK * 16;  // ... and after groups are opened
 
-// Statistics, and alternatives from the parts' groups.  PER: parts a thread.
-template <int ESIZE, int PER>
+// Statistics, and alternatives from the parts' groups.
+template <int ESIZE>
 __global__ __launch_bounds__(kThreads) void probs_groups_kernel(HeadProbsArgs a) {
     __shared__ Joins red;
-    __shared__ uint64_t pool[kPool], keys[kK], sorted[kK];
-    __shared__ uint32_t open[kK];
+    __shared__ uint32_t orders[kPool], places[kPool];
+    __shared__ uint64_t keys[kList], sorted[kK];
+    __shared__ uint32_t list[kThreads], open[kK];
     __shared__ int taken, opened;
-    static_assert(kShown <= kPool, "the groups' logits fit");
-    const int64_t c = blockIdx.x;
+    static_assert(kShown <= kPool && kList <= kPool && kSorted <= kList, "candidates fit");
+    const int64_t c = row_of_block();
+    if (c >= a.tokens) return;
     const int64_t t = a.src[c];
     if (c >= *a.count) {
         idle_row(a, t, threadIdx.x, kThreads);
         return;
     }
-    Parts<PER> p;
-    const Row r = join_parts<PER>(a, c, t, p, red);
+    const Row r = join_parts(a, c, t, orders, red);
     if (!r.fine) {
         write_top(a, t, sorted, 0, r);
         return;
     }
-    int parts = largest<PER>(p.order, [&](int u) { return (uint32_t)(u * kThreads + (int)threadIdx.x); }, a.k, keys, &taken, red);
-    // more parts: the best of those before and the next ones
-    for (int first = PER * kThreads; first < a.parts; first += PER * kThreads - kK) {
-        uint32_t o[PER], at[PER];
-        #pragma unroll
-        for (int u = 0; u < PER; ++u) {
-            const int i = u * kThreads + (int)threadIdx.x, next = first + i - kK;
-            const uint64_t before = i < parts ? keys[i] : 0;
-            const bool in = i >= kK && next < a.parts;
-            o[u] = i < kK ? order_in(before) : in ? order_of(a.part[next * a.t_pad + c].x) : 0;
-            at[u] = i < kK ? place_of(before) : (uint32_t)next;
-        }
-        parts = largest<PER>(o, [&](int u) { return at[u]; }, a.k, keys, &taken, red);
-    }
-    // the logits that those parts' groups show; the K largest
-    const int groups = a.part_rows / 16;
-    for (int i = threadIdx.x; i < parts * groups; i += kThreads) {
-        const uint32_t g = place_of(keys[i / groups]) * groups + i % groups;
-        const float2 x = a.top[g * a.t_pad + c];
-        pool[i] = key_of(order_of(x.x), word_of(g, (int)(__float_as_uint(x.y) & 15u)));
-    }
-    if (threadIdx.x == 0) opened = 0;
-    __syncthreads();
-    int held = largest_keys<kShown / kThreads>(pool, parts * groups, a.k, keys, &taken, red);
-    sort_keys(keys, held, sorted);
-    // Groups that may hide one before the last of them (whose own comes after it; fewer than
-    // K: any that hides one).
-    const uint64_t last = held == a.k ? sorted[held - 1] : 0;
-    for (int i = threadIdx.x; i < (held == a.k ? held - 1 : held); i += kThreads) {
-        const uint32_t g = group_of(place_of(sorted[i]));
-        const uint32_t second = second_order(a.top[g * a.t_pad + c].y);
-        if (key_of(second, word_of(g, 0)) > last) open[atomicAdd(&opened, 1)] = i;  // (in any order: they are sorted again)
-    }
-    __syncthreads();
-    if (opened > 0) {
-        for (int i = threadIdx.x; i < held; i += kThreads) pool[i] = sorted[i];
-        for (int i = threadIdx.x >> 6; i < 4 * opened; i += kWaves) {
-            const uint32_t shown = place_of(sorted[open[i / 4]]), g = group_of(shown);
-            uint32_t word[4], from[4];
-            #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                word[q] = word_of(g, 4 * (i % 4) + q);
-                from[q] = word[q] < a.vocab ? word[q] : shown;
+    places[threadIdx.x] = threadIdx.x;
+    // Of the threads' largest maxima the K largest and some more, of those threads' parts in
+    // the same way (a thread's parts follow one another), of those parts' groups, and of the
+    // words of groups that are opened.  One loop, so that the code is fetched once.
+    enum { kOfThreads, kOfParts, kOfGroups, kOfWords } stage = kOfThreads;
+    const int per = share_of_parts(a), groups = a.part_rows / 16;
+    int n = kThreads, threads = 0, first = 0, held = 0;
+    #pragma unroll 1
+    for (;;) {
+        // (kOfParts: their groups fit the pool, at most 128 of 8 groups and 256 of 2)
+        const int most = stage == kOfThreads ? min(kThreads, max(a.k, 1024 / per))
+                         : stage == kOfParts ? max(a.k, kList / groups) : kSorted;
+        const int got = largest(orders, places, n, a.k, most, keys, &taken, red);
+        if (stage >= kOfGroups) {
+            held = sort_keys(keys, got, a.k, sorted);
+            if (stage == kOfWords) break;
+            // Groups that may hide one before the last of them (whose own comes after it; fewer
+            // than K: any that hides one).
+            const uint64_t last = held == a.k ? sorted[held - 1] : 0;
+            for (int i = threadIdx.x; i < (held == a.k ? held - 1 : held); i += kThreads) {
+                const uint32_t g = group_of(place_of(sorted[i]));
+                const uint32_t second = second_order(a.top[g * a.t_pad + c].y);
+                if (key_of(second, word_of(g, 0)) > last) open[atomicAdd(&opened, 1)] = i;  // (in any order, too)
             }
-            float s[4];
-            dots<ESIZE>(a, t, from, s);
-            if ((threadIdx.x & 63) == 0) {
+            __syncthreads();
+            if (opened == 0) break;
+            for (int i = threadIdx.x; i < held; i += kThreads) {
+                orders[i] = order_in(sorted[i]);
+                places[i] = place_of(sorted[i]);
+            }
+            for (int i = threadIdx.x >> 6; i < 4 * opened; i += kWaves) {
+                const uint32_t shown = place_of(sorted[open[i / 4]]), g = group_of(shown);
+                uint32_t word[4], from[4];
                 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    pool[held + 4 * i + q] = word[q] < a.vocab && word[q] != shown ? key_of(order_of(s[q]), word[q]) : 0;
+                for (int q = 0; q < 4; ++q) {
+                    word[q] = word_of(g, 4 * (i % 4) + q);
+                    from[q] = word[q] < a.vocab ? word[q] : shown;
+                }
+                float s[4];
+                dots<ESIZE>(a, t, from, s);
+                if ((threadIdx.x & 63) == 0) {
+                    #pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int at = held + 4 * i + q;
+                        orders[at] = word[q] < a.vocab && word[q] != shown ? order_of(s[q]) : 0;
+                        places[at] = word[q];
+                    }
+                }
             }
+            n = held + 16 * opened;
+            stage = kOfWords;
+            continue;
         }
-        __syncthreads();
-        held = largest_keys<kPoolPer>(pool, held + 16 * opened, a.k, keys, &taken, red);
-        sort_keys(keys, held, sorted);
+        int parts = got;
+        if (stage == kOfThreads) {
+            for (int i = threadIdx.x; i < got; i += kThreads) list[i] = place_of(keys[i]);
+            if (threadIdx.x == 0) opened = 0;
+            __syncthreads();
+            threads = got;
+            parts = 0;
+            stage = kOfParts;
+        }
+        if (first < threads * per) {
+            // (more than the pool holds: the best of those before and the next ones)
+            const int next = min(threads * per - first, kPool - parts);
+            for (int i = threadIdx.x; i < parts + next; i += kThreads) {
+                const int at = first + i - parts;
+                const int part = i < parts ? (int)place_of(keys[i]) : (int)list[at / per] * per + at % per;
+                orders[i] = i < parts ? order_in(keys[i]) : part < a.parts ? order_of(a.part[part * a.t_pad + c].x) : 0;
+                places[i] = (uint32_t)part;
+            }
+            first += next;
+            n = parts + next;
+            continue;
+        }
+        // what those parts' groups show
+        for (int i = threadIdx.x; i < parts * groups; i += kThreads) {
+            const uint32_t g = place_of(keys[i / groups]) * groups + i % groups;
+            const float2 x = a.top[g * a.t_pad + c];
+            orders[i] = order_of(x.x);
+            places[i] = word_of(g, (int)(__float_as_uint(x.y) & 15u));
+        }
+        n = parts * groups;
+        stage = kOfGroups;
     }
     write_top(a, t, sorted, held, r);
-}
-
-template <int ESIZE>
-void launch_groups(const HeadProbsArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)a.tokens), block(kThreads);
-    if (a.parts <= 4 * kThreads) hipLaunchKernelGGL((probs_groups_kernel<ESIZE, 4>), grid, block, 0, stream, a);
-    else if (a.parts <= 8 * kThreads) hipLaunchKernelGGL((probs_groups_kernel<ESIZE, 8>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((probs_groups_kernel<ESIZE, 24>), grid, block, 0, stream, a);
 }
 
 }  // namespace
 
 hipError_t launch_head_probs(const HeadProbsArgs& a, hipStream_t stream) {
-    const dim3 block(kThreads);
+    const dim3 block(kThreads), rows((unsigned)((a.tokens + 7) / 8 * 8));
     if (a.k == 0) {
         // (8192 rows of 1002 parts: 169 us a block a row)
         if (a.tokens > 1024)
             hipLaunchKernelGGL(probs_join_kernel, dim3((unsigned)((a.tokens + kJoinRows - 1) / kJoinRows)), block, 0, stream, a);
         else
-            hipLaunchKernelGGL(probs_row_kernel, dim3((unsigned)a.tokens), block, 0, stream, a);
-    } else if (a.logits != nullptr) {
-        hipLaunchKernelGGL(probs_logits_kernel, dim3((unsigned)a.tokens), block, 0, stream, a);
-    } else if (a.esize == 2) {
-        launch_groups<2>(a, stream);
+            hipLaunchKernelGGL(probs_row_kernel, rows, block, 0, stream, a);
     } else {
-        launch_groups<4>(a, stream);
+        if (a.logits != nullptr) hipLaunchKernelGGL(probs_logits_kernel, rows, block, 0, stream, a);
+        else if (a.esize == 2) hipLaunchKernelGGL((probs_groups_kernel<2>), rows, block, 0, stream, a);
+        else hipLaunchKernelGGL((probs_groups_kernel<4>), rows, block, 0, stream, a);
     }
     return hipGetLastError();
 }
