@@ -57,8 +57,12 @@ struct HeadGemmArgs {
     float* target_logit;
     float* logits;               // Lse: the logits too (row stride logits_ld), or null
     int32_t logits_ld;
-    float* part_e;               // Probs: sum of p log2 p' per part (p' relative to the part's largest)
-    float2* top;                 // Top: top[group * t_pad + row], see k_head_probs.hip
+    // Probs, Top: part i of a row at part[i * part_step + row * row_step], and likewise ...
+    int64_t part_step, row_step;
+    float* part_e;               // ... its sum of p log2 p (p relative to the part's largest)
+    float2* top;                 // Top: what group i of a row shows, at top[i * part_step + row * top_row]
+    int64_t top_row;
+    int32_t rows;                // rows written
     const float* lse;            // per compact row
     const float* cp;             // coefficient of p
     const float* ct;             // coefficient at the target
@@ -170,11 +174,11 @@ struct HeadProbsArgs {
     int32_t k;
     const float* logits;    // of the compact rows, or null:
     int64_t logits_ld;
-    const float2* part;     // statistics of the rows' parts
+    const float2* part;     // statistics of the rows' parts, as the products' launch left them
     const float* part_e;
     int32_t parts;
     int32_t part_rows;      // words of a part
-    int64_t t_pad;
+    int64_t part_step, row_step, top_row;
     const float* target_logit;
     const float2* top;      // k > 0: the parts' groups
     const void* hidden;     // ... and the operands, for words that a group does not show

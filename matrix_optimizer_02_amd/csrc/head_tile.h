@@ -153,6 +153,13 @@ constexpr bool plain_loop(bool scaled) {
     return is_stats(MODE) && !scaled && C::TQ == 256;
 }
 
+// Whether statistics of padding rows are left out (then a wave may have none to store):
+// of few rows, which are stored row by row.
+template <typename C, int MODE>
+constexpr bool skip_padding() {
+    return is_probs(MODE) && C::TQ == 64;
+}
+
 // Writes a finished tile.  acc[i][j][v]: P row wr RW + 32 i + 8 (v / 4) + 4 khalf
 // + v % 4, Q row wc CW + 32 j + lrow.  SCALED: fp32 logits of scaled rows.  PARTS:
 // bf16 parts of the outputs (Grad) or an fp32 output (dW) where 3.
@@ -279,10 +286,15 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
                 e += __shfl_xor(e, 32, 64);
                 asm volatile("" : "+v"(e));  // formed here, or every exponential is kept for it
             }
-            if (khalf == 0) {
-                const int64_t at = ((int64_t)(args.first_tile + t.I) * C::WR + wr) * args.t_pad + row;
-                args.part[at] = make_float2(m, l);
-                if constexpr (is_probs(MODE)) args.part_e[at] = e;
+            const int64_t part = (int64_t)(args.first_tile + t.I) * C::WR + wr;
+            if constexpr (is_probs(MODE)) {
+                if (khalf == 0 && (!skip_padding<C, MODE>() || row < args.rows)) {
+                    const int64_t at = part * args.part_step + row * args.row_step;
+                    args.part[at] = make_float2(m, l);
+                    args.part_e[at] = e;
+                }
+            } else if (khalf == 0) {
+                args.part[part * args.t_pad + row] = make_float2(m, l);
             }
             if constexpr (MODE == kHeadTop) {
                 // Of the lane's 16 words of each block of 32: the largest (the first of equal ones), where
@@ -302,7 +314,9 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
                         m1 = larger ? x : m1;  // (fmaxf would take a quieted copy of every x)
                     }
                     const uint32_t second = (__float_as_uint(m2) & ~15u) | at1;
-                    args.top[(2 * (v_base / 32 + i) + khalf) * args.t_pad + row] = make_float2(m1, __uint_as_float(second));
+                    if (!skip_padding<C, MODE>() || row < args.rows)
+                        args.top[(2 * (v_base / 32 + i) + khalf) * args.part_step + row * args.top_row] =
+                            make_float2(m1, __uint_as_float(second));
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }

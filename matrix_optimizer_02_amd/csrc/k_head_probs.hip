@@ -27,7 +27,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kK = kHeadMaxAlternatives;
-constexpr int kSorted = kK;  // candidates that are sorted, at most
 
 __device__ __forceinline__ float nan_f() { return __uint_as_float(0x7fc00000u); }
 
@@ -217,15 +216,15 @@ __device__ __forceinline__ int share_of_parts(const HeadProbsArgs& a) { return (
 __device__ __forceinline__ Row join_parts(const HeadProbsArgs& a, int64_t c, int64_t t, uint32_t* orders, Joins& red) {
     const int per = share_of_parts(a), first = (int)threadIdx.x * per;
     const int mine = max(0, min(per, a.parts - first));
-    const float2* const part = a.part + (int64_t)first * a.t_pad + c;
-    const float* const part_e = a.part_e + (int64_t)first * a.t_pad + c;
+    const float2* const part = a.part + first * a.part_step + c * a.row_step;
+    const float* const part_e = a.part_e + first * a.part_step + c * a.row_step;
     constexpr int kAhead = 8;  // loads on their way at once; the first ones' results are kept
     float2 x[kAhead];
     float y[kAhead];
     #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-        x[u] = u < mine ? part[u * a.t_pad] : make_float2(-INFINITY, 0.f);
-        y[u] = u < mine ? part_e[u * a.t_pad] : 0.f;
+        x[u] = u < mine ? part[u * a.part_step] : make_float2(-INFINITY, 0.f);
+        y[u] = u < mine ? part_e[u * a.part_step] : 0.f;
     }
     float m = -INFINITY;
     #pragma unroll
@@ -234,7 +233,7 @@ __device__ __forceinline__ Row join_parts(const HeadProbsArgs& a, int64_t c, int
     for (int i = kAhead; i < mine; i += kAhead) {
         float z[kAhead];
         #pragma unroll
-        for (int u = 0; u < kAhead; ++u) z[u] = part[min(i + u, mine - 1) * a.t_pad].x;
+        for (int u = 0; u < kAhead; ++u) z[u] = part[min(i + u, mine - 1) * a.part_step].x;
         #pragma unroll
         for (int u = 0; u < kAhead; ++u) m = fmaxf(m, z[u]);
     }
@@ -251,8 +250,8 @@ __device__ __forceinline__ Row join_parts(const HeadProbsArgs& a, int64_t c, int
         #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int at = min(i + u, mine - 1);
-            x[u] = part[at * a.t_pad];
-            y[u] = part_e[at * a.t_pad];
+            x[u] = part[at * a.part_step];
+            y[u] = part_e[at * a.part_step];
         }
     }
     l = block_add(l, red);
@@ -275,11 +274,11 @@ __global__ __launch_bounds__(kThreads) void probs_join_kernel(HeadProbsArgs a) {
         idle_row(a, t, g, 16);
         return;
     }
-    const float2* const part = a.part + c;
-    const float* const part_e = a.part_e + c;
+    const float2* const part = a.part + c * a.row_step;
+    const float* const part_e = a.part_e + c * a.row_step;
     float m = -INFINITY;
     #pragma unroll 8
-    for (int i = g; i < a.parts; i += 16) m = fmaxf(m, part[i * a.t_pad].x);
+    for (int i = g; i < a.parts; i += 16) m = fmaxf(m, part[i * a.part_step].x);
     #pragma unroll
     for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 16));
     const int per = share_of_parts(a);
@@ -291,7 +290,7 @@ __global__ __launch_bounds__(kThreads) void probs_join_kernel(HeadProbsArgs a) {
             #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 const int i = (64 * w + 16 * b + g) * per + j;
-                if (i < a.parts) add_part(a, m, part[i * a.t_pad], part_e[i * a.t_pad], pl[b], pe[b]);
+                if (i < a.parts) add_part(a, m, part[i * a.part_step], part_e[i * a.part_step], pl[b], pe[b]);
             }
         }
         l[w] = (pl[0] + pl[2]) + (pl[1] + pl[3]);
@@ -329,7 +328,7 @@ constexpr int kKept = 64 * kK;
 __global__ __launch_bounds__(kThreads) void probs_logits_kernel(HeadProbsArgs a) {
     __shared__ Joins red;
     __shared__ uint32_t orders[kKept];
-    __shared__ uint64_t keys[kSorted], sorted[kK];
+    __shared__ uint64_t keys[kK], sorted[kK];
     __shared__ int taken;
     const int64_t c = row_of_block();
     if (c >= a.tokens) return;
@@ -345,7 +344,7 @@ __global__ __launch_bounds__(kThreads) void probs_logits_kernel(HeadProbsArgs a)
         const int n = (int)a.vocab;  // at most kKept (head_layout.cpp)
         #pragma unroll 8
         for (int i = threadIdx.x; i < n; i += kThreads) orders[i] = order_of(row[i]);
-        held = sort_keys(keys, largest<true>(orders, nullptr, n, a.k, kSorted, keys, &taken, red), a.k, sorted);
+        held = sort_keys(keys, largest<true>(orders, nullptr, n, a.k, kK, keys, &taken, red), a.k, sorted);
     }
     write_top(a, t, sorted, held, r);
 }
@@ -417,8 +416,7 @@ __device__ __forceinline__ uint32_t second_order(float shown) {
 }
 
 constexpr int kList = 512;           // of threads, then parts, that may hold alternatives
-constexpr int kShown = kK * 8;       // largest logits of the groups of kK parts of 128 words
-constexpr int kPool = kK + kK * 16;  // ... and after groups are opened
+constexpr int kPool = kK + kK * 16;  // candidates after groups are opened
 
 // Statistics, and alternatives from the parts' groups.
 template <int ESIZE>
@@ -428,7 +426,7 @@ __global__ __launch_bounds__(kThreads) void probs_groups_kernel(HeadProbsArgs a)
     __shared__ uint64_t keys[kList], sorted[kK];
     __shared__ uint32_t list[kThreads], open[kK];
     __shared__ int taken, opened;
-    static_assert(kShown <= kPool && kList <= kPool && kSorted <= kList, "candidates fit");
+    static_assert(kK * 8 <= kPool && kK <= kPool / 8, "the groups of kK parts of 128 words fit");
     const int64_t c = row_of_block();
     if (c >= a.tokens) return;
     const int64_t t = a.src[c];
@@ -442,17 +440,17 @@ __global__ __launch_bounds__(kThreads) void probs_groups_kernel(HeadProbsArgs a)
         return;
     }
     places[threadIdx.x] = threadIdx.x;
-    // Of the threads' largest maxima the K largest and some more, of those threads' parts in
-    // the same way (a thread's parts follow one another), of those parts' groups, and of the
-    // words of groups that are opened.  One loop, so that the code is fetched once.
+    // Of the threads' largest maxima the K largest and as many more as the next round holds, of
+    // those threads' parts in the same way (a thread's parts follow one another), of those
+    // parts' groups, and of the words of groups that are opened.  One loop, so that the code is
+    // fetched once.
     enum { kOfThreads, kOfParts, kOfGroups, kOfWords } stage = kOfThreads;
     const int per = share_of_parts(a), groups = a.part_rows / 16;
     int n = kThreads, threads = 0, first = 0, held = 0;
     #pragma unroll 1
     for (;;) {
-        // (kOfParts: their groups fit the pool, at most 128 of 8 groups and 256 of 2)
-        const int most = stage == kOfThreads ? min(kThreads, max(a.k, 1024 / per))
-                         : stage == kOfParts ? max(a.k, kList / groups) : kSorted;
+        const int most = stage == kOfThreads ? min(kThreads, max(a.k, kPool / per))
+                         : stage == kOfParts ? min(kList, kPool / groups) : kK;
         const int got = largest(orders, places, n, a.k, most, keys, &taken, red);
         if (stage >= kOfGroups) {
             held = sort_keys(keys, got, a.k, sorted);
@@ -462,7 +460,7 @@ __global__ __launch_bounds__(kThreads) void probs_groups_kernel(HeadProbsArgs a)
             const uint64_t last = held == a.k ? sorted[held - 1] : 0;
             for (int i = threadIdx.x; i < (held == a.k ? held - 1 : held); i += kThreads) {
                 const uint32_t g = group_of(place_of(sorted[i]));
-                const uint32_t second = second_order(a.top[g * a.t_pad + c].y);
+                const uint32_t second = second_order(a.top[g * a.part_step + c * a.top_row].y);
                 if (key_of(second, word_of(g, 0)) > last) open[atomicAdd(&opened, 1)] = i;  // (in any order, too)
             }
             __syncthreads();
@@ -509,7 +507,7 @@ __global__ __launch_bounds__(kThreads) void probs_groups_kernel(HeadProbsArgs a)
             for (int i = threadIdx.x; i < parts + next; i += kThreads) {
                 const int at = first + i - parts;
                 const int part = i < parts ? (int)place_of(keys[i]) : (int)list[at / per] * per + at % per;
-                orders[i] = i < parts ? order_in(keys[i]) : part < a.parts ? order_of(a.part[part * a.t_pad + c].x) : 0;
+                orders[i] = i < parts ? order_in(keys[i]) : part < a.parts ? order_of(a.part[part * a.part_step + c * a.row_step].x) : 0;
                 places[i] = (uint32_t)part;
             }
             first += next;
@@ -519,7 +517,7 @@ __global__ __launch_bounds__(kThreads) void probs_groups_kernel(HeadProbsArgs a)
         // what those parts' groups show
         for (int i = threadIdx.x; i < parts * groups; i += kThreads) {
             const uint32_t g = place_of(keys[i / groups]) * groups + i % groups;
-            const float2 x = a.top[g * a.t_pad + c];
+            const float2 x = a.top[g * a.part_step + c * a.top_row];
             orders[i] = order_of(x.x);
             places[i] = word_of(g, (int)(__float_as_uint(x.y) & 15u));
         }
