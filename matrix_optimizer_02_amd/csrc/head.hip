@@ -347,9 +347,8 @@ dmuon_status probs_chunk_forward(const Call& c, const Probs& o) {
         a.target_logit = v.target_logit();
         if (P.keep_logits) a.logits = v.at<float>(P.off_logits);
         a.logits_ld = (int32_t)round_up(L.vocab, kHeadTile);
-        a.part_step = P.part_step;
-        a.row_step = P.row_step;
-        a.top_row = P.top_row;
+        a.row_parts = P.row_parts;
+        a.row_groups = P.row_groups;
         a.rows = (int32_t)L.tokens;
         a.part_e = v.at<float>(P.off_part_e);
         a.top = v.at<float2>(P.off_top);
@@ -371,9 +370,8 @@ dmuon_status probs_chunk_forward(const Call& c, const Probs& o) {
     r.part_e = v.at<float>(P.off_part_e);
     r.parts = (int32_t)ceil_div(L.vocab, L.s_tile.tp) * wave_rows;
     r.part_rows = L.s_tile.tp / wave_rows;
-    r.part_step = P.part_step;
-    r.row_step = P.row_step;
-    r.top_row = P.top_row;
+    r.row_parts = P.row_parts;
+    r.row_groups = P.row_groups;
     r.target_logit = v.target_logit();
     r.top = v.at<float2>(P.off_top);
     r.hidden = c.hidden;
@@ -456,7 +454,7 @@ dmuon_status backward(const Call& c, const Upstream& u, void* grad_hidden, void*
     if (distill) b.add(u.student, 4 * d.tokens * d.top_k, false);
     if (grad_hidden != nullptr) b.add(grad_hidden, d.tokens * d.hidden * e, true);
     if (grad_weight != nullptr) b.add(grad_weight, d.vocab * d.hidden * e, true);
-    const ProbsLayout P = probs ? probs_layout_of(d, true) : ProbsLayout{head_layout_of(d, true), 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    const ProbsLayout P = probs ? probs_layout_of(d, true) : ProbsLayout{head_layout_of(d, true), 0, 0, 0, 0, 0, 0, 0, 0};
     const HeadLayout& L = P.head;
     if (d.tokens == 0) {
         if (!b.good()) return DMUON_ERR_INVALID_ARG;

@@ -57,12 +57,11 @@ struct HeadGemmArgs {
     float* target_logit;
     float* logits;               // Lse: the logits too (row stride logits_ld), or null
     int32_t logits_ld;
-    // Probs, Top: part i of a row at part[i * part_step + row * row_step], and likewise ...
-    int64_t part_step, row_step;
-    float* part_e;               // ... its sum of p log2 p (p relative to the part's largest)
-    float2* top;                 // Top: what group i of a row shows, at top[i * part_step + row * top_row]
-    int64_t top_row;
-    int32_t rows;                // rows written
+    int64_t row_parts;           // Probs, Top: part[row * row_parts + i] instead, and likewise ...
+    float* part_e;               // ... the part's sum of p log2 p (p relative to its largest)
+    float2* top;                 // Top: what group i of a row shows, top[row * row_groups + i]
+    int64_t row_groups;
+    int32_t rows;                // rows of padding may be left out from this one on
     const float* lse;            // per compact row
     const float* cp;             // coefficient of p
     const float* ct;             // coefficient at the target
@@ -178,7 +177,7 @@ struct HeadProbsArgs {
     const float* part_e;
     int32_t parts;
     int32_t part_rows;      // words of a part
-    int64_t part_step, row_step, top_row;
+    int64_t row_parts, row_groups;
     const float* target_logit;
     const float2* top;      // k > 0: the parts' groups
     const void* hidden;     // ... and the operands, for words that a group does not show

@@ -16,7 +16,6 @@ constexpr int64_t kPieceBytes = int64_t(256) << 20;
 constexpr int64_t kLowTokens = 128;
 // Bytes that a forward call of the log probabilities holds for its alternatives.
 constexpr int64_t kProbsBytes = int64_t(1) << 30;
-constexpr int64_t kRowParts = 64;  // tokens
 constexpr int64_t kPieceMin = 8192;  // vocab rows: fewer would leave dW's launch short of tiles
 
 // Tiles with the time a workgroup takes for 64 of K, in microseconds, when it has
@@ -232,14 +231,10 @@ ProbsLayout probs_layout_of(const dmuon_head_desc& d, bool backward) {
     if (backward) {
         L.off_ce = take(4 * t_pad);
     } else {
-        const int64_t parts = (v_pad / s.tp) * head_wave_rows(s.tp, s.tq);
-        // A wave's rows side by side are written in whole lines; of few rows, whose workgroups
-        // have the chip to themselves and wait for every line, each one's parts lie together.
-        const bool by_row = d.tokens <= kRowParts;
-        L.part_step = by_row ? 1 : t_pad;
-        L.row_step = by_row ? parts : 1;
-        L.top_row = by_row ? v_pad / 16 : 1;
-        L.off_part_e = take(4 * parts * t_pad);
+        // a row's parts and groups lie together: one workgroup reads them
+        L.row_parts = (v_pad / s.tp) * head_wave_rows(s.tp, s.tq);
+        L.row_groups = v_pad / 16;
+        L.off_part_e = take(4 * L.row_parts * t_pad);
         if (L.keep_logits) L.off_logits = take(4 * t_pad * v_pad);
         else if (d.top_k > 0) L.off_top = take(v_pad / 2 * t_pad);
     }

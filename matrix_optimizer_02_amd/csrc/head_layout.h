@@ -86,7 +86,7 @@ HeadLayout head_layout_of(dmuon_head_desc d, bool backward);
 struct ProbsLayout {
     HeadLayout head;
     int32_t keep_logits;  // forward: the logits lie in memory
-    int64_t part_step, row_step, top_row;  // strides of the rows' parts and groups
+    int64_t row_parts, row_groups;  // of a row (row_parts even: pairs of groups are 16-byte aligned)
     size_t off_logits;
     size_t off_part_e;    // forward otherwise: sums for the entropy, the groups' largest
     size_t off_top;

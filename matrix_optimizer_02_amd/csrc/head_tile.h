@@ -289,7 +289,7 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
             const int64_t part = (int64_t)(args.first_tile + t.I) * C::WR + wr;
             if constexpr (is_probs(MODE)) {
                 if (khalf == 0 && (!skip_padding<C, MODE>() || row < args.rows)) {
-                    const int64_t at = part * args.part_step + row * args.row_step;
+                    const int64_t at = row * args.row_parts + part;
                     args.part[at] = make_float2(m, l);
                     args.part_e[at] = e;
                 }
@@ -301,6 +301,7 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
                 // it is, and the second.  Where the second is among a row's alternatives, the others
                 // are formed again (k_head_probs.hip): four instructions a logit here, where keeping
                 // two with their places took seven.
+                float shown[2 * C::FI];
                 #pragma unroll
                 for (int i = 0; i < C::FI; ++i) {
                     float m1 = -INFINITY, m2 = -INFINITY;
@@ -313,11 +314,21 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
                         m2 = __builtin_amdgcn_fmed3f(m1, m2, x);
                         m1 = larger ? x : m1;  // (fmaxf would take a quieted copy of every x)
                     }
-                    const uint32_t second = (__float_as_uint(m2) & ~15u) | at1;
-                    if (!skip_padding<C, MODE>() || row < args.rows)
-                        args.top[(2 * (v_base / 32 + i) + khalf) * args.part_step + row * args.top_row] =
-                            make_float2(m1, __uint_as_float(second));
+                    shown[2 * i] = m1;
+                    shown[2 * i + 1] = __uint_as_float((__float_as_uint(m2) & ~15u) | at1);
                     __builtin_amdgcn_sched_barrier(0);
+                }
+                if (!skip_padding<C, MODE>() || row < args.rows) {
+                    float* const out = reinterpret_cast<float*>(args.top + row * args.row_groups +
+                                                                part * (2 * C::FI) + khalf * C::FI);
+                    if constexpr (C::FI == 1) {
+                        *reinterpret_cast<float2*>(out) = make_float2(shown[0], shown[1]);
+                    } else {
+                        #pragma unroll
+                        for (int i = 0; i < C::FI; i += 2)
+                            *reinterpret_cast<float4*>(out + 2 * i) =
+                                make_float4(shown[2 * i], shown[2 * i + 1], shown[2 * i + 2], shown[2 * i + 3]);
+                    }
                 }
             }
         }

@@ -2,11 +2,11 @@
 // token joins the statistics that the logits' products left, and finds the
 // alternatives.
 //
-// A part is the words whose softmax statistics one wave formed (32 to 128 of them,
-// one after the other); a group is 16 words of one lane: of the block of 32 words
-// b, group 2 b + h holds words 32 b + 8 q + 4 h + r (q, r < 4) as its elements
-// 4 q + r, so a group's elements are in the order of their ids.  Of each group the
-// products' epilogue shows the largest logit, its place and the size of the second.
+// A part is the words whose softmax statistics one wave formed: 32 F of them, one after
+// the other (F 1, 2 or 4).  A group is 16 words of one lane: group h F + i of a part (h <
+// 2, i < F) holds its words 32 i + 8 q + 4 h + r (q, r < 4) as its elements 4 q + r,
+// in the order of their ids.  Of each group the products' epilogue shows the largest logit,
+// its place and the size of the second.
 //
 // The K alternatives lie in the K parts with the largest maxima (equal maxima: the
 // earlier part): were one in another part, each of those K parts would hold a word
@@ -77,32 +77,36 @@ __device__ __forceinline__ float block_add(float v, Joins& red) {
     return (red.f[0] + red.f[1]) + (red.f[2] + red.f[3]);
 }
 
-// At least the k largest and at most `most` (>= k) of n values in LDS (orders o, 0 where
-// there is none; at places p, or INDEX: at their own), equal ones by the lower place, in any order; returns their
-// number (fewer than k where there are not as many).  Counting how many reach a threshold,
-// two bits of it a round: a few rounds leave few enough of them.
-template <bool INDEX = false>
+// At least the k largest and at most `most` (>= k) of n values in LDS (n <= PER kThreads;
+// orders o, 0 where there is none; at places p, or INDEX: at their own), equal ones by the
+// lower place, in any order; returns their number (fewer than k where there are not as
+// many).  Counting how many reach a threshold, two bits of it a round: a few rounds leave few
+// enough of them.  Then, of too many that equal the threshold, the same with their places,
+// from the last on.
+template <int PER, bool INDEX = false>
 __device__ __forceinline__ int largest(const uint32_t* o, const uint32_t* p, int n, int k, int most, uint64_t* out,
                                        int* taken, Joins& red) {
-    int turn = 0;
-    // how many of the values are at least a, b and c: of all, or of the places (from the
-    // last on) of those that equal `only`
-    auto count = [&](uint32_t only, uint32_t a, uint32_t b, uint32_t c) {
+    __syncthreads();  // the values are there, and the last call's number has been read
+    if (threadIdx.x == 0) *taken = 0;
+    uint32_t x[PER];
+    #pragma unroll
+    for (int u = 0; u < PER; ++u) {
+        const int i = u * kThreads + (int)threadIdx.x;
+        x[u] = i < n ? o[i] : 0;
+    }
+    uint32_t least = 0, low = 0, at = 0;
+    int reach = n, above = 0, bit = 30, turn = 0;
+    enum { kOrders, kAbove, kPlaces } pass = kOrders;
+    #pragma unroll 1
+    while (reach > most) {
+        // thresholds of this round (no order is the largest integer)
+        const uint32_t a = pass == kAbove ? least + 1 : at | 1u << bit, b = at | 2u << bit, c = at | 3u << bit;
         int4 s = make_int4(0, 0, 0, 0);
-        for (int i0 = 0; i0 < n; i0 += 4 * kThreads) {
-            uint32_t x[4];
-            #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int i = i0 + q * kThreads + (int)threadIdx.x;
-                x[q] = i < n ? o[i] : 0;
-                if (only != 0) x[q] = i < n && x[q] == only ? ~(INDEX ? (uint32_t)i : p[i]) : 0;
-            }
-            #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                s.x += __popcll(__builtin_amdgcn_ballot_w64(x[q] >= a));
-                s.y += __popcll(__builtin_amdgcn_ballot_w64(x[q] >= b));
-                s.z += __popcll(__builtin_amdgcn_ballot_w64(x[q] >= c));
-            }
+        #pragma unroll
+        for (int u = 0; u < PER; ++u) {
+            s.x += __popcll(__builtin_amdgcn_ballot_w64(x[u] >= a));
+            s.y += __popcll(__builtin_amdgcn_ballot_w64(x[u] >= b));
+            s.z += __popcll(__builtin_amdgcn_ballot_w64(x[u] >= c));
         }
         turn ^= 1;  // (the counts of the round before may still be read)
         if ((threadIdx.x & 63) == 0) red.counts[turn][threadIdx.x >> 6] = s;
@@ -113,33 +117,33 @@ __device__ __forceinline__ int largest(const uint32_t* o, const uint32_t* p, int
             const int4 m = red.counts[turn][w];
             s.x += m.x, s.y += m.y, s.z += m.z;
         }
-        return s;
-    };
-    __syncthreads();  // (the last call's number has been read)
-    if (threadIdx.x == 0) *taken = 0;
-    __syncthreads();
-    // The largest threshold that k values reach; then, of too many that equal it, the one of
-    // their places.
-    uint32_t least = 0, low = 0;
-    int reach = n;  // values at the threshold, or more than there are
-    #pragma unroll 1
-    for (int pass = 0; pass < 2 && reach > most; ++pass) {
-        uint32_t& at = pass == 0 ? least : low;
-        const int above = pass == 0 ? 0 : count(0, least + 1, 1u, 1u).x;  // (no order is the largest integer)
-        #pragma unroll 1
-        for (int bit = 30; bit >= 0 && reach > most; bit -= 2) {
-            const uint32_t a = at | 1u << bit, b = at | 2u << bit, c = at | 3u << bit;
-            const int4 s = count(pass == 0 ? 0 : least, a, b, c);
-            if (above + s.z >= k) at = c, reach = above + s.z;
-            else if (above + s.y >= k) at = b, reach = above + s.y;
-            else if (above + s.x >= k) at = a, reach = above + s.x;
+        if (pass == kAbove) {
+            above = s.x;
+            #pragma unroll
+            for (int u = 0; u < PER; ++u) {
+                const int i = u * kThreads + (int)threadIdx.x;
+                x[u] = x[u] == least ? ~(INDEX ? (uint32_t)i : p[i]) : 0;  // (least > 0: i < n)
+            }
+            pass = kPlaces;
+            at = 0;
+            bit = 30;
+            continue;
         }
-        if (least == 0) break;  // fewer than k: all of them
+        if (above + s.z >= k) at = c, reach = above + s.z;
+        else if (above + s.y >= k) at = b, reach = above + s.y;
+        else if (above + s.x >= k) at = a, reach = above + s.x;
+        (pass == kOrders ? least : low) = at;
+        bit -= 2;
+        if (bit < 0) {
+            if (least == 0 || pass == kPlaces) break;  // (fewer than k: all of them)
+            pass = kAbove;
+        }
     }
+    __syncthreads();
     for (int i = threadIdx.x; i < n; i += kThreads) {
-        const uint32_t x = o[i], place = INDEX ? (uint32_t)i : p[i];
-        if (x != 0 && (x > least || (x == least && ~place >= low)))
-            out[atomicAdd(taken, 1)] = key_of(x, place);  // (places in a list that is sorted)
+        const uint32_t y = o[i], place = INDEX ? (uint32_t)i : p[i];
+        if (y != 0 && (y > least || (y == least && ~place >= low)))
+            out[atomicAdd(taken, 1)] = key_of(y, place);  // (places in a list that is sorted)
     }
     __syncthreads();
     return *taken;
@@ -150,7 +154,7 @@ __device__ __forceinline__ int sort_keys(const uint64_t* keys, int n, int k, uin
     for (int i = threadIdx.x; i < n; i += kThreads) {
         const uint64_t mine = keys[i];
         int rank = 0;
-        #pragma unroll 4
+        #pragma unroll 16
         for (int j = 0; j < n; ++j) rank += keys[j] > mine ? 1 : 0;
         if (rank < k) sorted[rank] = mine;
     }
@@ -216,15 +220,15 @@ __device__ __forceinline__ int share_of_parts(const HeadProbsArgs& a) { return (
 __device__ __forceinline__ Row join_parts(const HeadProbsArgs& a, int64_t c, int64_t t, uint32_t* orders, Joins& red) {
     const int per = share_of_parts(a), first = (int)threadIdx.x * per;
     const int mine = max(0, min(per, a.parts - first));
-    const float2* const part = a.part + first * a.part_step + c * a.row_step;
-    const float* const part_e = a.part_e + first * a.part_step + c * a.row_step;
+    const float2* const part = a.part + c * a.row_parts + first;
+    const float* const part_e = a.part_e + c * a.row_parts + first;
     constexpr int kAhead = 8;  // loads on their way at once; the first ones' results are kept
     float2 x[kAhead];
     float y[kAhead];
     #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-        x[u] = u < mine ? part[u * a.part_step] : make_float2(-INFINITY, 0.f);
-        y[u] = u < mine ? part_e[u * a.part_step] : 0.f;
+        x[u] = u < mine ? part[u] : make_float2(-INFINITY, 0.f);
+        y[u] = u < mine ? part_e[u] : 0.f;
     }
     float m = -INFINITY;
     #pragma unroll
@@ -233,7 +237,7 @@ __device__ __forceinline__ Row join_parts(const HeadProbsArgs& a, int64_t c, int
     for (int i = kAhead; i < mine; i += kAhead) {
         float z[kAhead];
         #pragma unroll
-        for (int u = 0; u < kAhead; ++u) z[u] = part[min(i + u, mine - 1) * a.part_step].x;
+        for (int u = 0; u < kAhead; ++u) z[u] = part[min(i + u, mine - 1)].x;
         #pragma unroll
         for (int u = 0; u < kAhead; ++u) m = fmaxf(m, z[u]);
     }
@@ -250,8 +254,8 @@ __device__ __forceinline__ Row join_parts(const HeadProbsArgs& a, int64_t c, int
         #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int at = min(i + u, mine - 1);
-            x[u] = part[at * a.part_step];
-            y[u] = part_e[at * a.part_step];
+            x[u] = part[at];
+            y[u] = part_e[at];
         }
     }
     l = block_add(l, red);
@@ -259,68 +263,51 @@ __device__ __forceinline__ Row join_parts(const HeadProbsArgs& a, int64_t c, int
     return row_of(a, c, t, m, l, e, threadIdx.x == 0);
 }
 
-// Statistics alone, of many rows: 16 rows by 16 threads a block, so that the rows' parts,
-// which lie side by side, are read in whole lines.  The sums are added as join_parts adds
-// them (a thread stands for 16 of its 256): outputs do not depend on K or on the number
-// of tokens.
-constexpr int kJoinRows = 16;
-__global__ __launch_bounds__(kThreads) void probs_join_kernel(HeadProbsArgs a) {
-    const int n = *a.count;
-    const int r = threadIdx.x / 16, g = threadIdx.x % 16;
-    const int64_t c = (int64_t)blockIdx.x * kJoinRows + r;
-    if (c >= a.tokens) return;
-    const int64_t t = a.src[c];
-    if (c >= n) {
-        idle_row(a, t, g, 16);
-        return;
-    }
-    const float2* const part = a.part + c * a.row_step;
-    const float* const part_e = a.part_e + c * a.row_step;
-    float m = -INFINITY;
-    #pragma unroll 8
-    for (int i = g; i < a.parts; i += 16) m = fmaxf(m, part[i * a.part_step].x);
-    #pragma unroll
-    for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 16));
-    const int per = share_of_parts(a);
-    float l[kWaves], e[kWaves];
-    #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        float pl[4] = {0.f, 0.f, 0.f, 0.f}, pe[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int j = 0; j < per; ++j) {
-            #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const int i = (64 * w + 16 * b + g) * per + j;
-                if (i < a.parts) add_part(a, m, part[i * a.part_step], part_e[i * a.part_step], pl[b], pe[b]);
-            }
-        }
-        l[w] = (pl[0] + pl[2]) + (pl[1] + pl[3]);
-        e[w] = (pe[0] + pe[2]) + (pe[1] + pe[3]);
-        #pragma unroll
-        for (int off = 8; off > 0; off >>= 1) {
-            l[w] += __shfl_xor(l[w], off, 16);
-            e[w] += __shfl_xor(e[w], off, 16);
-        }
-    }
-    row_of(a, c, t, m, (l[0] + l[1]) + (l[2] + l[3]), (e[0] + e[1]) + (e[2] + e[3]), g == 0);
-}
-
-// The row of a block: each XCD takes neighbouring rows, whose parts share lines of its L2.
-__device__ __forceinline__ int64_t row_of_block() {
-    const int64_t each = gridDim.x / 8;
-    return (int64_t)(blockIdx.x % 8) * each + blockIdx.x / 8;
-}
-
 // Statistics alone, of few rows.
 __global__ __launch_bounds__(kThreads) void probs_row_kernel(HeadProbsArgs a) {
     __shared__ Joins red;
-    const int64_t c = row_of_block();
-    if (c >= a.tokens) return;
+    const int64_t c = blockIdx.x;
     const int64_t t = a.src[c];
     if (c >= *a.count) {
         idle_row(a, t, threadIdx.x, kThreads);
         return;
     }
     join_parts(a, c, t, nullptr, red);
+}
+
+// The same of many rows, a wave a row: a lane stands for four threads of join_parts, whose
+// order of summation it keeps (outputs do not depend on K or on the number of tokens).
+// 8192 rows of 1002 parts, us: 31 for 280 a block a row.
+__global__ __launch_bounds__(kThreads) void probs_rows_kernel(HeadProbsArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t c = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+    if (c >= a.tokens) return;
+    const int64_t t = a.src[c];
+    if (c >= *a.count) {
+        idle_row(a, t, lane, 64);
+        return;
+    }
+    const float2* const part = a.part + c * a.row_parts;
+    const float* const part_e = a.part_e + c * a.row_parts;
+    float m = -INFINITY;
+    #pragma unroll 4
+    for (int i = lane; i < a.parts; i += 64) m = fmaxf(m, part[i].x);
+    m = wave_max(m);
+    const int per = share_of_parts(a);
+    float l[kWaves] = {0.f, 0.f, 0.f, 0.f}, e[kWaves] = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < per; ++j) {
+        #pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const int i = (64 * w + lane) * per + j;
+            if (i < a.parts) add_part(a, m, part[i], part_e[i], l[w], e[w]);
+        }
+    }
+    #pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        l[w] = wave_add(l[w]);
+        e[w] = wave_add(e[w]);
+    }
+    row_of(a, c, t, m, (l[0] + l[1]) + (l[2] + l[3]), (e[0] + e[1]) + (e[2] + e[3]), lane == 0);
 }
 
 // Alternatives from the row's kept logits.
@@ -330,8 +317,7 @@ __global__ __launch_bounds__(kThreads) void probs_logits_kernel(HeadProbsArgs a)
     __shared__ uint32_t orders[kKept];
     __shared__ uint64_t keys[kK], sorted[kK];
     __shared__ int taken;
-    const int64_t c = row_of_block();
-    if (c >= a.tokens) return;
+    const int64_t c = blockIdx.x;
     const int64_t t = a.src[c];
     if (c >= *a.count) {
         idle_row(a, t, threadIdx.x, kThreads);
@@ -344,7 +330,7 @@ __global__ __launch_bounds__(kThreads) void probs_logits_kernel(HeadProbsArgs a)
         const int n = (int)a.vocab;  // at most kKept (head_layout.cpp)
         #pragma unroll 8
         for (int i = threadIdx.x; i < n; i += kThreads) orders[i] = order_of(row[i]);
-        held = sort_keys(keys, largest<true>(orders, nullptr, n, a.k, kK, keys, &taken, red), a.k, sorted);
+        held = sort_keys(keys, largest<kKept / kThreads, true>(orders, nullptr, n, a.k, kK, keys, &taken, red), a.k, sorted);
     }
     write_top(a, t, sorted, held, r);
 }
@@ -405,9 +391,14 @@ __device__ __forceinline__ void dots(const HeadProbsArgs& a, int64_t t, const ui
     for (int q = 0; q < 4; ++q) s[q] = wave_add(s[q]);
 }
 
-__device__ __forceinline__ uint32_t group_of(uint32_t word) { return word / 32 * 2 + ((word >> 2) & 1); }
-__device__ __forceinline__ uint32_t word_of(uint32_t group, int at) {
-    return group / 2 * 32 + 8 * (at / 4) + 4 * (group & 1) + at % 4;
+// Groups and their words, for parts of 32 << f words.
+__device__ __forceinline__ uint32_t group_of(uint32_t word, int f) {
+    const uint32_t part = word >> (5 + f), i = (word >> 5) & ((1 << f) - 1), h = (word >> 2) & 1;
+    return (((part << 1) + h) << f) + i;
+}
+__device__ __forceinline__ uint32_t word_of(uint32_t group, int at, int f) {
+    const uint32_t i = group & ((1 << f) - 1), h = (group >> f) & 1, part = group >> (f + 1);
+    return (part << (5 + f)) + 32 * i + 8 * (at / 4) + 4 * h + at % 4;
 }
 // The order of a group's second logit, or up to 15 more: its last four bits hold a place.
 __device__ __forceinline__ uint32_t second_order(float shown) {
@@ -417,6 +408,7 @@ __device__ __forceinline__ uint32_t second_order(float shown) {
 
 constexpr int kList = 512;           // of threads, then parts, that may hold alternatives
 constexpr int kPool = kK + kK * 16;  // candidates after groups are opened
+constexpr int kPoolPer = (kPool + kThreads - 1) / kThreads;
 
 // Statistics, and alternatives from the parts' groups.
 template <int ESIZE>
@@ -427,8 +419,7 @@ __global__ __launch_bounds__(kThreads) void probs_groups_kernel(HeadProbsArgs a)
     __shared__ uint32_t list[kThreads], open[kK];
     __shared__ int taken, opened;
     static_assert(kK * 8 <= kPool && kK <= kPool / 8, "the groups of kK parts of 128 words fit");
-    const int64_t c = row_of_block();
-    if (c >= a.tokens) return;
+    const int64_t c = blockIdx.x;
     const int64_t t = a.src[c];
     if (c >= *a.count) {
         idle_row(a, t, threadIdx.x, kThreads);
@@ -439,19 +430,21 @@ __global__ __launch_bounds__(kThreads) void probs_groups_kernel(HeadProbsArgs a)
         write_top(a, t, sorted, 0, r);
         return;
     }
-    places[threadIdx.x] = threadIdx.x;
     // Of the threads' largest maxima the K largest and as many more as the next round holds, of
     // those threads' parts in the same way (a thread's parts follow one another), of those
     // parts' groups, and of the words of groups that are opened.  One loop, so that the code is
     // fetched once.
     enum { kOfThreads, kOfParts, kOfGroups, kOfWords } stage = kOfThreads;
-    const int per = share_of_parts(a), groups = a.part_rows / 16;
+    places[threadIdx.x] = list[threadIdx.x] = threadIdx.x;
+    const int per = share_of_parts(a), groups = a.part_rows / 16, f = groups / 4;  // (groups 2, 4 or 8)
     int n = kThreads, threads = 0, first = 0, held = 0;
     #pragma unroll 1
     for (;;) {
         const int most = stage == kOfThreads ? min(kThreads, max(a.k, kPool / per))
                          : stage == kOfParts ? min(kList, kPool / groups) : kK;
-        const int got = largest(orders, places, n, a.k, most, keys, &taken, red);
+        // (all threads' parts may fit the next round as they are)
+        const bool all = stage == kOfThreads && kThreads * per <= kPool;
+        const int got = all ? kThreads : largest<kPoolPer>(orders, places, n, a.k, most, keys, &taken, red);
         if (stage >= kOfGroups) {
             held = sort_keys(keys, got, a.k, sorted);
             if (stage == kOfWords) break;
@@ -459,9 +452,9 @@ __global__ __launch_bounds__(kThreads) void probs_groups_kernel(HeadProbsArgs a)
             // than K: any that hides one).
             const uint64_t last = held == a.k ? sorted[held - 1] : 0;
             for (int i = threadIdx.x; i < (held == a.k ? held - 1 : held); i += kThreads) {
-                const uint32_t g = group_of(place_of(sorted[i]));
-                const uint32_t second = second_order(a.top[g * a.part_step + c * a.top_row].y);
-                if (key_of(second, word_of(g, 0)) > last) open[atomicAdd(&opened, 1)] = i;  // (in any order, too)
+                const uint32_t g = group_of(place_of(sorted[i]), f);
+                const uint32_t second = second_order(a.top[c * a.row_groups + g].y);
+                if (key_of(second, word_of(g, 0, f)) > last) open[atomicAdd(&opened, 1)] = i;  // (in any order, too)
             }
             __syncthreads();
             if (opened == 0) break;
@@ -470,11 +463,11 @@ __global__ __launch_bounds__(kThreads) void probs_groups_kernel(HeadProbsArgs a)
                 places[i] = place_of(sorted[i]);
             }
             for (int i = threadIdx.x >> 6; i < 4 * opened; i += kWaves) {
-                const uint32_t shown = place_of(sorted[open[i / 4]]), g = group_of(shown);
+                const uint32_t shown = place_of(sorted[open[i / 4]]), g = group_of(shown, f);
                 uint32_t word[4], from[4];
                 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    word[q] = word_of(g, 4 * (i % 4) + q);
+                    word[q] = word_of(g, 4 * (i % 4) + q, f);
                     from[q] = word[q] < a.vocab ? word[q] : shown;
                 }
                 float s[4];
@@ -494,7 +487,7 @@ __global__ __launch_bounds__(kThreads) void probs_groups_kernel(HeadProbsArgs a)
         }
         int parts = got;
         if (stage == kOfThreads) {
-            for (int i = threadIdx.x; i < got; i += kThreads) list[i] = place_of(keys[i]);
+            if (!all && (int)threadIdx.x < got) list[threadIdx.x] = place_of(keys[threadIdx.x]);
             if (threadIdx.x == 0) opened = 0;
             __syncthreads();
             threads = got;
@@ -507,7 +500,7 @@ __global__ __launch_bounds__(kThreads) void probs_groups_kernel(HeadProbsArgs a)
             for (int i = threadIdx.x; i < parts + next; i += kThreads) {
                 const int at = first + i - parts;
                 const int part = i < parts ? (int)place_of(keys[i]) : (int)list[at / per] * per + at % per;
-                orders[i] = i < parts ? order_in(keys[i]) : part < a.parts ? order_of(a.part[part * a.part_step + c * a.row_step].x) : 0;
+                orders[i] = i < parts ? order_in(keys[i]) : part < a.parts ? order_of(a.part[c * a.row_parts + part].x) : 0;
                 places[i] = (uint32_t)part;
             }
             first += next;
@@ -517,9 +510,9 @@ __global__ __launch_bounds__(kThreads) void probs_groups_kernel(HeadProbsArgs a)
         // what those parts' groups show
         for (int i = threadIdx.x; i < parts * groups; i += kThreads) {
             const uint32_t g = place_of(keys[i / groups]) * groups + i % groups;
-            const float2 x = a.top[g * a.part_step + c * a.top_row];
+            const float2 x = a.top[c * a.row_groups + g];
             orders[i] = order_of(x.x);
-            places[i] = word_of(g, (int)(__float_as_uint(x.y) & 15u));
+            places[i] = word_of(g, (int)(__float_as_uint(x.y) & 15u), f);
         }
         n = parts * groups;
         stage = kOfGroups;
@@ -530,18 +523,13 @@ __global__ __launch_bounds__(kThreads) void probs_groups_kernel(HeadProbsArgs a)
 }  // namespace
 
 hipError_t launch_head_probs(const HeadProbsArgs& a, hipStream_t stream) {
-    const dim3 block(kThreads), rows((unsigned)((a.tokens + 7) / 8 * 8));
-    if (a.k == 0) {
-        // (8192 rows of 1002 parts: 169 us a block a row)
-        if (a.tokens > 1024)
-            hipLaunchKernelGGL(probs_join_kernel, dim3((unsigned)((a.tokens + kJoinRows - 1) / kJoinRows)), block, 0, stream, a);
-        else
-            hipLaunchKernelGGL(probs_row_kernel, rows, block, 0, stream, a);
-    } else {
-        if (a.logits != nullptr) hipLaunchKernelGGL(probs_logits_kernel, rows, block, 0, stream, a);
-        else if (a.esize == 2) hipLaunchKernelGGL((probs_groups_kernel<2>), rows, block, 0, stream, a);
-        else hipLaunchKernelGGL((probs_groups_kernel<4>), rows, block, 0, stream, a);
-    }
+    const dim3 block(kThreads), rows((unsigned)a.tokens);
+    if (a.k == 0 && a.tokens > 256)
+        hipLaunchKernelGGL(probs_rows_kernel, dim3((unsigned)((a.tokens + kWaves - 1) / kWaves)), block, 0, stream, a);
+    else if (a.k == 0) hipLaunchKernelGGL(probs_row_kernel, rows, block, 0, stream, a);
+    else if (a.logits != nullptr) hipLaunchKernelGGL(probs_logits_kernel, rows, block, 0, stream, a);
+    else if (a.esize == 2) hipLaunchKernelGGL((probs_groups_kernel<2>), rows, block, 0, stream, a);
+    else hipLaunchKernelGGL((probs_groups_kernel<4>), rows, block, 0, stream, a);
     return hipGetLastError();
 }
 
