@@ -182,7 +182,7 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
     // Rows are compared as (constant) against (bound - 4 khalf), the lane's part on the one
     // side that is not a constant: 64 row numbers would otherwise be kept in registers.
     // (The plain loop leaves room for them, and is compiled to the shorter code with them.)
-    constexpr bool kRowNumbers = plain_loop<C, MODE>(SCALED) && !is_probs(MODE);
+    constexpr bool kRowNumbers = plain_loop<C, MODE>(SCALED);
     int khalf = lane >> 5;
     if constexpr (!kRowNumbers) asm volatile("" : "+v"(khalf));
     if constexpr (SCALED) {
@@ -269,15 +269,26 @@ __device__ __forceinline__ void write_tile(const HeadGemmArgs& args, const Tile&
             [[maybe_unused]] float es[4] = {0.f, 0.f, 0.f, 0.f};
             #pragma unroll
             for (int i = 0; i < C::FI; ++i) {
-                #pragma unroll
-                for (int v = 0; v < 16; ++v) {
-                    const float x = (acc[i][j][v] - m0) * scale;
-                    const float p = __builtin_amdgcn_exp2f(x);
-                    ls[v & 3] += p;
-                    // (p is 0 long before x is -200, and 0 times the logarithm has to be 0)
-                    if constexpr (is_probs(MODE)) es[v & 3] = fmaf(p, fmaxf(x, -200.f), es[v & 3]);
+                if constexpr (is_probs(MODE)) {
+                    // in three steps: one after the other, each exponential would be waited for
+                    float x[16], p[16];
+                    #pragma unroll
+                    for (int v = 0; v < 16; ++v) x[v] = (acc[i][j][v] - m0) * scale;
+                    __builtin_amdgcn_sched_barrier(0);
+                    #pragma unroll
+                    for (int v = 0; v < 16; ++v) p[v] = __builtin_amdgcn_exp2f(x[v]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    #pragma unroll
+                    for (int v = 0; v < 16; ++v) {
+                        ls[v & 3] += p[v];
+                        // (p is 0 long before x is -200, and 0 times the logarithm has to be 0)
+                        es[v & 3] = fmaf(p[v], fmaxf(x[v], -200.f), es[v & 3]);
+                    }
+                } else {
+                    #pragma unroll
+                    for (int v = 0; v < 16; ++v) ls[v & 3] += __builtin_amdgcn_exp2f((acc[i][j][v] - m0) * scale);
                 }
-                if (!kRowNumbers || is_probs(MODE)) __builtin_amdgcn_sched_barrier(0);  // no more of the differences in registers at once
+                if (!kRowNumbers) __builtin_amdgcn_sched_barrier(0);  // no more of the differences in registers at once
             }
             float l = (ls[0] + ls[1]) + (ls[2] + ls[3]);
             l += __shfl_xor(l, 32, 64);

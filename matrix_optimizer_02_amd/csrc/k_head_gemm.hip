@@ -179,7 +179,9 @@ __global__ __launch_bounds__(C::NT) __attribute__((
     static_assert(TQ % kPieces == 0 && TQ / kPieces % C::CW == 0, "a wave's columns lie in one piece");
     // Stores that every wave issues behind that slab's loads, at least: they need not
     // have completed for the slab to be there.
-    constexpr int kStores = skip_padding<C, MODE>() ? 0 : is_stats(MODE) ? C::FJ
+    constexpr int kStores = skip_padding<C, MODE>() ? 0
+                            : is_probs(MODE) ? C::FJ * (2 + (MODE == kHeadTop ? (C::FI + 1) / 2 : 0))
+                            : MODE == kHeadLse ? C::FJ
                             : is_grad(MODE) && TQ == 256 ? TQ * TP / 8 / C::NT
                             : MODE == kHeadDh ? C::FI * C::FJ * 4 : 0;
     bool behind = false;
