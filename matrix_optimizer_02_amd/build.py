@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libdmuon_ns.so")
 
 HIP_SOURCES = ["api.hip", "clip.hip", "head.hip", "k_adamw.hip", "k_diag.hip", "k_elementwise.hip", "k_gemm_bf16.hip",
                "k_gemm_f32.hip", "k_head_gemm.hip", "k_head_probs.hip", "k_head_rows.hip", "k_head_stream.hip",
-               "k_head_x3.hip", "k_resident.hip", "tune.hip"]
+               "k_head_wide.hip", "k_head_x3.hip", "k_resident.hip", "tune.hip"]
 CXX_SOURCES = ["head_layout.cpp", "plan.cpp"]
 ARCH = "gfx950"
 

@@ -79,6 +79,8 @@ struct HeadGemmArgs {
 };
 
 hipError_t launch_head_gemm(int mode, HeadTile tile, const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream);
+// ... Probs and Top of bf16 operands, 256 x 256 tiles (k_head_wide.hip).
+hipError_t launch_head_wide(int mode, const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream);
 // ... dH and dW of fp32 operands (k_head_x3.hip).
 hipError_t launch_head_x3(int mode, HeadTile tile, const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream);
 // The same with W read in place whatever its width and type (Lse, Grad, dH;

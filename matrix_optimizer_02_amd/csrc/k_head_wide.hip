@@ -1,0 +1,400 @@
+// Tile products of the output head for bf16 operands and work that fills the chip: 256 x
+// 256 tiles by four waves of 128 x 128 (modes Lse, Probs, Top, Grad and GradEntropy of
+// k_head_gemm.hip; the same sums in the same order, the same statistics).
+//
+// Eight waves of 128 x 64 read 192 KB of fragments from LDS for every 64 KB that a slab
+// brings; four of 128 x 128 read 128 KB.  Their 256 accumulators a lane are all of the
+// accumulation registers, which leaves the compiler none to move them about with: they
+// are named here, and the compiler does not know of them.  One wave a SIMD has nobody to
+// cover for it, so everything is issued between its products: a slab's 32 fragments one k-step
+// ahead, its 16 loads spread over three k-steps (all in one they take 10% longer: they
+// fill LDS against the fragments' reads), and its one barrier with a k-step's products on
+// their way and fragments of the next slab behind it.  The sequence of slabs runs on over the
+// tiles' ends, so the next tile's first two slabs load behind the epilogue.
+//
+// What bounds it: the matrix cores with the loads' way into LDS.  8192 tokens, hidden
+// 4096, vocabulary 128256, statistics of softmax and entropy: 6.29 ms, 1368 TFLOP/s,
+// where eight waves take 6.96 to 7.15 on the same cards; 5.4 without its loads, 6.0
+// without its epilogue.  Waiting for the loads costs nothing (6.47 either way with loads
+// in two k-steps); lines touched ahead of them cost 10%.
+#include "head_tile.h"
+
+#include <type_traits>
+#include <utility>
+
+namespace dmuon {
+namespace {
+
+using namespace head;
+
+constexpr int kWT = 256;                      // tile edge
+constexpr int kWThreads = 256;
+constexpr int kHalf = kWT * kRowBytes;        // an operand's slab
+constexpr int kWStage = 2 * kHalf;
+constexpr int kWPiece = 32 * 256;             // 32 token rows of a wave's 128 words, bf16
+
+typedef __attribute__((address_space(3))) const bf16x8 lds_frag;
+__device__ __forceinline__ bf16x8 frag(uint32_t at) { return *reinterpret_cast<lds_frag*>(at); }
+
+template <typename F, int... M>
+__device__ __forceinline__ void each(F&& f, std::integer_sequence<int, M...>) {
+    (f(std::integral_constant<int, M>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+    each(f, std::make_integer_sequence<int, N>{});
+}
+
+// The accumulators are AGPRs that the compiler does not allocate: tuple (i, j) is
+// a[16 (4 i + j)] to the 15 after it.
+template <int N>
+__device__ __forceinline__ void mma(const bf16x8& a, const bf16x8& b) {
+    asm volatile("v_mfma_f32_32x32x16_bf16 a[%2:%3], %0, %1, a[%2:%3]" ::"v"(a), "v"(b), "n"(16 * N), "n"(16 * N + 15));
+}
+template <int N>
+__device__ __forceinline__ void mma_first(const bf16x8& a, const bf16x8& b) {
+    asm volatile("v_mfma_f32_32x32x16_bf16 a[%2:%3], %0, %1, 0" ::"v"(a), "v"(b), "n"(16 * N), "n"(16 * N + 15));
+}
+template <int N>
+__device__ __forceinline__ float acc_at() {
+    float x;
+    asm volatile("v_accvgpr_read_b32 %0, a[%1]" : "=v"(x) : "n"(N));
+    return x;
+}
+
+// dma16 to lds + AT.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+template <int AT>
+__device__ __forceinline__ void dma16_at(const void* base, uint32_t voff, uint32_t lds) {
+    asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(base), "n"(AT)
+                 : "m0", "scc", "memory");
+}
+#pragma clang diagnostic pop
+
+constexpr int kLoads3 = 6, kLoads0 = 6, kLoads1 = 16 - kLoads3 - kLoads0;
+
+template <int MODE>
+__global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void head_wide_kernel(HeadGemmArgs args) {
+    __shared__ __attribute__((aligned(1024))) char smem[2 * kWStage + (is_grad(MODE) ? kWPiece * 4 : 0)];
+    asm volatile("" ::: "a0", "a255");
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wr = wave & 1, wc = wave >> 1;
+    const int lrow = lane & 31;
+    const int khalf = lane >> 5;
+
+    const int n = __builtin_amdgcn_readfirstlane(*args.count);
+    const int n_k = n <= kBK ? kBK : (n + kBK - 1) / kBK * kBK;
+    const Share sh = share_of<kWT, MODE>(args, n, n_k);
+    if (sh.at >= sh.count) return;
+    const int slabs = args.k / kBK;
+
+    // ---- loads: slab by slab, over the ends of tiles ------------------------------------
+    // (a lane's offsets from the wave's first row: kept, or every load would take two scalar
+    // additions and some of the scalar registers that the loop has too few of)
+    uint32_t voff_p[8], voff_q[8];
+    #pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int row = lane / kChunks, lc = (lane % kChunks) ^ swizzle(8 * k + row);
+        voff_p[k] = (uint32_t)(2 * ((8 * k + row) * args.p_ld + lc * 8));
+        voff_q[k] = (uint32_t)(2 * ((8 * k + row) * args.q_ld + lc * 8));
+    }
+    struct Cursor {
+        const char *p, *q;
+        int kq, s;
+    } cur;
+    auto open_tile = [&](int kq) {
+        const Tile t = tile_at(args, sh, kq);
+        const int row0 = t.I * kWT;
+        cur.p = row0 >= args.tail_row ? args.p_tail + 2 * (int64_t)(row0 - args.tail_row) * args.p_ld
+                                      : args.p + 2 * (int64_t)row0 * args.p_ld;
+        cur.q = args.q + 2 * (int64_t)t.J * kWT * args.q_ld;
+        cur.p += 128 * (int64_t)wave * args.p_ld;  // its 64 rows
+        cur.q += 128 * (int64_t)wave * args.q_ld;
+        cur.kq = kq;
+        cur.s = 0;
+    };
+    // (past the last tile's end its last slab again, which nobody reads)
+    auto next_slab = [&] {
+        if (cur.s + 1 < slabs) {
+            ++cur.s;
+            cur.p += kRowBytes;
+            cur.q += kRowBytes;
+        } else if (cur.kq + sh.step < sh.count) {
+            open_tile(cur.kq + sh.step);
+        }
+    };
+    const uint32_t lds0 = lds_offset(smem), mine = lds0 + wave * 8 * 1024;
+    // load i of 16: 1 KB of P (i < 8) or Q
+    auto load = [&](auto i_, uint32_t stage) {
+        constexpr int i = decltype(i_)::value;
+        if constexpr (i < 8) dma16_at<i * 1024>(cur.p, voff_p[i], mine + stage);
+        else dma16_at<kHalf + (i - 8) * 1024>(cur.q, voff_q[i - 8], mine + stage);
+    };
+
+    // ---- fragments -------------------------------------------------------------------------
+    uint32_t pa[KS], qa[KS];  // of k-step ks in stage 0
+    #pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+        const uint32_t o = (uint32_t)(lrow * kRowBytes + (((ks * 2 + khalf) ^ swizzle(lrow)) << 4));
+        pa[ks] = lds0 + wr * 128 * kRowBytes + o;
+        qa[ks] = lds0 + kHalf + wc * 128 * kRowBytes + o;
+    }
+    bf16x8 fa[2][4], fb[2][4];
+
+    open_tile(sh.at);
+    each<16>([&](auto i_) { load(i_, 0); });
+    next_slab();
+    each<kLoads3>([&](auto i_) { load(i_, kWStage); });
+    wait_vm<kLoads3>();
+    __builtin_amdgcn_s_barrier();
+    #pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        fa[0][r] = frag(pa[0] + r * 32 * kRowBytes);
+        fb[0][r] = frag(qa[0] + r * 32 * kRowBytes);
+    }
+    uint32_t stage = 0;
+    for (int kq = sh.at; kq < sh.count; kq += sh.step) {
+        #pragma unroll 1
+        for (int s = 0; s < slabs; ++s) {
+            // Regions: 16 MFMAs on one set of fragments while the next is read.
+            auto region = [&](auto ks_, auto first_) {
+                constexpr int ks = decltype(ks_)::value, set = ks & 1;
+                constexpr bool kFirst = decltype(first_)::value;
+                const uint32_t from = ks + 1 < KS ? stage : stage ^ kWStage;
+                const uint32_t ap = pa[(ks + 1) % KS] + from, aq = qa[(ks + 1) % KS] + from;
+                each<16>([&](auto m_) {
+                    constexpr int m = decltype(m_)::value, i = m / 4, j = m % 4;
+                    if constexpr (kFirst) mma_first<m>(fa[set][i], fb[set][j]);
+                    else mma<m>(fa[set][i], fb[set][j]);
+                    if constexpr (m < 8) {
+                        // in the order of their use
+                        constexpr int r = m == 0 ? 0 : m <= 4 ? m - 1 : m - 4;
+                        if constexpr (m == 0 || m > 4) fa[set ^ 1][r] = frag(ap + r * 32 * kRowBytes);
+                        else fb[set ^ 1][r] = frag(aq + r * 32 * kRowBytes);
+                    }
+                    if constexpr (m % 2 == 1) {
+                        if constexpr (ks == KS - 1) {
+                            if constexpr (m / 2 < kLoads3) load(std::integral_constant<int, m / 2>{}, stage);
+                        } else if constexpr (ks == 0) {
+                            if constexpr (m / 2 < kLoads0) load(std::integral_constant<int, kLoads3 + m / 2>{}, stage ^ kWStage);
+                        } else if constexpr (ks == 1) {
+                            if constexpr (m / 2 < kLoads1) load(std::integral_constant<int, kLoads3 + kLoads0 + m / 2>{}, stage ^ kWStage);
+                        }
+                    }
+                });
+            };
+            if (s == 0) region(std::integral_constant<int, 0>{}, std::true_type{});
+            else region(std::integral_constant<int, 0>{}, std::false_type{});
+            region(std::integral_constant<int, 1>{}, std::false_type{});
+            next_slab();
+            region(std::integral_constant<int, 2>{}, std::false_type{});
+            // every fragment of this stage is in registers, and the next slab has landed
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            region(std::integral_constant<int, 3>{}, std::false_type{});
+            stage ^= kWStage;
+        }
+        // ---- epilogue: see write_tile --------------------------------------------------------
+        asm volatile("s_nop 15\n\ts_nop 15");  // the last products are in the accumulators
+        // (read from the kernel's arguments here: held through the loop, they would take the scalar
+        // registers that it needs)
+        const auto* ka = (const __attribute__((address_space(4))) HeadGemmArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+        asm volatile("" : "+s"(ka));
+        const Tile t = tile_at(args, sh, kq);
+        const int64_t v_base = ka->v0 + (int64_t)t.I * kWT + wr * 128;
+        const int64_t left = ka->vocab - v_base;
+        const int limit = left < 128 ? (int)(left < 0 ? 0 : left) : 128;
+        const int row0 = t.J * kWT + wc * 128 + lrow;
+        int target[4];
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) target[j] = ka->target != nullptr ? ka->target[row0 + 32 * j] : -1;
+        // where a lane's target is among its elements: 32 i + 8 q + r of 32 i + 8 q + 4 khalf + r, or -1
+        auto place = [&](int j) {
+            const int64_t off = target[j] - v_base;
+            return off >= 0 && off < limit && (((int)off >> 2) & 1) == khalf ? (int)off - 4 * khalf : -1;
+        };
+        auto row_of = [](int e) { return 32 * (e / 16) + 8 * (e % 16 / 4) + e % 4; };
+        if constexpr (is_stats(MODE)) {
+            const float scale = ka->inv_temp * kLog2e;
+            const int64_t part = (int64_t)(ka->first_tile + t.I) * 2 + wr;
+            each<4>([&](auto j_) {
+                constexpr int j = decltype(j_)::value;
+                float x[64];
+                each<64>([&](auto e_) {
+                    constexpr int e = decltype(e_)::value;
+                    x[e] = acc_at<16 * (4 * (e / 16) + j) + e % 16>();
+                });
+                __builtin_amdgcn_sched_barrier(0);
+                const int row = row0 + 32 * j;
+                if (limit < 128) {
+                    #pragma unroll
+                    for (int e = 0; e < 64; ++e)
+                        if (row_of(e) >= limit - 4 * khalf) x[e] = -INFINITY;
+                }
+                const int at = place(j);
+                if (__builtin_amdgcn_ballot_w64(at >= 0)) {
+                    float s = 0.f;
+                    #pragma unroll
+                    for (int e = 0; e < 64; ++e)
+                        if (at == row_of(e)) s = x[e];
+                    if (at >= 0) ka->target_logit[row] = s;
+                }
+                float m = -INFINITY;
+                #pragma unroll
+                for (int e = 0; e < 64; ++e) m = fmaxf(m, x[e]);
+                m = fmaxf(m, __shfl_xor(m, 32, 64));
+                const float m0 = m == -INFINITY ? 0.f : m;
+                if constexpr (MODE == kHeadTop) {
+                    float shown[8];
+                    #pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float m1 = -INFINITY, m2 = -INFINITY;
+                        uint32_t at1 = 0;
+                        #pragma unroll
+                        for (int v = 0; v < 16; ++v) {
+                            const float y = x[16 * i + v];
+                            const bool larger = y > m1;
+                            at1 = larger ? v : at1;
+                            m2 = __builtin_amdgcn_fmed3f(m1, m2, y);
+                            m1 = larger ? y : m1;
+                        }
+                        shown[2 * i] = m1;
+                        shown[2 * i + 1] = __uint_as_float((__float_as_uint(m2) & ~15u) | at1);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    float4* const out = reinterpret_cast<float4*>(ka->top + row * ka->row_groups + part * 8 + khalf * 4);
+                    out[0] = make_float4(shown[0], shown[1], shown[2], shown[3]);
+                    out[1] = make_float4(shown[4], shown[5], shown[6], shown[7]);
+                }
+                float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                [[maybe_unused]] float es[4] = {0.f, 0.f, 0.f, 0.f};
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float p[16];
+                    #pragma unroll
+                    for (int v = 0; v < 16; ++v) x[16 * i + v] = (x[16 * i + v] - m0) * scale;
+                    __builtin_amdgcn_sched_barrier(0);
+                    #pragma unroll
+                    for (int v = 0; v < 16; ++v) p[v] = __builtin_amdgcn_exp2f(x[16 * i + v]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    #pragma unroll
+                    for (int v = 0; v < 16; ++v) {
+                        ls[v & 3] += p[v];
+                        if constexpr (is_probs(MODE)) es[v & 3] = fmaf(p[v], fmaxf(x[16 * i + v], -200.f), es[v & 3]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                float l = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                l += __shfl_xor(l, 32, 64);
+                if constexpr (is_probs(MODE)) {
+                    float e = (es[0] + es[1]) + (es[2] + es[3]);
+                    e += __shfl_xor(e, 32, 64);
+                    if (khalf == 0) {
+                        const int64_t to = row * ka->row_parts + part;
+                        ka->part[to] = make_float2(m, l);
+                        ka->part_e[to] = e;
+                    }
+                } else if (khalf == 0) {
+                    ka->part[part * ka->t_pad + row] = make_float2(m, l);
+                }
+            });
+        } else {
+            const float inv_norm = 1.f / norm_of(ka->norm), inv_temp = ka->inv_temp;
+            float lse[4], cp[4], ct[4];
+            [[maybe_unused]] float ce[4];
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                lse[j] = ka->lse[row0 + 32 * j];
+                cp[j] = ka->cp[row0 + 32 * j] * inv_norm;
+                ct[j] = ka->ct[row0 + 32 * j] * inv_norm;
+                if constexpr (MODE == kHeadGradEntropy) ce[j] = ka->ce[row0 + 32 * j] * inv_norm;
+            }
+            // a wave's 32 rows at a time through an LDS piece of its own, as rows of 128 words
+            char* const piece = smem + 2 * kWStage + wave * kWPiece;
+            const int64_t g_ld = ka->g_ld;
+            char* const g_out = ka->g + 2 * ((int64_t)(t.J * kWT + wc * 128) * g_ld + t.I * kWT + wr * 128);
+            each<4>([&](auto j_) {
+                constexpr int j = decltype(j_)::value;
+                float x[64];
+                each<64>([&](auto e_) {
+                    constexpr int e = decltype(e_)::value;
+                    x[e] = acc_at<16 * (4 * (e / 16) + j) + e % 16>();
+                });
+                __builtin_amdgcn_sched_barrier(0);
+                auto weight = [&](float y) { return MODE == kHeadGradEntropy ? fmaf(ce[j], fmaxf(y, -200.f), cp[j]) : cp[j]; };
+                const int at = place(j);
+                float hit = 0.f;
+                const bool any = __builtin_amdgcn_ballot_w64(at >= 0);
+                if (any) {
+                    #pragma unroll
+                    for (int e = 0; e < 64; ++e)
+                        if (at == row_of(e)) hit = x[e];
+                    const float y = fmaf(hit, inv_temp, -lse[j]);
+                    hit = fmaf(__builtin_amdgcn_exp2f(y * kLog2e), weight(y), -ct[j]);
+                }
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float p[16];
+                    #pragma unroll
+                    for (int v = 0; v < 16; ++v) x[16 * i + v] = fmaf(x[16 * i + v], inv_temp, -lse[j]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    #pragma unroll
+                    for (int v = 0; v < 16; ++v) p[v] = __builtin_amdgcn_exp2f(x[16 * i + v] * kLog2e);
+                    __builtin_amdgcn_sched_barrier(0);
+                    #pragma unroll
+                    for (int v = 0; v < 16; ++v) x[16 * i + v] = p[v] * weight(x[16 * i + v]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (any) {
+                    #pragma unroll
+                    for (int e = 0; e < 64; ++e)
+                        if (at == row_of(e)) x[e] = hit;
+                }
+                if (limit < 128) {
+                    #pragma unroll
+                    for (int e = 0; e < 64; ++e)
+                        if (row_of(e) >= limit - 4 * khalf) x[e] = 0.f;
+                }
+                #pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    uint16_t b[4];
+                    #pragma unroll
+                    for (int e = 0; e < 4; ++e) b[e] = f32_to_bf16(x[4 * q + e]);
+                    *reinterpret_cast<uint2*>(piece + lrow * 256 + ((q ^ (lrow & 15)) << 4) + khalf * 8) =
+                        make_uint2((uint32_t)b[0] | ((uint32_t)b[1] << 16), (uint32_t)b[2] | ((uint32_t)b[3] << 16));
+                }
+                // (only this wave's own: its LDS accesses complete in order)
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                #pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int c = 4 * u + lane / 16, ch = lane % 16;
+                    const uint4 v = *reinterpret_cast<const uint4*>(piece + c * 256 + ((ch ^ (c & 15)) << 4));
+                    *reinterpret_cast<uint4*>(g_out + 2 * ((32 * j + c) * g_ld + ch * 8)) = v;
+                }
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            });
+        }
+    }
+    wait_vm<0>();  // no load may land when the workgroup has gone
+}
+
+}  // namespace
+
+hipError_t launch_head_wide(int mode, const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream) {
+    const int64_t per_xcd = (max_tiles + kXcds - 1) / kXcds, most = head_slots(kWT) / kXcds;
+    const dim3 grid(kXcds * (int)(per_xcd < most ? per_xcd : most)), block(kWThreads);
+    switch (mode) {
+        case kHeadLse: hipLaunchKernelGGL((head_wide_kernel<kHeadLse>), grid, block, 0, stream, a); break;
+        case kHeadProbs: hipLaunchKernelGGL((head_wide_kernel<kHeadProbs>), grid, block, 0, stream, a); break;
+        case kHeadTop: hipLaunchKernelGGL((head_wide_kernel<kHeadTop>), grid, block, 0, stream, a); break;
+        case kHeadGrad: hipLaunchKernelGGL((head_wide_kernel<kHeadGrad>), grid, block, 0, stream, a); break;
+        case kHeadGradEntropy: hipLaunchKernelGGL((head_wide_kernel<kHeadGradEntropy>), grid, block, 0, stream, a); break;
+        default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace dmuon
