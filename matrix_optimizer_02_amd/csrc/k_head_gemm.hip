@@ -460,7 +460,7 @@ hipError_t launch_head_gemm(int mode, HeadTile tile, const HeadGemmArgs& a, int6
     if (tile.tp == 64) return launch_config<Config<64, 64, 4>>(mode, a, max_tiles, stream);
     if (tile.tq == 64) return launch_config<Config<256, 64, 2>>(mode, a, max_tiles, stream);
     if (tile.tq == 128) return launch_config<Config<256, 128, 3>>(mode, a, max_tiles, stream);
-    if (a.parts == 1 && a.logits == nullptr && (is_stats(mode) || is_grad(mode)))
+    if (a.parts == 1 && a.logits == nullptr)
         return launch_head_wide(mode, a, max_tiles, stream);
     return launch_config<Config<256, 256, 2>>(mode, a, max_tiles, stream);
 }

@@ -36,6 +36,14 @@ constexpr int kWPiece = 32 * 256;             // 32 token rows of a wave's 128 w
 typedef __attribute__((address_space(3))) const bf16x8 lds_frag;
 __device__ __forceinline__ bf16x8 frag(uint32_t at) { return *reinterpret_cast<lds_frag*>(at); }
 
+// ... of a K-major slab: two transposing reads, STEP bytes apart.
+template <int AT, int STEP>
+__device__ __forceinline__ bf16x8 frag_wide(uint32_t at) {
+    const shortx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_shortx4*>(at + AT));
+    const shortx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_shortx4*>(at + AT + STEP));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
 template <typename F, int... M>
 __device__ __forceinline__ void each(F&& f, std::integer_sequence<int, M...>) {
     (f(std::integral_constant<int, M>{}), ...);
@@ -72,12 +80,31 @@ __device__ __forceinline__ void dma16_at(const void* base, uint32_t voff, uint32
 }
 #pragma clang diagnostic pop
 
+// A wave's 32 rows of 128 bf16 in an LDS piece of its own: written by the columns that
+// the accumulators hold, read by rows (chunk ch of row c).
+__device__ __forceinline__ void to_piece(char* piece, const float (&x)[64], int lrow, int khalf) {
+    #pragma unroll
+    for (int q = 0; q < 16; ++q) {
+        uint16_t b[4];
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] = f32_to_bf16(x[4 * q + e]);
+        *reinterpret_cast<uint2*>(piece + lrow * 256 + ((q ^ (lrow & 15)) << 4) + khalf * 8) =
+            make_uint2((uint32_t)b[0] | ((uint32_t)b[1] << 16), (uint32_t)b[2] | ((uint32_t)b[3] << 16));
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // (only this wave's own: there is no barrier)
+}
+__device__ __forceinline__ uint4 from_piece(const char* piece, int c, int ch) {
+    return *reinterpret_cast<const uint4*>(piece + c * 256 + ((ch ^ (c & 15)) << 4));
+}
+
 constexpr int kLoads3 = 6, kLoads0 = 6, kLoads1 = 16 - kLoads3 - kLoads0;
 
 template <int MODE>
 __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void head_wide_kernel(HeadGemmArgs args) {
-    __shared__ __attribute__((aligned(1024))) char smem[2 * kWStage + (is_grad(MODE) ? kWPiece * 4 : 0)];
+    __shared__ __attribute__((aligned(1024))) char smem[2 * kWStage + (is_grad(MODE) || MODE == kHeadDw ? kWPiece * 4 : 0)];
     asm volatile("" ::: "a0", "a255");
+    constexpr bool PW = MODE == kHeadDh || is_dw(MODE), QW = is_dw(MODE);  // K-major operands
+    using WP = Wide<kWT>;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -89,39 +116,83 @@ __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1)
     const int n_k = n <= kBK ? kBK : (n + kBK - 1) / kBK * kBK;
     const Share sh = share_of<kWT, MODE>(args, n, n_k);
     if (sh.at >= sh.count) return;
-    const int slabs = args.k / kBK;
+    // K extent of a tile: its first k and its slabs (a last split may have none: it then
+    // multiplies one for nothing)
+    auto extent = [&](const Tile& t, int& first, bool& empty) {
+        first = 0;
+        int k = args.k;
+        if (MODE == kHeadDh) {
+            first = t.split * args.split_k;
+            k = imin(args.split_k, args.k - first);
+        } else if (MODE == kHeadDw) {
+            k = n_k;
+        } else if (MODE == kHeadDwSum) {
+            const int per = (n_k / kBK + args.splits - 1) / args.splits * kBK;
+            first = t.split * per;
+            k = imin(per, n_k - first);
+        }
+        empty = k <= 0;
+        if (empty) first = 0;
+        return empty ? 1 : k / kBK;
+    };
 
     // ---- loads: slab by slab, over the ends of tiles ------------------------------------
     // (a lane's offsets from the wave's first row: kept, or every load would take two scalar
     // additions and some of the scalar registers that the loop has too few of)
     uint32_t voff_p[8], voff_q[8];
+    struct Cursor {
+        const char *p, *q;
+        int kq, left;  // slabs left in the tile
+        int k;         // dH: of the piece's rows
+    } cur;
+    // K-contiguous: the wave's 64 rows; K-major: its 16 k
+    const int p_step = PW ? kBK * args.p_ld : kBK, q_step = QW ? kBK * args.q_ld : kBK;
+    auto open_tile = [&](int kq) {
+        const Tile t = tile_at(args, sh, kq);
+        int first;
+        bool empty;
+        cur.left = extent(t, first, empty);
+        cur.kq = kq;
+        if constexpr (PW) {
+            cur.k = first;
+            const bool tail = MODE == kHeadDh && first >= args.tail_row;
+            cur.p = (tail ? args.p_tail + 2 * (int64_t)(first - args.tail_row) * args.p_ld
+                          : args.p + 2 * (int64_t)first * args.p_ld) + 32 * (int64_t)wave * args.p_ld;
+            #pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int row = lane / WP::kChunksRow, lc = (lane % WP::kChunksRow) ^ WP::swz(2 * k + row);
+                // columns past the row's end repeat its last chunk (never stored)
+                voff_p[k] = (uint32_t)(2 * ((2 * k + row) * args.p_ld + imin(t.I * kWT + lc * 8, args.p_ld - 8)));
+            }
+        } else {
+            const int row0 = t.I * kWT;
+            cur.p = (row0 >= args.tail_row ? args.p_tail + 2 * (int64_t)(row0 - args.tail_row) * args.p_ld
+                                           : args.p + 2 * (int64_t)row0 * args.p_ld) + 128 * (int64_t)wave * args.p_ld;
+        }
+        if constexpr (QW) cur.q = args.q + 2 * ((int64_t)(first + 16 * wave) * args.q_ld + (int64_t)t.J * kWT);
+        else cur.q = args.q + 2 * ((int64_t)(t.J * kWT + 64 * wave) * args.q_ld + first);
+    };
     #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const int row = lane / kChunks, lc = (lane % kChunks) ^ swizzle(8 * k + row);
-        voff_p[k] = (uint32_t)(2 * ((8 * k + row) * args.p_ld + lc * 8));
-        voff_q[k] = (uint32_t)(2 * ((8 * k + row) * args.q_ld + lc * 8));
+        if (!PW) voff_p[k] = (uint32_t)(2 * ((8 * k + row) * args.p_ld + lc * 8));
+        if (!QW) {
+            voff_q[k] = (uint32_t)(2 * ((8 * k + row) * args.q_ld + lc * 8));
+        } else {
+            const int wrow = lane / WP::kChunksRow, wlc = (lane % WP::kChunksRow) ^ WP::swz(2 * k + wrow);
+            voff_q[k] = (uint32_t)(2 * ((2 * k + wrow) * args.q_ld + wlc * 8));
+        }
     }
-    struct Cursor {
-        const char *p, *q;
-        int kq, s;
-    } cur;
-    auto open_tile = [&](int kq) {
-        const Tile t = tile_at(args, sh, kq);
-        const int row0 = t.I * kWT;
-        cur.p = row0 >= args.tail_row ? args.p_tail + 2 * (int64_t)(row0 - args.tail_row) * args.p_ld
-                                      : args.p + 2 * (int64_t)row0 * args.p_ld;
-        cur.q = args.q + 2 * (int64_t)t.J * kWT * args.q_ld;
-        cur.p += 128 * (int64_t)wave * args.p_ld;  // its 64 rows
-        cur.q += 128 * (int64_t)wave * args.q_ld;
-        cur.kq = kq;
-        cur.s = 0;
-    };
     // (past the last tile's end its last slab again, which nobody reads)
     auto next_slab = [&] {
-        if (cur.s + 1 < slabs) {
-            ++cur.s;
-            cur.p += kRowBytes;
-            cur.q += kRowBytes;
+        if (cur.left > 1) {
+            --cur.left;
+            cur.p += 2 * (int64_t)p_step;
+            cur.q += 2 * (int64_t)q_step;
+            if (MODE == kHeadDh) {
+                cur.k += kBK;
+                if (cur.k == args.tail_row) cur.p = args.p_tail + 32 * (int64_t)wave * args.p_ld;
+            }
         } else if (cur.kq + sh.step < sh.count) {
             open_tile(cur.kq + sh.step);
         }
@@ -135,13 +206,33 @@ __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1)
     };
 
     // ---- fragments -------------------------------------------------------------------------
-    uint32_t pa[KS], qa[KS];  // of k-step ks in stage 0
+    // K-contiguous rows: of k-step ks in stage 0; K-major: of rows or columns 32 i ...
+    uint32_t pa[4], qa[4];
+    const int tr_g = lane >> 4, tr_s = lane & 15;
     #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-        const uint32_t o = (uint32_t)(lrow * kRowBytes + (((ks * 2 + khalf) ^ swizzle(lrow)) << 4));
-        pa[ks] = lds0 + wr * 128 * kRowBytes + o;
-        qa[ks] = lds0 + kHalf + wc * 128 * kRowBytes + o;
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t o = (uint32_t)(lrow * kRowBytes + (((k * 2 + khalf) ^ swizzle(lrow)) << 4));
+        pa[k] = lds0 + wr * 128 * kRowBytes + o;
+        qa[k] = lds0 + kHalf + wc * 128 * kRowBytes + o;
+        // transposing read: see k_head_gemm.hip
+        const int row = 8 * (tr_g >> 1) + (tr_s >> 2), col = 32 * k + 16 * (tr_g & 1) + 4 * (tr_s & 3);
+        auto wide = [&](int col0) {
+            return (uint32_t)(row * WP::kBytes + ((((col0 + col) >> 3) ^ WP::swz(tr_s >> 2)) << 4) + (col & 7) * 2);
+        };
+        if (PW) pa[k] = lds0 + wide(wr * 128);
+        if (QW) qa[k] = lds0 + kHalf + wide(wc * 128);
     }
+    // fragment i of k-step ks, `from` a stage
+    auto read_p = [&](auto i_, auto ks_, uint32_t from) {
+        constexpr int i = decltype(i_)::value, ks = decltype(ks_)::value;
+        if constexpr (PW) return frag_wide<ks * 16 * WP::kBytes, 4 * WP::kBytes>(pa[i] + from);
+        else return frag(pa[ks] + from + i * 32 * kRowBytes);
+    };
+    auto read_q = [&](auto j_, auto ks_, uint32_t from) {
+        constexpr int j = decltype(j_)::value, ks = decltype(ks_)::value;
+        if constexpr (QW) return frag_wide<ks * 16 * WP::kBytes, 4 * WP::kBytes>(qa[j] + from);
+        else return frag(qa[ks] + from + j * 32 * kRowBytes);
+    };
     bf16x8 fa[2][4], fb[2][4];
 
     open_tile(sh.at);
@@ -150,13 +241,17 @@ __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1)
     each<kLoads3>([&](auto i_) { load(i_, kWStage); });
     wait_vm<kLoads3>();
     __builtin_amdgcn_s_barrier();
-    #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        fa[0][r] = frag(pa[0] + r * 32 * kRowBytes);
-        fb[0][r] = frag(qa[0] + r * 32 * kRowBytes);
-    }
+    each<4>([&](auto r_) {
+        constexpr int r = decltype(r_)::value;
+        fa[0][r] = read_p(r_, std::integral_constant<int, 0>{}, 0);
+        fb[0][r] = read_q(r_, std::integral_constant<int, 0>{}, 0);
+    });
     uint32_t stage = 0;
     for (int kq = sh.at; kq < sh.count; kq += sh.step) {
+        const Tile t = tile_at(args, sh, kq);
+        int k_first;
+        bool empty;
+        const int slabs = extent(t, k_first, empty);
         #pragma unroll 1
         for (int s = 0; s < slabs; ++s) {
             // Regions: 16 MFMAs on one set of fragments while the next is read.
@@ -164,16 +259,16 @@ __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1)
                 constexpr int ks = decltype(ks_)::value, set = ks & 1;
                 constexpr bool kFirst = decltype(first_)::value;
                 const uint32_t from = ks + 1 < KS ? stage : stage ^ kWStage;
-                const uint32_t ap = pa[(ks + 1) % KS] + from, aq = qa[(ks + 1) % KS] + from;
+                constexpr std::integral_constant<int, (ks + 1) % KS> next{};
                 each<16>([&](auto m_) {
                     constexpr int m = decltype(m_)::value, i = m / 4, j = m % 4;
                     if constexpr (kFirst) mma_first<m>(fa[set][i], fb[set][j]);
                     else mma<m>(fa[set][i], fb[set][j]);
                     if constexpr (m < 8) {
                         // in the order of their use
-                        constexpr int r = m == 0 ? 0 : m <= 4 ? m - 1 : m - 4;
-                        if constexpr (m == 0 || m > 4) fa[set ^ 1][r] = frag(ap + r * 32 * kRowBytes);
-                        else fb[set ^ 1][r] = frag(aq + r * 32 * kRowBytes);
+                        constexpr std::integral_constant<int, m == 0 ? 0 : m <= 4 ? m - 1 : m - 4> r{};
+                        if constexpr (m == 0 || m > 4) fa[set ^ 1][r] = read_p(r, next, from);
+                        else fb[set ^ 1][r] = read_q(r, next, from);
                     }
                     if constexpr (m % 2 == 1) {
                         if constexpr (ks == KS - 1) {
@@ -203,14 +298,14 @@ __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1)
         // registers that it needs)
         const auto* ka = (const __attribute__((address_space(4))) HeadGemmArgs*)__builtin_amdgcn_kernarg_segment_ptr();
         asm volatile("" : "+s"(ka));
-        const Tile t = tile_at(args, sh, kq);
         const int64_t v_base = ka->v0 + (int64_t)t.I * kWT + wr * 128;
         const int64_t left = ka->vocab - v_base;
         const int limit = left < 128 ? (int)(left < 0 ? 0 : left) : 128;
         const int row0 = t.J * kWT + wc * 128 + lrow;
-        int target[4];
+        [[maybe_unused]] int target[4];
         #pragma unroll
-        for (int j = 0; j < 4; ++j) target[j] = ka->target != nullptr ? ka->target[row0 + 32 * j] : -1;
+        for (int j = 0; j < 4; ++j)
+            if constexpr (is_stats(MODE) || is_grad(MODE)) target[j] = ka->target != nullptr ? ka->target[row0 + 32 * j] : -1;
         // where a lane's target is among its elements: 32 i + 8 q + r of 32 i + 8 q + 4 khalf + r, or -1
         auto place = [&](int j) {
             const int64_t off = target[j] - v_base;
@@ -301,6 +396,69 @@ __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1)
                     ka->part[part * ka->t_pad + row] = make_float2(m, l);
                 }
             });
+        } else if constexpr (MODE == kHeadDh || MODE == kHeadDwSum) {
+            // in the order in which eight waves of 128 x 64 hold them (launch_head_sum)
+            float4* const d = reinterpret_cast<float4*>(ka->sums) +
+                              ((int64_t)(t.split * sh.tiles_j + t.J) * ka->tiles_i + t.I) * (kWT * kWT / 4) + lane;
+            const bool add = MODE == kHeadDh && ka->accumulate;
+            each<4>([&](auto j_) {
+                constexpr int j = decltype(j_)::value;
+                float x[64];
+                each<64>([&](auto e_) {
+                    constexpr int e = decltype(e_)::value;
+                    x[e] = acc_at<16 * (4 * (e / 16) + j) + e % 16>();
+                });
+                const int wave8 = 2 * (2 * wc + j / 2) + wr;
+                float4* const p = d + (int64_t)wave8 * (4 * 2 * 4 * 64) + (j % 2) * (4 * 64);
+                #pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float4 b[8];
+                    if (add) {
+                        #pragma unroll
+                        for (int q = 0; q < 8; ++q) b[q] = p[((2 * h + q / 4) * 2 * 4 + q % 4) * 64];
+                    }
+                    #pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const int e = 32 * h + 4 * q;
+                        float4 o = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                        if (MODE == kHeadDwSum && empty) o = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (add) o = make_float4(o.x + b[q].x, o.y + b[q].y, o.z + b[q].z, o.w + b[q].w);
+                        p[((2 * h + q / 4) * 2 * 4 + q % 4) * 64] = o;
+                    }
+                }
+            });
+        } else if constexpr (MODE == kHeadDw) {
+            const float norm = norm_of(ka->norm);
+            const int dw_ld = ka->dw_ld, col = t.I * kWT + wr * 128 + (lane % 16) * 8;
+            const int64_t dw_rows = ka->dw_rows;
+            uint16_t* const dw = static_cast<uint16_t*>(ka->dw);
+            char* const piece = smem + 2 * kWStage + wave * kWPiece;
+            each<4>([&](auto j_) {
+                constexpr int j = decltype(j_)::value;
+                float x[64];
+                each<64>([&](auto e_) {
+                    constexpr int e = decltype(e_)::value;
+                    x[e] = acc_at<16 * (4 * (e / 16) + j) + e % 16>() * norm;
+                });
+                to_piece(piece, x, lrow, khalf);
+                #pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int c = 4 * u + lane / 16;
+                    const int64_t row = (int64_t)t.J * kWT + wc * 128 + 32 * j + c;
+                    const uint4 v = from_piece(piece, c, lane % 16);
+                    if (row >= dw_rows || col >= dw_ld) continue;
+                    uint16_t* const p = dw + row * dw_ld + col;
+                    if ((dw_ld & 7) == 0) {
+                        *reinterpret_cast<uint4*>(p) = v;
+                    } else {
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        #pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (col + e < dw_ld) p[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+                    }
+                }
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            });
         } else {
             const float inv_norm = 1.f / norm_of(ka->norm), inv_temp = ka->inv_temp;
             float lse[4], cp[4], ct[4];
@@ -358,21 +516,11 @@ __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1)
                     for (int e = 0; e < 64; ++e)
                         if (row_of(e) >= limit - 4 * khalf) x[e] = 0.f;
                 }
-                #pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    uint16_t b[4];
-                    #pragma unroll
-                    for (int e = 0; e < 4; ++e) b[e] = f32_to_bf16(x[4 * q + e]);
-                    *reinterpret_cast<uint2*>(piece + lrow * 256 + ((q ^ (lrow & 15)) << 4) + khalf * 8) =
-                        make_uint2((uint32_t)b[0] | ((uint32_t)b[1] << 16), (uint32_t)b[2] | ((uint32_t)b[3] << 16));
-                }
-                // (only this wave's own: its LDS accesses complete in order)
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                to_piece(piece, x, lrow, khalf);
                 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     const int c = 4 * u + lane / 16, ch = lane % 16;
-                    const uint4 v = *reinterpret_cast<const uint4*>(piece + c * 256 + ((ch ^ (c & 15)) << 4));
-                    *reinterpret_cast<uint4*>(g_out + 2 * ((32 * j + c) * g_ld + ch * 8)) = v;
+                    *reinterpret_cast<uint4*>(g_out + 2 * ((32 * j + c) * g_ld + ch * 8)) = from_piece(piece, c, ch);
                 }
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             });
@@ -392,6 +540,9 @@ hipError_t launch_head_wide(int mode, const HeadGemmArgs& a, int64_t max_tiles, 
         case kHeadTop: hipLaunchKernelGGL((head_wide_kernel<kHeadTop>), grid, block, 0, stream, a); break;
         case kHeadGrad: hipLaunchKernelGGL((head_wide_kernel<kHeadGrad>), grid, block, 0, stream, a); break;
         case kHeadGradEntropy: hipLaunchKernelGGL((head_wide_kernel<kHeadGradEntropy>), grid, block, 0, stream, a); break;
+        case kHeadDh: hipLaunchKernelGGL((head_wide_kernel<kHeadDh>), grid, block, 0, stream, a); break;
+        case kHeadDw: hipLaunchKernelGGL((head_wide_kernel<kHeadDw>), grid, block, 0, stream, a); break;
+        case kHeadDwSum: hipLaunchKernelGGL((head_wide_kernel<kHeadDwSum>), grid, block, 0, stream, a); break;
         default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
