@@ -22,7 +22,8 @@
 // MFMA k-steps (hi hi, hi lo, lo hi).  The gradients of fp32 operands:
 // k_head_x3.hip.
 //
-// Tiles.  256 x 256 outputs, 8 waves, for work that fills the chip; 256 x 128
+// Tiles.  256 x 256 outputs, 8 waves, for work that fills the chip (bf16 operands:
+// k_head_wide.hip, four waves); 256 x 128
 // where 256 token rows would be mostly padding; 256 x 64 for batches of at most
 // 64 rows, which are bound by reading W; 64 x 64, 4 waves, where the others
 // would leave most CUs idle (pick_tile in head_layout.cpp has the rule, with the
@@ -32,17 +33,7 @@
 // What bounds it: the MFMA.  The main loop is pipelined in registers: while one set
 // of fragments is multiplied the next is read from LDS, also across the barrier that
 // lands the next slab, and the first slab of the next tile loads behind the epilogue.
-// Against read, wait, multiply (8192 tokens, hidden 4096, vocabulary 128256, bf16):
-// backward 21.4 ms for 21.8; 238 x 1792 x 16374 backward 92 us for 103.  The softmax
-// statistics of 256 x 256 bf16 tiles keep the plain loop (plain_loop in head_tile.h
-// has the figures).  At that first size Lse reaches 1148 TFLOP/s, Grad 1063, dH 1160
-// and dW 1166 on one card (1234, 1153, 1221 and 1235 on another), where a library's plain
-// products of the same operands, logits written, reach 1451 (logits), 1345 (dH) and 1124
-// (dW).  The matrix cores are busy for 56 to 60% of the cycles, LDS conflicts take at most
-// 2% of its own and memory is read and written at 1.0 to 1.2 TB/s: what is lost is lost
-// at barriers and in epilogues.  What keeps Lse from more is its epilogue (an exponential a
-// logit, with the MFMA idle: two tiles' accumulators do not fit in one wave's
-// registers) and one workgroup a CU, so that no other covers the barriers.
+// Against read, wait, multiply: 238 x 1792 x 16374, bf16, backward 92 us for 103.
 #include "head_tile.h"
 
 namespace dmuon {
@@ -52,8 +43,7 @@ using namespace head;
 
 // KIND: kHeadBf16, or kHeadHalf2 (logits of fp32 operands).
 template <typename C, int MODE, int KIND>
-__global__ __launch_bounds__(C::NT) __attribute__((
-    amdgpu_waves_per_eu(2, plain_loop<C, MODE>(KIND == kHeadHalf2) ? 8 : 2))) void head_gemm_kernel(HeadGemmArgs args) {
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void head_gemm_kernel(HeadGemmArgs args) {
     constexpr bool PW = MODE == kHeadDh || is_dw(MODE);  // P is K-major
     constexpr bool QW = is_dw(MODE);                     // Q is K-major
     constexpr int TP = C::TP, TQ = C::TQ;
@@ -197,7 +187,6 @@ __global__ __launch_bounds__(C::NT) __attribute__((
                 #pragma unroll
                 for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
 
-        constexpr bool kPlain = plain_loop<C, MODE>(KIND == kHeadHalf2);
         // ---- main loop ---------------------------------------------------------------
         const int slabs = pl.K / kBK;
         const int swz = swizzle(lrow);
@@ -232,7 +221,7 @@ __global__ __launch_bounds__(C::NT) __attribute__((
         __syncthreads();  // the previous tile's epilogue has left the buffers
         #pragma unroll
         for (int s = 1; s < C::ST - 1; ++s)
-            if (!kPlain || s < slabs) load_slab(pl.L, imin(s, slabs - 1) * kBK, s - 1);
+            load_slab(pl.L, imin(s, slabs - 1) * kBK, s - 1);
         int stage = C::ST - 1;
         // Loads complete in order: a slab has landed when only later slabs' may be in flight.
         // The barrier lands it for every wave; each is then done with the slab before.
@@ -264,36 +253,7 @@ __global__ __launch_bounds__(C::NT) __attribute__((
         };
         // Regions: MFMAs on one set of fragments while the next set is read.  The last
         // region of a slab runs behind the barrier that lands the next one.
-        if constexpr (kPlain) {
-            // read, wait, multiply: see plain_loop
-            for (int s = 0; s < slabs; ++s) {
-                if (C::ST > 2 && s + C::ST - 2 < slabs)
-                    wait_vm<(C::ST - 2) * (C::kPLoads + C::kQLoads)>();
-                else if (C::ST == 2 && s == 0 && behind)
-                    wait_vm<kStores>();
-                else
-                    wait_vm<0>();
-                __syncthreads();
-                if (s + C::ST - 1 < slabs)
-                    load_slab(pl.L, (s + C::ST - 1) * kBK, stage == 0 ? C::ST - 1 : stage - 1);
-                const char* pb = smem + stage * (C::kPBytes + C::kQBytes);
-                const char* qb = pb + C::kPBytes;
-                stage = stage + 1 == C::ST ? 0 : stage + 1;
-                #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    bf16x8 fa[C::FI], fb[C::FJ];
-                    #pragma unroll
-                    for (int i = 0; i < C::FI; ++i) fa[i] = read_p(pb, i, ks);
-                    #pragma unroll
-                    for (int j = 0; j < C::FJ; ++j) fb[j] = read_q(qb, j, ks);
-                    #pragma unroll
-                    for (int i = 0; i < C::FI; ++i)
-                        #pragma unroll
-                        for (int j = 0; j < C::FJ; ++j)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
-                }
-            }
-        } else if constexpr (KIND == kHeadHalf2) {
+        if constexpr (KIND == kHeadHalf2) {
             // k-steps 0, 1 of the slab hold hi, 2, 3 lo.  A region: one P fragment pair (i)
             // of one k-step, its three products with the Q pairs.
             bf16x8 ph[2], pl_[2], qh[2][C::FJ], ql[2][C::FJ];
@@ -422,32 +382,27 @@ hipError_t launch(const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream) 
     return hipGetLastError();
 }
 
+template <typename C, int KIND>
+hipError_t launch_logits(int mode, const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream) {
+    switch (mode) {
+        case kHeadLse: return launch<C, kHeadLse, KIND>(a, max_tiles, stream);
+        case kHeadGrad: return launch<C, kHeadGrad, KIND>(a, max_tiles, stream);
+        case kHeadGradEntropy: return launch<C, kHeadGradEntropy, KIND>(a, max_tiles, stream);
+        case kHeadProbs: return launch<C, kHeadProbs, KIND>(a, max_tiles, stream);
+        case kHeadTop: return launch<C, kHeadTop, KIND>(a, max_tiles, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
 template <typename C>
 hipError_t launch_config(int mode, const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream) {
-    const bool f32 = a.parts > 1;
     switch (mode) {
-        case kHeadLse:
-            return f32 ? launch<C, kHeadLse, kHeadHalf2>(a, max_tiles, stream)
-                       : launch<C, kHeadLse, kHeadBf16>(a, max_tiles, stream);
-        case kHeadGrad:
-            return f32 ? launch<C, kHeadGrad, kHeadHalf2>(a, max_tiles, stream)
-                       : launch<C, kHeadGrad, kHeadBf16>(a, max_tiles, stream);
-        case kHeadGradEntropy:
-            return f32 ? launch<C, kHeadGradEntropy, kHeadHalf2>(a, max_tiles, stream)
-                       : launch<C, kHeadGradEntropy, kHeadBf16>(a, max_tiles, stream);
-        case kHeadProbs:
-            return f32 ? launch<C, kHeadProbs, kHeadHalf2>(a, max_tiles, stream)
-                       : launch<C, kHeadProbs, kHeadBf16>(a, max_tiles, stream);
-        case kHeadTop:
-            return f32 ? launch<C, kHeadTop, kHeadHalf2>(a, max_tiles, stream)
-                       : launch<C, kHeadTop, kHeadBf16>(a, max_tiles, stream);
-        case kHeadDh:
-            return launch<C, kHeadDh, kHeadBf16>(a, max_tiles, stream);
-        case kHeadDw:
-            return launch<C, kHeadDw, kHeadBf16>(a, max_tiles, stream);
-        case kHeadDwSum:
-            return launch<C, kHeadDwSum, kHeadBf16>(a, max_tiles, stream);
-        default: return hipErrorInvalidValue;
+        case kHeadDh: return launch<C, kHeadDh, kHeadBf16>(a, max_tiles, stream);
+        case kHeadDw: return launch<C, kHeadDw, kHeadBf16>(a, max_tiles, stream);
+        case kHeadDwSum: return launch<C, kHeadDwSum, kHeadBf16>(a, max_tiles, stream);
+        default:
+            return a.parts > 1 ? launch_logits<C, kHeadHalf2>(mode, a, max_tiles, stream)
+                               : launch_logits<C, kHeadBf16>(mode, a, max_tiles, stream);
     }
 }
 
@@ -460,9 +415,8 @@ hipError_t launch_head_gemm(int mode, HeadTile tile, const HeadGemmArgs& a, int6
     if (tile.tp == 64) return launch_config<Config<64, 64, 4>>(mode, a, max_tiles, stream);
     if (tile.tq == 64) return launch_config<Config<256, 64, 2>>(mode, a, max_tiles, stream);
     if (tile.tq == 128) return launch_config<Config<256, 128, 3>>(mode, a, max_tiles, stream);
-    if (a.parts == 1 && a.logits == nullptr)
-        return launch_head_wide(mode, a, max_tiles, stream);
-    return launch_config<Config<256, 256, 2>>(mode, a, max_tiles, stream);
+    if (a.parts == 1) return launch_head_wide(mode, a, max_tiles, stream);
+    return launch_logits<Config<256, 256, 2>, kHeadHalf2>(mode, a, max_tiles, stream);
 }
 
 }  // namespace dmuon

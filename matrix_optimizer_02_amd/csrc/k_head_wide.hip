@@ -1,6 +1,6 @@
 // Tile products of the output head for bf16 operands and work that fills the chip: 256 x
-// 256 tiles by four waves of 128 x 128 (modes Lse, Probs, Top, Grad and GradEntropy of
-// k_head_gemm.hip; the same sums in the same order, the same statistics).
+// 256 tiles by four waves of 128 x 128 (the modes of k_head_gemm.hip; the same sums in
+// the same order, the same statistics as its other tiles).
 //
 // Eight waves of 128 x 64 read 192 KB of fragments from LDS for every 64 KB that a slab
 // brings; four of 128 x 128 read 128 KB.  Their 256 accumulators a lane are all of the
@@ -14,9 +14,9 @@
 //
 // What bounds it: the matrix cores with the loads' way into LDS.  8192 tokens, hidden
 // 4096, vocabulary 128256, statistics of softmax and entropy: 6.29 ms, 1368 TFLOP/s,
-// where eight waves take 6.96 to 7.15 on the same cards; 5.4 without its loads, 6.0
-// without its epilogue.  Waiting for the loads costs nothing (6.47 either way with loads
-// in two k-steps); lines touched ahead of them cost 10%.
+// where eight waves take 6.96 to 7.15 on the same cards; 5.8 without its loads.  5734
+// tokens of that size, a piece of 16384 vocabulary rows: ds 633 us for 712, dH 772 for 829, dW
+// 591 for 625.  Lines touched ahead of the loads cost 10%.
 #include "head_tile.h"
 
 #include <type_traits>
@@ -324,6 +324,14 @@ __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1)
                 });
                 __builtin_amdgcn_sched_barrier(0);
                 const int row = row0 + 32 * j;
+                if constexpr (MODE != kHeadTop) {
+                    if (ka->logits != nullptr) {
+                        float* const out = ka->logits + (int64_t)row * ka->logits_ld + v_base + 4 * khalf;
+                        #pragma unroll
+                        for (int q = 0; q < 16; ++q)
+                            *reinterpret_cast<float4*>(out + 8 * q) = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+                    }
+                }
                 if (limit < 128) {
                     #pragma unroll
                     for (int e = 0; e < 64; ++e)
