@@ -42,7 +42,7 @@ extern "C" {
 
 /* Bytes of device workspace for grad_norm_batched over these tensors.  Errors:
  * INVALID_ARG (null pointer, negative count or size, unknown dtype),
- * UNSUPPORTED (2^45 bytes or more in a tensor, or in up to 150 that follow one
+ * UNSUPPORTED (2^45 bytes or more in a tensor, or in up to 192 that follow one
  * another). */
 DMUON_API dmuon_status grad_norm_workspace_bytes(int32_t count, const int64_t* numels, const int32_t* dtypes,
                                                  size_t* bytes);

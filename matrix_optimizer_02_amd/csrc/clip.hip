@@ -6,8 +6,9 @@
 //   clip    one launch per kClipRecs tensors
 //
 // A tensor is cut into pieces of 32 KB at 16-byte addresses, so that every
-// whole group of 16 bytes is one load whatever element the tensor begins at; the
-// groups that its ends cut are read element by element.  Workgroup b takes
+// whole group of 16 bytes is one load whatever element the tensor begins at, and a
+// thread has all its loads of a piece in flight; the groups that its ends cut are read
+// an element a thread.  Workgroup b takes
 // pieces b, b + grid, ...: the launch sweeps over the tensors.
 #include <hip/hip_runtime.h>
 
@@ -26,33 +27,31 @@ constexpr int kThreads = 256;
 constexpr int kGroups = 8;                            // 16-byte groups a thread has in flight
 constexpr int kPiece = kThreads * kGroups * 16;       // bytes
 constexpr int kMostBlocks = 2048;                     // of a launch: 8 workgroups on each of 256 CUs
-constexpr int kNormRecs = 150, kClipRecs = 110;       // tensors of a launch: a table of at most 3.6 KB in its arguments
+constexpr int kNormRecs = 192, kClipRecs = 128;       // tensors of a launch: a table of 3.8 KB at most in its arguments
 constexpr int64_t kMostBytes = int64_t(1) << 45;      // of a tensor
 constexpr int64_t kMostPieces = int64_t(1) << 30;     // of a launch
 
 struct NormRec {
     const char* in;
-    int64_t bytes;
-    int32_t first;  // its first piece in the launch
-    int32_t bf16;
+    int64_t bytes_bf16;  // 2 bytes + whether it is bf16
 };
 struct NormArgs {
     double* sums;   // one per workgroup
     int32_t count, pieces;
+    int32_t first[kNormRecs];  // a tensor's first piece in the launch
     NormRec rec[kNormRecs];
 };
 
 struct ClipRec {
     const char* in;
     char* out;
-    int64_t bytes;
-    int32_t first;
-    int32_t bf16;
+    int64_t bytes_bf16;
 };
 struct ClipArgs {
     const float* norm;
     double max_norm, eps;
     int32_t count, pieces;
+    int32_t first[kClipRecs];
     ClipRec rec[kClipRecs];
 };
 
@@ -78,6 +77,33 @@ __device__ __forceinline__ void add_squares(double (&s)[2], const u32x4_t& u, bo
     }
 }
 
+// The record whose pieces hold piece c: the last whose first is at most c.  Every wave looks
+// at all of them at once: a search by halves waits for eight loads, one after the other.
+template <int RECS>
+__device__ __forceinline__ int record_of(const int32_t* first, int count, int c) {
+    static_assert(RECS % 64 == 0, "whole waves");
+    const int lane = (int)(threadIdx.x & 63u);
+    int at[RECS / 64], n = 0;
+    #pragma unroll
+    for (int k = 0; k < RECS / 64; ++k) at[k] = first[64 * k + lane];  // (what follows the records is not looked at)
+    #pragma unroll
+    for (int k = 0; k < RECS / 64; ++k) n += __popcll(__builtin_amdgcn_ballot_w64(64 * k + lane < count && at[k] <= c));
+    return __builtin_amdgcn_readfirstlane(n) - 1;
+}
+
+// A piece's elements are bytes lo .. hi - 1 of it.  Of the 16-byte groups that lo and hi cut
+// the workgroup's first 16 threads take an element each: this thread's place, or -1.
+template <int E>
+__device__ __forceinline__ int cut_element(int64_t lo, int64_t hi) {
+    const int t = (int)threadIdx.x, each = 16 / E;
+    const int begin = lo > 0 ? (int)lo : 0, end = hi < kPiece ? (int)hi : kPiece;
+    if (t >= 2 * each) return -1;
+    const int first = begin & ~15, last = (end - 1) & ~15;
+    const int at = t < each ? first : last, e = at + t % each * E;
+    const bool cut = at < begin || at + 16 > end;
+    return cut && e >= begin && e < end && (t < each || last != first) ? e : -1;
+}
+
 // Squares in 64 bits: the conversion and the addition of an element take two
 // instructions, which the loads hide, and no element is too large or too small
 // to be squared.
@@ -91,20 +117,23 @@ __device__ __forceinline__ void piece_squares(double (&s)[2], const char* base, 
         for (int j = 0; j < kGroups; ++j) add_squares(s, u[j], BF16);
         return;
     }
-    #pragma unroll 1
-    for (int j = 0; j < kGroups; ++j) {
+    u32x4_t u[kGroups];
+    auto whole = [&](int j) {
         const int off = (j * kThreads + (int)threadIdx.x) * 16;
-        if (off >= lo && off + 16 <= hi) {
-            add_squares(s, *reinterpret_cast<const u32x4_t*>(base + off), BF16);
-        } else if (off + 16 > lo && off < hi) {
-            constexpr int E = BF16 ? 2 : 4;
-            #pragma unroll 1
-            for (int e = off; e < off + 16; e += E)
-                if (e >= lo && e < hi) {
-                    if (BF16) add_square(s[0], bf16_to_f32(*reinterpret_cast<const uint16_t*>(base + e)));
-                    else add_square(s[0], *reinterpret_cast<const float*>(base + e));
-                }
-        }
+        return off >= lo && off + 16 <= hi;
+    };
+    #pragma unroll
+    for (int j = 0; j < kGroups; ++j)
+        if (whole(j)) u[j] = *reinterpret_cast<const u32x4_t*>(base + (j * kThreads + (int)threadIdx.x) * 16);
+    const int e = cut_element<BF16 ? 2 : 4>(lo, hi);
+    if (e >= 0) {
+        if (BF16) add_square(s[0], bf16_to_f32(*reinterpret_cast<const uint16_t*>(base + e)));
+        else add_square(s[0], *reinterpret_cast<const float*>(base + e));
+    }
+    #pragma unroll
+    for (int j = 0; j < kGroups; ++j) {
+        if (whole(j)) add_squares(s, u[j], BF16);
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
@@ -124,11 +153,12 @@ __device__ __forceinline__ double block_sum64(double v) {
 __global__ __launch_bounds__(kThreads) void norm_squares_kernel(NormArgs a) {
     double s[2] = {0.0, 0.0};
     for (int c = (int)blockIdx.x; c < a.pieces; c += (int)gridDim.x) {
-        const int i = upper_index(a.count, c, [&](int k) { return a.rec[k].first; });
+        const int i = record_of<kNormRecs>(a.first, a.count, c);
         const char* const in = a.rec[i].in;
-        const int64_t at = (int64_t)(c - a.rec[i].first) * kPiece - low4(in);  // of the piece in the tensor
-        if (a.rec[i].bf16) piece_squares<true>(s, in + at, -at, a.rec[i].bytes - at);
-        else piece_squares<false>(s, in + at, -at, a.rec[i].bytes - at);
+        const int64_t bytes = a.rec[i].bytes_bf16 >> 1;
+        const int64_t at = (int64_t)(c - a.first[i]) * kPiece - low4(in);  // of the piece in the tensor
+        if (a.rec[i].bytes_bf16 & 1) piece_squares<true>(s, in + at, -at, bytes - at);
+        else piece_squares<false>(s, in + at, -at, bytes - at);
     }
     const double total = block_sum64<kThreads>(s[0] + s[1]);
     if (threadIdx.x == 0) a.sums[blockIdx.x] = total;
@@ -169,22 +199,22 @@ __device__ __forceinline__ void piece_scaled(const char* in, char* out, int64_t 
             *reinterpret_cast<u32x4_t*>(out + (j * kThreads + (int)threadIdx.x) * 16) = scaled<BF16>(u[j], f);
         return;
     }
-    #pragma unroll 1
-    for (int j = 0; j < kGroups; ++j) {
+    u32x4_t u[kGroups];
+    auto whole = [&](int j) {
         const int off = (j * kThreads + (int)threadIdx.x) * 16;
-        if (off >= lo && off + 16 <= hi) {
-            *reinterpret_cast<u32x4_t*>(out + off) = scaled<BF16>(reinterpret_cast<const Any16*>(in + off)->v, f);
-        } else if (off + 16 > lo && off < hi) {
-            constexpr int E = BF16 ? 2 : 4;
-            #pragma unroll 1
-            for (int e = off; e < off + 16; e += E)
-                if (e >= lo && e < hi) {
-                    if (BF16) Elem<uint16_t>::store(reinterpret_cast<uint16_t*>(out + e),
-                                                    bf16_to_f32(*reinterpret_cast<const uint16_t*>(in + e)) * f);
-                    else *reinterpret_cast<float*>(out + e) = *reinterpret_cast<const float*>(in + e) * f;
-                }
-        }
+        return off >= lo && off + 16 <= hi;
+    };
+    #pragma unroll
+    for (int j = 0; j < kGroups; ++j)
+        if (whole(j)) u[j] = reinterpret_cast<const Any16*>(in + (j * kThreads + (int)threadIdx.x) * 16)->v;
+    const int e = cut_element<BF16 ? 2 : 4>(lo, hi);
+    if (e >= 0) {
+        if (BF16) Elem<uint16_t>::store(reinterpret_cast<uint16_t*>(out + e), bf16_to_f32(*reinterpret_cast<const uint16_t*>(in + e)) * f);
+        else *reinterpret_cast<float*>(out + e) = *reinterpret_cast<const float*>(in + e) * f;
     }
+    #pragma unroll
+    for (int j = 0; j < kGroups; ++j)
+        if (whole(j)) *reinterpret_cast<u32x4_t*>(out + (j * kThreads + (int)threadIdx.x) * 16) = scaled<BF16>(u[j], f);
 }
 
 __global__ __launch_bounds__(kThreads) void clip_kernel(ClipArgs a) {
@@ -193,13 +223,14 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(ClipArgs a) {
     // (a ratio that is NaN: both infinite, and nothing is to be clipped)
     const float f = norm != norm ? norm : ratio < 1.0 ? (float)ratio : 1.f;
     for (int c = a.pieces - 1 - (int)blockIdx.x; c >= 0; c -= (int)gridDim.x) {
-        const int i = upper_index(a.count, c, [&](int k) { return a.rec[k].first; });
+        const int i = record_of<kClipRecs>(a.first, a.count, c);
         const char* const in = a.rec[i].in;
         char* const out = a.rec[i].out;
         if (in == out && f == 1.f) continue;
-        const int64_t at = (int64_t)(c - a.rec[i].first) * kPiece - low4(out);
-        if (a.rec[i].bf16) piece_scaled<true>(in + at, out + at, -at, a.rec[i].bytes - at, f);
-        else piece_scaled<false>(in + at, out + at, -at, a.rec[i].bytes - at, f);
+        const int64_t bytes = a.rec[i].bytes_bf16 >> 1;
+        const int64_t at = (int64_t)(c - a.first[i]) * kPiece - low4(out);
+        if (a.rec[i].bytes_bf16 & 1) piece_scaled<true>(in + at, out + at, -at, bytes - at, f);
+        else piece_scaled<false>(in + at, out + at, -at, bytes - at, f);
     }
 }
 
@@ -297,8 +328,8 @@ dmuon_status norm(int32_t count, const int64_t* numels, const int32_t* dtypes, c
                       for (int32_t i = begin; i < end; ++i) {
                           if (numels[i] == 0) continue;
                           const int64_t bytes = numels[i] * element_bytes(dtypes[i]);
-                          a.rec[a.count++] = NormRec{static_cast<const char*>(grads[i]), bytes, first,
-                                                     dtypes[i] == DMUON_BF16};
+                          a.first[a.count] = first;
+                          a.rec[a.count++] = NormRec{static_cast<const char*>(grads[i]), 2 * bytes + (dtypes[i] == DMUON_BF16)};
                           first += (int32_t)pieces_of(bytes, (int64_t)(reinterpret_cast<uintptr_t>(grads[i]) & 15u));
                       }
                       const int blocks = blocks_of(pieces);
@@ -344,8 +375,9 @@ dmuon_status clip(int32_t count, const int64_t* numels, const int32_t* dtypes, c
         for (int32_t i = begin; i < end; ++i) {
             if (numels[i] == 0) continue;
             const int64_t bytes = numels[i] * element_bytes(dtypes[i]);
-            a.rec[a.count++] = ClipRec{static_cast<const char*>(grads[i]), static_cast<char*>(outs[i]), bytes, first,
-                                       dtypes[i] == DMUON_BF16};
+            a.first[a.count] = first;
+            a.rec[a.count++] = ClipRec{static_cast<const char*>(grads[i]), static_cast<char*>(outs[i]),
+                                       2 * bytes + (dtypes[i] == DMUON_BF16)};
             first += (int32_t)pieces_of(bytes, (int64_t)(where(i) & 15u));
         }
         hipLaunchKernelGGL(clip_kernel, dim3(blocks_of(pieces)), dim3(kThreads), 0, stream, a);

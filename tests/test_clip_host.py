@@ -59,10 +59,11 @@ def test_workspace_sizes():
     assert ws_bytes([], []) == (OK, 0)
     assert ws_bytes([0, 0], [BF16, F32]) == (OK, 0)
     assert ws_bytes([1], [BF16]) == (OK, 256)
-    # 2048 sums a launch at most, one launch per 150 tensors that are not empty
+    # 2048 sums a launch at most, one launch per 192 tensors that are not empty
     assert ws_bytes([1 << 33], [F32]) == (OK, 2048 * 8)
     assert ws_bytes([1 << 20] * 300 + [0] * 50, [BF16] * 350) == (OK, 2 * 2048 * 8)
     assert ws_bytes([1] * 151, [BF16] * 151) == (OK, (151 * 8 + 255) // 256 * 256)
+    assert ws_bytes([1] * 193, [F32] * 193) == (OK, (193 * 8 + 255) // 256 * 256)
     # 32 KB of bf16 that begin at their last possible place reach into a second piece
     assert ws_bytes([16384] * 32, [BF16] * 32) == (OK, 64 * 8)
 

@@ -80,7 +80,7 @@ def clipped_close(out, g, f):
 
 
 LISTS = [[1], [2], [7], [8], [9], [0, 3, 0], [15, 16, 17], [16383], [16384], [16385], [8191, 8192, 8193], [100001],
-         [1] * 150, [3] * 151, list(range(0, 401)), [40000] * 5 + [1] * 300, [1 << 21, 5]]
+         [1] * 150, [3] * 151, [1] * 192, [3] * 193, [9] * 129, list(range(0, 401)), [40000] * 5 + [1] * 300, [1 << 21, 5]]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
