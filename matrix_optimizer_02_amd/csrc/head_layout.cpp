@@ -219,6 +219,13 @@ ProbsLayout probs_layout_of(const dmuon_head_desc& d, bool backward) {
     dmuon_head_desc h = d;
     h.top_k = 0;
     L.head = head_layout_of(h, backward);
+    // Few rows read W at the rate of the memory, which a last round of the chip's slots that is
+    // not full costs less than the tiles' rule counts: 256 x 64 tiles wherever each slot has one.
+    // Against 64 x 64, us: 40 x 3584 x 152064, 20 alternatives, 249 / 274; 16 x 5120 x 151936
+    // 334 / 380; with half of the slots taken 64 x 2048 x 32000 63 / 57.
+    if (!backward && L.head.planes == 1 && !L.head.stream_weight && d.tokens <= 64 &&
+        ceil_div(d.vocab, 256) >= head_slots(256))
+        L.head.s_tile = HeadTile{256, 64};
     size_t at = L.head.bytes;
     auto take = [&](int64_t bytes) {
         const size_t o = at;

@@ -413,7 +413,7 @@ hipError_t launch_head_gemm(int mode, HeadTile tile, const HeadGemmArgs& a, int6
     if (max_tiles > (int64_t)0x3fffffff) return hipErrorInvalidValue;
     if (a.parts > 1 && (mode == kHeadDh || mode == kHeadDw || mode == kHeadDwSum)) return launch_head_x3(mode, tile, a, max_tiles, stream);
     if (tile.tp == 64) return launch_config<Config<64, 64, 4>>(mode, a, max_tiles, stream);
-    if (tile.tq == 64) return launch_config<Config<256, 64, 2>>(mode, a, max_tiles, stream);
+    if (tile.tq == 64) return launch_config<Config<256, 64, 3>>(mode, a, max_tiles, stream);
     if (tile.tq == 128) return launch_config<Config<256, 128, 3>>(mode, a, max_tiles, stream);
     if (a.parts == 1) return launch_head_wide(mode, a, max_tiles, stream);
     return launch_logits<Config<256, 256, 2>, kHeadHalf2>(mode, a, max_tiles, stream);
