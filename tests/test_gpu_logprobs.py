@@ -60,7 +60,6 @@ def test_alternatives_side_by_side(t, v, k, dtype):
     w[:, 0] = torch.arange(v, device="cuda") // 256   # a word's place, in two digits
     w[:, 1] = torch.arange(v, device="cuda") % 256
     w[:, 2] = 1.0
-    # -(place - middle)^2 / 2^k is no bilinear form: a table of its terms instead
     h = torch.zeros(t, dd, device="cuda")
     h[:, 0], h[:, 1] = 256.0, 1.0                     # logits rise with the id: the last K
     say("rising", t, v, k, dtype)

@@ -1,0 +1,89 @@
+"""The output head's log probabilities where sizes turn: many tiles a workgroup, more
+tokens than a chunk, more parts than a list holds, addresses past 32 bits."""
+
+import sys
+
+import pytest
+import torch
+
+import probs_device as pd
+from probs_device import BF16, F32
+
+pytestmark = pytest.mark.gpu
+
+
+def say(*a):
+    print(*a, flush=True)
+    sys.stdout.flush()
+
+
+@pytest.mark.parametrize("t,dd,v,k,dtype", [
+    (1531, 1536, 50257, 0, BF16), (2048, 64, 20011, 20, BF16), (2050, 396, 82304, 3, BF16), (4097, 192, 32000, 128, BF16),
+    (1029, 2048, 9001, 0, BF16), (1100, 1000, 17000, 40, F32), (2049, 128, 20000, 0, F32)])
+def test_several_tiles_a_workgroup(t, dd, v, k, dtype):
+    say("tiles", t, dd, v, k, dtype)
+    h, w, y, g, e = pd.inputs(t, dd, v, dtype, t, 0.2)
+    got = pd.run(h, w, y, k, 0.8, g, e)
+    pd.check(f"{t}x{dd}x{v}", got, h, w, y, k, 0.8, g, e, block=256)
+
+
+@pytest.mark.parametrize("t,v,k", [(14400, 152064, 3), (33100, 8000, 128)])
+def test_more_tokens_than_a_chunk(t, v, k):
+    """Chunks of tokens of calls with alternatives (their logits kept or not), the last one short."""
+    say("chunk", t, v, k)
+    h, w, y = pd.grid_inputs(t, 64, v, BF16, 9, 0.1)
+    got = pd.run(h, w, y, k)
+    pd.check("chunks", got, h, w, y, k, exact_ids=True, block=512)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("t,v,k", [(3, 200000, 128), (2, 3000001, 128), (1, 2200000, 1), (70, 600000, 100)])
+def test_many_words(t, v, k, dtype):
+    """More parts a thread than its list of candidates takes at once."""
+    say("words", t, v, k, dtype)
+    h, w, y = pd.grid_inputs(t, 64, v, dtype, v)
+    got = pd.run(h, w, y, k)
+    pd.check(f"{v} words", got, h, w, y, k, exact_ids=True, block=8)
+
+
+@pytest.mark.parametrize("t,k", [(2, 20), (300, 20), (300, 0)])
+def test_weights_past_32_bits(t, k):
+    dd, v = 4096, 600000
+    say("weights", t, k)
+    gen = torch.Generator("cuda").manual_seed(t)
+    w = torch.empty(v, dd, device="cuda", dtype=BF16)
+    for r in range(0, v, 100000):
+        w[r:r + 100000] = (torch.randn(100000, dd, device="cuda", generator=gen) / 64).to(BF16)
+    h = torch.randn(t, dd, device="cuda", generator=gen).to(BF16)
+    h[0] = w[-1] * 40  # its first alternative lies at the end
+    y = torch.randint(v - 1000, v, (t,), device="cuda", generator=gen)
+    got = pd.run(h, w, y, k)
+    pd.check("weights", got, h, w, y, k, block=64)
+    assert k == 0 or int(got["top_ids"][0, 0]) == v - 1
+
+
+def test_statistics_past_32_bits():
+    t, v = 240000, 152064
+    say("statistics")
+    h, w, y, _, _ = pd.inputs(t, 64, v, BF16, 1, 0.0)
+    got = pd.run(h, w, y, 0)
+    for rows in (slice(0, 50), slice(t - 50, t)):
+        pd.check(f"rows {rows}", {n: x[rows] for n, x in got.items()}, h[rows], w, y[rows], 0)
+
+
+@pytest.mark.parametrize("t", [40, 300])
+def test_rows_of_a_wide_range_with_alternatives(t):
+    """fp32 rows whose small elements carry the logits: the products of three parts, and groups formed again."""
+    say("wide range", t)
+    dd, v, k = 256, 9000, 60
+    gen = torch.Generator("cuda").manual_seed(6)
+    h = torch.randn(t, dd, device="cuda", generator=gen)
+    w = torch.randn(v, dd, device="cuda", generator=gen)
+    h[:, 0], w[:, 0] = 2.0 ** 24, 2.0 ** -24
+    w[:, 1:] *= 0.5
+    # runs of words that differ little, so that a group holds several of a row's alternatives
+    w[16:32] = w[16:17] * (1 + torch.arange(16, device="cuda")[:, None] * 2.0 ** -10)
+    h[:, 1:] += 0.1 * w[16, 1:]
+    y = torch.randint(0, v, (t,), device="cuda", generator=gen)
+    got = pd.run(h, w, y, k)
+    pd.check("wide range", got, h, w, y, k)
