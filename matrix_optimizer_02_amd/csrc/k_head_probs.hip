@@ -17,7 +17,8 @@
 // words, once for K = 128.
 //
 // What bounds it: latency.  The largest of n values are found by counting how many reach
-// a threshold, two bits of it a round.
+// a threshold, two bits of it a round.  A row of 128256 words, 20 alternatives: 15 us (5 of
+// them the statistics), 27 where a group is opened; 2048 rows with 5 55 us, 4096 with 64 125.
 #include "head_internal.h"
 #include "kcommon.h"
 
@@ -104,6 +105,7 @@ __device__ __forceinline__ int largest(const uint32_t* o, const uint32_t* p, int
         int4 s = make_int4(0, 0, 0, 0);
         #pragma unroll
         for (int u = 0; u < PER; ++u) {
+            if (u > 0 && u * kThreads >= n) break;
             s.x += __popcll(__builtin_amdgcn_ballot_w64(x[u] >= a));
             s.y += __popcll(__builtin_amdgcn_ballot_w64(x[u] >= b));
             s.z += __popcll(__builtin_amdgcn_ballot_w64(x[u] >= c));
@@ -299,7 +301,8 @@ __global__ __launch_bounds__(kThreads) void probs_logits_kernel(HeadProbsArgs a)
     write_top(a, t, sorted, held, r);
 }
 
-// One wave: the logits of a row of H and four rows of W.
+// One wave: the logits of a row of H and four rows of W, kDeep loads of each on their way.
+constexpr int kDeep = 4;
 template <int ESIZE>
 __device__ __forceinline__ void dots(const HeadProbsArgs& a, int64_t t, const uint32_t (&word)[4], float (&s)[4]) {
     const int lane = threadIdx.x & 63;
@@ -309,18 +312,28 @@ __device__ __forceinline__ void dots(const HeadProbsArgs& a, int64_t t, const ui
         const uint16_t* h = static_cast<const uint16_t*>(a.hidden) + t * a.cols;
         const uint16_t* w = static_cast<const uint16_t*>(a.weight);
         if (a.cols % 8 == 0) {
-            #pragma unroll 2
-            for (int64_t d = lane * 8; d < a.cols; d += 512) {
-                const uint4 u = *reinterpret_cast<const uint4*>(h + d);
-                const uint32_t us[4] = {u.x, u.y, u.z, u.w};
+            #pragma unroll 1
+            for (int64_t d0 = lane * 8; d0 < a.cols; d0 += 512 * kDeep) {
+                uint4 u[kDeep], v[kDeep][4];
                 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(w + word[q] * a.cols + d);
-                    const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
+                for (int i = 0; i < kDeep; ++i) {
+                    const int64_t d = min(d0 + 512 * i, a.cols - 8);
+                    u[i] = *reinterpret_cast<const uint4*>(h + d);
                     #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        s[q] = fmaf(__uint_as_float(us[e] << 16), __uint_as_float(vs[e] << 16), s[q]);
-                        s[q] = fmaf(__uint_as_float(us[e] & 0xffff0000u), __uint_as_float(vs[e] & 0xffff0000u), s[q]);
+                    for (int q = 0; q < 4; ++q) v[i][q] = *reinterpret_cast<const uint4*>(w + word[q] * a.cols + d);
+                }
+                #pragma unroll
+                for (int i = 0; i < kDeep; ++i) {
+                    if (d0 + 512 * i >= a.cols) break;
+                    const uint32_t us[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                    #pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t vs[4] = {v[i][q].x, v[i][q].y, v[i][q].z, v[i][q].w};
+                        #pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            s[q] = fmaf(__uint_as_float(us[e] << 16), __uint_as_float(vs[e] << 16), s[q]);
+                            s[q] = fmaf(__uint_as_float(us[e] & 0xffff0000u), __uint_as_float(vs[e] & 0xffff0000u), s[q]);
+                        }
                     }
                 }
             }
@@ -335,13 +348,22 @@ __device__ __forceinline__ void dots(const HeadProbsArgs& a, int64_t t, const ui
         const float* h = static_cast<const float*>(a.hidden) + t * a.cols;
         const float* w = static_cast<const float*>(a.weight);
         if (a.cols % 4 == 0) {
-            #pragma unroll 2
-            for (int64_t d = lane * 4; d < a.cols; d += 256) {
-                const float4 u = *reinterpret_cast<const float4*>(h + d);
+            #pragma unroll 1
+            for (int64_t d0 = lane * 4; d0 < a.cols; d0 += 256 * kDeep) {
+                float4 u[kDeep], v[kDeep][4];
                 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float4 v = *reinterpret_cast<const float4*>(w + word[q] * a.cols + d);
-                    s[q] = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, s[q]))));
+                for (int i = 0; i < kDeep; ++i) {
+                    const int64_t d = min(d0 + 256 * i, a.cols - 4);
+                    u[i] = *reinterpret_cast<const float4*>(h + d);
+                    #pragma unroll
+                    for (int q = 0; q < 4; ++q) v[i][q] = *reinterpret_cast<const float4*>(w + word[q] * a.cols + d);
+                }
+                #pragma unroll
+                for (int i = 0; i < kDeep; ++i) {
+                    if (d0 + 256 * i >= a.cols) break;
+                    #pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        s[q] = fmaf(u[i].x, v[i][q].x, fmaf(u[i].y, v[i][q].y, fmaf(u[i].z, v[i][q].z, fmaf(u[i].w, v[i][q].w, s[q]))));
                 }
             }
         } else {
@@ -370,6 +392,7 @@ __device__ __forceinline__ uint32_t second_order(float shown) {
     return order_of(__uint_as_float(u >> 31 ? u & ~15u : u | 15u));
 }
 
+constexpr int kFew = 2;              // a round leaves up to kFew K candidates: fewer take more steps to find
 constexpr int kList = 512;           // of threads, then parts, that may hold alternatives
 constexpr int kPool = kK + kK * 16;  // candidates after groups are opened
 constexpr int kPoolPer = (kPool + kThreads - 1) / kThreads;
@@ -404,10 +427,10 @@ __global__ __launch_bounds__(kThreads) void probs_groups_kernel(HeadProbsArgs a)
     int n = kThreads, threads = 0, first = 0, held = 0;
     #pragma unroll 1
     for (;;) {
-        const int most = stage == kOfThreads ? min(kThreads, max(a.k, kPool / per))
-                         : stage == kOfParts ? min(kList, kPool / groups) : kK;
+        const int most = stage == kOfThreads ? min(kThreads, max(a.k, min(kFew * a.k, kPool / per)))
+                         : stage == kOfParts ? min(kList, max(a.k, min(kFew * a.k, kPool / groups))) : kK;
         // (all threads' parts may fit the next round as they are)
-        const bool all = stage == kOfThreads && kThreads * per <= kPool;
+        const bool all = stage == kOfThreads && most == kThreads && kThreads * per <= kPool;
         const int got = all ? kThreads : largest<kPoolPer>(orders, places, n, a.k, most, keys, &taken, red);
         if (stage >= kOfGroups) {
             held = sort_keys(keys, got, a.k, sorted);
