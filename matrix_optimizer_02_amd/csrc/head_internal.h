@@ -24,7 +24,7 @@ enum HeadMode : int32_t {
     kHeadDh = 2,    // P = W (k = vocab rows, columns of hidden), Q = ds rows: fp32 sums, added per piece
     kHeadDw = 3,    // P = H (k = tokens, columns of hidden), Q = ds (k = tokens, columns of vocab): dW rows
     kHeadDwSum = 4,  // the same in splits of the tokens: fp32 sums
-    kHeadGradEntropy = 5, // as Grad, with the entropy's gradient
+    kHeadGradEntropy = 5,  // as Grad, with the entropy's gradient
     kHeadProbs = 6,  // as Lse, with the sum that the entropy takes
     kHeadTop = 7     // ... and what every group of 16 words shows of its largest logits
 };
@@ -55,7 +55,7 @@ struct HeadGemmArgs {
     int64_t t_pad;
     int32_t first_tile;          // vocab tile index of the piece's first tile
     float* target_logit;
-    float* logits;               // Lse: the logits too (row stride logits_ld), or null
+    float* logits;               // Lse, Probs: the logits too (row stride logits_ld), or null
     int32_t logits_ld;
     int64_t row_parts;           // Probs, Top: part[row * row_parts + i] instead, and likewise ...
     float* part_e;               // ... the part's sum of p log2 p (p relative to its largest)
@@ -79,7 +79,7 @@ struct HeadGemmArgs {
 };
 
 hipError_t launch_head_gemm(int mode, HeadTile tile, const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream);
-// ... Probs and Top of bf16 operands, 256 x 256 tiles (k_head_wide.hip).
+// ... in 256 x 256 tiles of bf16 operands (k_head_wide.hip).
 hipError_t launch_head_wide(int mode, const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream);
 // ... dH and dW of fp32 operands (k_head_x3.hip).
 hipError_t launch_head_x3(int mode, HeadTile tile, const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream);

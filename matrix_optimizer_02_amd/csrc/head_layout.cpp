@@ -223,7 +223,8 @@ ProbsLayout probs_layout_of(const dmuon_head_desc& d, bool backward) {
     // not full costs less than the tiles' rule counts: 256 x 64 tiles wherever each slot has one.
     // Against 64 x 64, us: 40 x 3584 x 152064, 20 alternatives, 249 / 274; 16 x 5120 x 151936
     // 334 / 380; with half of the slots taken 64 x 2048 x 32000 63 / 57.
-    if (!backward && L.head.planes == 1 && !L.head.stream_weight && d.tokens <= 64 &&
+    // (Fewer parts a row than of 64 x 64: the arrays hold them.)
+    if (!backward && L.head.planes == 1 && !L.head.stream_weight && d.tokens <= 64 && L.head.s_tile.tp == 64 &&
         ceil_div(d.vocab, 256) >= head_slots(256))
         L.head.s_tile = HeadTile{256, 64};
     size_t at = L.head.bytes;

@@ -1,7 +1,9 @@
-// The products of the output-head losses on bf16 MFMA (gfx950), one tile
-// kernel in five modes, each C[r][c] = sum over k of P[r][k] Q[c][k]:
-//   Lse   s^T = W H^T     softmax statistics of every vocab tile
-//   Grad  s^T = W H^T     again, ds = cp exp(s / T - lse) - ct [target] out
+// The products of the output head on bf16 MFMA (gfx950), one tile kernel in
+// eight modes, each C[r][c] = sum over k of P[r][k] Q[c][k]:
+//   Lse   s^T = W H^T     softmax statistics of every vocab tile (Probs: with the sum for the
+//         entropy; Top: with what groups of words show of their largest logits)
+//   Grad  s^T = W H^T     again, ds = cp exp(s / T - lse) - ct [target] out (GradEntropy: cp
+//         with a multiple of log p)
 //   dH    dH^T = W^T ds^T  k over the vocab rows of the piece, fp32 sums
 //   dW    dW^T = H^T ds    k over the tokens (DwSum: in splits of them, fp32 sums)
 // s itself never leaves the registers.  With the vocabulary along the tile's P
