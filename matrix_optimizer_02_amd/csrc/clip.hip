@@ -297,24 +297,23 @@ dmuon_status norm(int32_t count, const int64_t* numels, const int32_t* dtypes, c
     dmuon_status st = check_sizes(count, numels, dtypes);
     if (st != DMUON_OK) return st;
     if (!at_element(out, DMUON_F32) || (count > 0 && grads == nullptr)) return DMUON_ERR_INVALID_ARG;
-    std::vector<Span> spans;
-    spans.reserve((size_t)count + 2);
-    for (int32_t i = 0; i < count; ++i) {
-        if (numels[i] == 0) continue;
-        if (!at_element(grads[i], dtypes[i])) return DMUON_ERR_INVALID_ARG;
-        spans.push_back(span_of(grads[i], numels[i] * element_bytes(dtypes[i]), false));
-    }
     int64_t sums = 0;
     st = most_sums(count, numels, dtypes, &sums);
     if (st != DMUON_OK) return st;
-    spans.push_back(span_of(out, 4, true));
-    if (sums > 0) {
-        if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0 ||
-            workspace_bytes < align_up((size_t)sums * 8))
-            return DMUON_ERR_WORKSPACE;
-        spans.push_back(span_of(workspace, sums * 8, true));
+    if (sums > 0 && (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0 ||
+                     workspace_bytes < align_up((size_t)sums * 8)))
+        st = DMUON_ERR_WORKSPACE;
+    // (the gradients are only read: each has to miss the two that are written)
+    const Span to = span_of(out, 4, true), ws_span = span_of(sums > 0 ? workspace : nullptr, sums * 8, true);
+    auto meet = [](const Span& x, const Span& y) { return x.lo < y.hi && y.lo < x.hi; };
+    for (int32_t i = 0; i < count; ++i) {
+        if (numels[i] == 0) continue;
+        if (!at_element(grads[i], dtypes[i])) return DMUON_ERR_INVALID_ARG;
+        const Span g = span_of(grads[i], numels[i] * element_bytes(dtypes[i]), false);
+        if (meet(g, to) || (st == DMUON_OK && meet(g, ws_span))) return DMUON_ERR_INVALID_ARG;
     }
-    if (!disjoint_where_written(spans)) return DMUON_ERR_INVALID_ARG;
+    if (st != DMUON_OK) return st;
+    if (meet(to, ws_span)) return DMUON_ERR_INVALID_ARG;
 
     double* const ws = static_cast<double*>(workspace);
     int32_t used = 0;

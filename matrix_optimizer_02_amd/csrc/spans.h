@@ -18,7 +18,8 @@ struct Span {
 // harmless).  Sorted by start, a span overlaps an earlier one exactly when it
 // starts below that one's end, so one sweep suffices.
 inline bool disjoint_where_written(std::vector<Span>& v) {
-    std::sort(v.begin(), v.end(), [](const Span& x, const Span& y) { return x.lo < y.lo; });
+    const auto before = [](const Span& x, const Span& y) { return x.lo < y.lo; };
+    if (!std::is_sorted(v.begin(), v.end(), before)) std::sort(v.begin(), v.end(), before);
     uintptr_t end_any = 0, end_written = 0;
     for (const Span& sp : v) {
         if (sp.lo < end_written || (sp.written && sp.lo < end_any)) return false;

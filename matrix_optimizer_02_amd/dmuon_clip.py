@@ -72,8 +72,14 @@ def _outputs(grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor
     return _Table(outs, "outs")
 
 
+def _here(t: torch.Tensor, what: str) -> None:
+    # (the short way of what follows, for calls of a few microseconds)
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        _on_current_device(t, what)
+
+
 def _scalar(norm: torch.Tensor) -> ctypes.c_void_p:
-    _on_current_device(norm, "norm")
+    _here(norm, "norm")
     if norm.numel() != 1 or norm.dtype is not torch.float32:
         raise ValueError(f"norm: expected one float32, got {norm.dtype} {tuple(norm.shape)}")
     return ctypes.c_void_p(norm.data_ptr())
@@ -89,7 +95,7 @@ def _workspace_bytes(table: _Table) -> int:
 def _norm(table: _Table, norm, workspace, stream):
     if workspace is None:
         raise ValueError("workspace is required (see norm_workspace_for)")
-    _on_current_device(workspace, "workspace")
+    _here(workspace, "workspace")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     _check(_lib.grad_norm_batched(table.count, table.numels, table.dtypes, table.pointers, _scalar(norm),
