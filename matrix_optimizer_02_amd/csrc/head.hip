@@ -485,6 +485,7 @@ dmuon_status backward(const Call& c, const Upstream& u, void* grad_hidden, void*
     if (st != DMUON_OK) return st;
     const int64_t dh_tiles_j = ceil_div(L.low ? 2 * head_low_row((int)L.tokens) : L.tokens, L.dh_tile.tq);
     const int32_t dh_tiles_i = (int32_t)ceil_div(L.hidden, L.dh_tile.tp);
+    const int64_t dh_first_k = round_up(std::min(L.piece, L.vocab), kHeadSlab);  // K of the first piece
     for (int64_t v0 = 0; v0 < L.vocab; v0 += L.piece) {
         const int64_t left = std::min(L.piece, L.vocab - v0);
         HeadGemmArgs w{};
@@ -532,11 +533,13 @@ dmuon_status backward(const Call& c, const Upstream& u, void* grad_hidden, void*
             h.k = (int32_t)round_up(left, kHeadSlab);
             h.split_k = (int32_t)L.split_k;
             h.splits = (int32_t)ceil_div(h.k, L.split_k);
+            h.room = L.dh_room;
+            h.first_k = (int32_t)dh_first_k;
             h.tiles_i = dh_tiles_i;
             h.sums = v.at<float>(L.off_dh);
             h.accumulate = v0 != 0;
             const auto launch = L.stream_weight ? launch_head_stream : launch_head_gemm;
-            HEAD_TRY(launch(kHeadDh, L.dh_tile, h, h.splits * dh_tiles_i * dh_tiles_j, c.stream));
+            HEAD_TRY(launch(kHeadDh, L.dh_tile, h, L.dh_room != 0 ? L.dh_room : h.splits * dh_tiles_i * dh_tiles_j, c.stream));
         }
         if (grad_weight != nullptr) {
             HeadGemmArgs g{};
@@ -582,6 +585,8 @@ dmuon_status backward(const Call& c, const Upstream& u, void* grad_hidden, void*
         h.low = L.low;
         h.sums = v.at<float>(L.off_dh);
         h.splits = L.splits;
+        h.room = L.dh_room;
+        h.first_k = (int32_t)dh_first_k;
         h.tiles_i = dh_tiles_i;
         h.tile = L.dh_tile;
         h.out = grad_hidden;

@@ -44,6 +44,7 @@ struct HeadGemmArgs {
     int32_t parts;               // 1: bf16; 3: fp32
     int32_t k;                   // K extent (dH: of the piece; dW: taken from count)
     int32_t split_k, splits;     // dH: K of a split; DwSum: splits of the tokens
+    int32_t room, first_k;       // dH: if room, splits by head_dh_splits for the first piece's first_k instead
     int32_t tiles_i;             // tiles along P's rows (or columns)
     int32_t tiles_j;             // tiles along Q's (dW: vocab); else from count
     // softmax
@@ -248,6 +249,7 @@ struct HeadSumArgs {
     int32_t low;
     const float* sums;
     int32_t splits;
+    int32_t room, first_k; // as in HeadGemmArgs
     int32_t tiles_i;
     HeadTile tile;
     void* out;

@@ -87,7 +87,7 @@ dmuon_status head_check_desc(const dmuon_head_desc* d) {
     return DMUON_OK;
 }
 
-HeadLayout head_layout_of(dmuon_head_desc d, bool backward) {
+HeadLayout head_layout_of(dmuon_head_desc d, bool backward, bool split_live) {
     HeadLayout L{};
     d.tokens = std::max<int64_t>(d.tokens, 1);
     L.tokens = d.tokens;
@@ -176,7 +176,20 @@ HeadLayout head_layout_of(dmuon_head_desc d, bool backward) {
     }
     if (backward) {
         L.off_g = take(2 * L.planes * L.t_pad * L.piece);
-        L.off_dh = take(4 * L.splits * L.t_pad * round_up(L.hidden, kHeadTile));
+        // Tiles of rows that take no part leave slots empty, which only the device knows: with
+        // room for twice the splits it fills them (8192 tokens, hidden 4096, 5734 of them
+        // live: 368 tiles on 256 slots take two rounds, 736 of half the length three).  Backward
+        // without dW, us, against the splits of all rows: 8192 x 4096 x 128256, 30% dead 10201 /
+        // 11098, 40% 8969 / 10199, 90% 1862 / 3272, none 13460 / 13456.  Calls of
+        // so many tiles that a round is a small part keep theirs; so do the losses, whose
+        // results would round differently.
+        int64_t splits_held = L.splits;
+        const int64_t dh_tiles = ceil_div(L.hidden, kHeadTile) * (L.t_pad / kHeadTile);
+        if (split_live && !f32 && L.dh_tile.tq == kHeadTile && dh_tiles * L.splits <= 4 * head_slots(kHeadTile)) {
+            splits_held = 2 * L.splits;
+            L.dh_room = (int32_t)(splits_held * dh_tiles);
+        }
+        L.off_dh = take(4 * splits_held * L.t_pad * round_up(L.hidden, kHeadTile));
         if (L.dw_splits > 1) L.off_dw = take(4 * L.dw_splits * L.piece * round_up(L.hidden, kHeadTile));
     } else {
         // Distillation needs K logits a token.  Dots of H's rows with the gathered rows of W
@@ -218,7 +231,7 @@ ProbsLayout probs_layout_of(const dmuon_head_desc& d, bool backward) {
     ProbsLayout L{};
     dmuon_head_desc h = d;
     h.top_k = 0;
-    L.head = head_layout_of(h, backward);
+    L.head = head_layout_of(h, backward, true);
     // Few rows read W at the rate of the memory, which a last round of the chip's slots that is
     // not full costs less than the tiles' rule counts: 256 x 64 tiles wherever each slot has one.
     // Against 64 x 64, us: 40 x 3584 x 152064, 20 alternatives, 249 / 274; 16 x 5120 x 151936

@@ -63,6 +63,7 @@ struct HeadLayout {
     int32_t pieces;
     int64_t split_k;        // dH: vocab rows of a split (multiple of 64)
     int32_t splits;         // ... splits of a full piece
+    int32_t dh_room;        // tiles that the sums of dH hold, where the device chooses the splits (else 0)
     int32_t dw_splits;      // dW: splits of the tokens
     int32_t keep_logits;    // distillation, small vocabularies: see head_layout.cpp
     // byte offsets
@@ -76,10 +77,27 @@ struct HeadLayout {
 inline int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 inline int64_t ceil_div(int64_t x, int64_t a) { return (x + a - 1) / a; }
 
+// Splits of dH's K, of `slabs` slabs, for so many tiles of 256 x 256 in an array that holds
+// `room` of them: the fewest rounds of the chip's slots.  A round's sums are written, and
+// read to be added to, at what kHeadSumSlabs slabs take.
+constexpr int kHeadSumSlabs = 20, kHeadMostSplits = 16;
+constexpr int head_dh_splits(int tiles, int slabs, int room) {
+    int best = 1, least = INT32_MAX;
+    for (int s = 1; s <= kHeadMostSplits && s <= slabs && s * tiles <= room; ++s) {
+        const int cost = ((s * tiles + 255) / 256) * ((slabs + s - 1) / s + kHeadSumSlabs);
+        if (cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
 // INVALID_ARG or UNSUPPORTED for sizes out of range.
 dmuon_status head_check_desc(const dmuon_head_desc* d);
-// The cut of one call (a descriptor that head_check_desc accepts).
-HeadLayout head_layout_of(dmuon_head_desc d, bool backward);
+// The cut of one call (a descriptor that head_check_desc accepts).  With split_live the
+// device cuts dH's K by the rows that take part (dh_room).
+HeadLayout head_layout_of(dmuon_head_desc d, bool backward, bool split_live = false);
 
 // The log probabilities: arrays beside those of a head loss.  The forward call takes a
 // chunk of the tokens at a time.

@@ -111,11 +111,11 @@ struct Share {
     int tiles_j, per_split, first, count, at, step;
 };
 template <int TQ, int MODE>
-__device__ __forceinline__ Share share_of(const HeadGemmArgs& args, int n, int n_k) {
+__device__ __forceinline__ Share share_of(const HeadGemmArgs& args, int n, int n_k, int splits) {
     Share s;
     s.tiles_j = is_dw(MODE) ? args.tiles_j : ((is_grad(MODE) ? n_k : n) + TQ - 1) / TQ;
     s.per_split = args.tiles_i * s.tiles_j;
-    const int total = s.per_split * (MODE == kHeadDh || MODE == kHeadDwSum ? args.splits : 1);
+    const int total = s.per_split * (MODE == kHeadDh || MODE == kHeadDwSum ? splits : 1);
     const int x = (int)(blockIdx.x % kXcds);
     s.step = ((int)gridDim.x - x + kXcds - 1) / kXcds;
     const int each = total / kXcds, rem = total % kXcds;

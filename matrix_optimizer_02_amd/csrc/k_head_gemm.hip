@@ -61,7 +61,7 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
     // ---- which tiles -----------------------------------------------------------------
     const int n = __builtin_amdgcn_readfirstlane(*args.count);
     const int n_k = n <= kBK ? kBK : (n + kBK - 1) / kBK * kBK;  // dW's K extent
-    const Share sh = share_of<TQ, MODE>(args, n, n_k);
+    const Share sh = share_of<TQ, MODE>(args, n, n_k, args.splits);
     // Where a tile's slabs come from, and its K extent (a multiple of kBK).
     struct Plan {
         Tile t;

@@ -536,6 +536,12 @@ __global__ __launch_bounds__(kRowThreads) void head_sum_kernel(HeadSumArgs a) {
     const int low_row = a.low ? head_low_row(n) : 0;
     const int tiles_j = (n + TQ - 1) / TQ;  // of the rows themselves
     const int64_t per_split = (int64_t)((a.low ? 2 * low_row : n) + TQ - 1) / TQ * a.tiles_i * (TP * TQ);
+    int splits = a.splits;
+    if (a.room != 0) {
+        const int slabs = a.first_k / kHeadSlab, s = head_dh_splits(tiles_j * a.tiles_i, slabs, a.room);
+        const int per = (slabs + s - 1) / s;
+        splits = (slabs + per - 1) / per;
+    }
     const int lane = threadIdx.x & 63;
     const float norm = *a.norm > 0.f ? *a.norm : 1.f;
     const int64_t groups = (int64_t)tiles_j * a.tiles_i * kGroups;
@@ -555,7 +561,7 @@ __global__ __launch_bounds__(kRowThreads) void head_sum_kernel(HeadSumArgs a) {
         auto add = [&](int64_t group) {
             const float* p = a.sums + group * 256 + lane * 4;
             #pragma unroll 4
-            for (int k = 0; k < a.splits; ++k) {
+            for (int k = 0; k < splits; ++k) {
                 const float4 u = *reinterpret_cast<const float4*>(p + k * per_split);
                 s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
             }

@@ -112,7 +112,7 @@ __global__ __launch_bounds__(S::C::NT, S::C::NT == 512 ? 1 : 2) void head_stream
     if (S::F32 && !PW && args.q_range != nullptr && !wide_range<NT>(args, reinterpret_cast<float4*>(smem))) return;
     const int n = __builtin_amdgcn_readfirstlane(*args.count);
     const int n_k = n <= kBK ? kBK : (n + kBK - 1) / kBK * kBK;
-    const Share sh = share_of<TQ, MODE>(args, n, n_k);
+    const Share sh = share_of<TQ, MODE>(args, n, n_k, args.splits);
     const int cols = args.p_ld;  // of W
 
     for (int kq = sh.at; kq < sh.count; kq += sh.step) {

@@ -114,7 +114,13 @@ __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1)
 
     const int n = __builtin_amdgcn_readfirstlane(*args.count);
     const int n_k = n <= kBK ? kBK : (n + kBK - 1) / kBK * kBK;
-    const Share sh = share_of<kWT, MODE>(args, n, n_k);
+    int split_k = args.split_k, splits = args.splits;
+    if (MODE == kHeadDh && args.room != 0) {
+        const int slabs = args.first_k / kBK, s = head_dh_splits((n + kWT - 1) / kWT * args.tiles_i, slabs, args.room);
+        split_k = (slabs + s - 1) / s * kBK;
+        splits = (args.k + split_k - 1) / split_k;
+    }
+    const Share sh = share_of<kWT, MODE>(args, n, n_k, splits);
     if (sh.at >= sh.count) return;
     // K extent of a tile: its first k and its slabs (a last split may have none: it then
     // multiplies one for nothing)
@@ -122,12 +128,12 @@ __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1)
         first = 0;
         int k = args.k;
         if (MODE == kHeadDh) {
-            first = t.split * args.split_k;
-            k = imin(args.split_k, args.k - first);
+            first = t.split * split_k;
+            k = imin(split_k, args.k - first);
         } else if (MODE == kHeadDw) {
             k = n_k;
         } else if (MODE == kHeadDwSum) {
-            const int per = (n_k / kBK + args.splits - 1) / args.splits * kBK;
+            const int per = (n_k / kBK + splits - 1) / splits * kBK;
             first = t.split * per;
             k = imin(per, n_k - first);
         }

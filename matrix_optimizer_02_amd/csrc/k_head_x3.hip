@@ -59,7 +59,7 @@ __global__ __launch_bounds__(S::C::NT, S::C::NT == 512 ? 1 : 2) void head_x3_ker
     const int lrow = lane & 31, khalf = lane >> 5;
     const int n = __builtin_amdgcn_readfirstlane(*args.count);
     const int n_k = n <= kBK ? kBK : (n + kBK - 1) / kBK * kBK;
-    const Share sh = share_of<TQ, MODE>(args, n, n_k);
+    const Share sh = share_of<TQ, MODE>(args, n, n_k, args.splits);
 
     for (int kq = sh.at; kq < sh.count; kq += sh.step) {
         const Tile t = tile_at(args, sh, kq);

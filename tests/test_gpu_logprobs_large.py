@@ -27,6 +27,17 @@ def test_several_tiles_a_workgroup(t, dd, v, k, dtype):
     pd.check(f"{t}x{dd}x{v}", got, h, w, y, k, 0.8, g, e, block=256)
 
 
+@pytest.mark.parametrize("dead", [0.0, 0.3, 0.55, 0.9, 0.9995])
+@pytest.mark.parametrize("t,dd,v", [(4200, 320, 70001), (1100, 1024, 40000)])
+def test_rows_that_take_no_part(t, dd, v, dead):
+    """dH's vocabulary is cut by the rows that take part, over pieces of which the last is short."""
+    say("dead", t, dd, v, dead)
+    h, w, y, g, e = pd.inputs(t, dd, v, BF16, t, dead)
+    y[5], h[5], g[5], e[5] = 1, 0.5, 0.01, 0.01  # (one at least does)
+    got = pd.run(h, w, y, 0, 1.0, g, e)
+    pd.check(f"{t}x{dd}x{v}, {dead}", got, h, w, y, 0, 1.0, g, e, block=256)
+
+
 @pytest.mark.parametrize("t,v,k", [(14400, 152064, 3), (33100, 8000, 128)])
 def test_more_tokens_than_a_chunk(t, v, k):
     """Chunks of tokens of calls with alternatives (their logits kept or not), the last one short."""
