@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import probs_device as pd
+from matrix_optimizer_02_amd import dmuon_logprobs as lp
 from probs_device import BF16, F32
 
 pytestmark = pytest.mark.gpu
@@ -98,3 +99,57 @@ def test_rows_of_a_wide_range_with_alternatives(t):
     y = torch.randint(0, v, (t,), device="cuda", generator=gen)
     got = pd.run(h, w, y, k)
     pd.check("wide range", got, h, w, y, k)
+
+
+def outputs(t, dd, v):
+    f = lambda *s, dt=F32: torch.empty(s, dtype=dt, device="cuda")
+    return dict(lse=f(t), logprobs=f(t), entropy=f(t), dh=f(t, dd, dt=BF16), dw=f(v, dd, dt=BF16))
+
+
+def step(h, w, y, g, e, o, ws):
+    lp.head_log_probs_forward(h, w, y, o["logprobs"], o["entropy"], o["lse"], workspace=ws)
+    lp.head_log_probs_backward(h, w, y, o["lse"], o["entropy"], g, e, o["dh"], o["dw"], workspace=ws)
+
+
+def test_replayed_with_other_rows():
+    """A captured training step whose rows that take part change from replay to replay."""
+    say("replayed")
+    t, dd, v = 1300, 512, 30000
+    h, w, y, g, e = pd.inputs(t, dd, v, BF16, 3)
+    ws, o = pd.workspace(t, dd, v, BF16), outputs(t, dd, v)
+    step(h, w, y, g, e, o, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(h, w, y, g, e, o, ws)
+    first = y.clone()
+    for dead in (0.0, 0.5, 0.95, 0.2, 1.0):
+        y.copy_(torch.where(torch.rand(t, device="cuda") < dead, pd.IGN, first))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {n: x.clone() for n, x in o.items()}
+        step(h, w, y, g, e, o, ws)
+        torch.cuda.synchronize()
+        for n in o:
+            assert torch.equal(got[n], o[n]), (dead, n)
+        pd.check(f"{dead} dead", got, h, w, y, 0, 1.0, g, e, block=256)
+
+
+def test_two_streams_at_once():
+    """Calls of different sizes on two streams, each with its own workspace, as each alone."""
+    say("two streams")
+    sets = []
+    for t, dd, v in ((1100, 384, 20000), (40, 384, 70000)):
+        h, w, y, g, e = pd.inputs(t, dd, v, BF16, t, 0.2)
+        alone, o, ws = outputs(t, dd, v), outputs(t, dd, v), pd.workspace(t, dd, v, BF16)
+        step(h, w, y, g, e, alone, ws)
+        sets.append((h, w, y, g, e, alone, o, ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for h, w, y, g, e, alone, o, ws, s in sets:
+            with torch.cuda.stream(s):
+                step(h, w, y, g, e, o, ws)
+    torch.cuda.synchronize()
+    for h, w, y, g, e, alone, o, ws, s in sets:
+        for n in o:
+            assert torch.equal(o[n], alone[n]), n
