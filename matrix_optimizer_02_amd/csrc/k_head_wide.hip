@@ -97,6 +97,12 @@ __device__ __forceinline__ uint4 from_piece(const char* piece, int c, int ch) {
     return *reinterpret_cast<const uint4*>(piece + c * 256 + ((ch ^ (c & 15)) << 4));
 }
 
+// ds and dW are written past the L2, which the operands' tiles are read from again: 8192 tokens,
+// hidden 4096, vocabulary 128256, forward and backward 19.68 ms for 19.84.
+__device__ __forceinline__ void store_past(void* p, const uint4& v) {
+    __builtin_nontemporal_store(u32x4_t{v.x, v.y, v.z, v.w}, static_cast<u32x4_t*>(p));
+}
+
 constexpr int kLoads3 = 6, kLoads0 = 6, kLoads1 = 16 - kLoads3 - kLoads0;
 
 template <int MODE>
@@ -463,7 +469,7 @@ __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1)
                     if (row >= dw_rows || col >= dw_ld) continue;
                     uint16_t* const p = dw + row * dw_ld + col;
                     if ((dw_ld & 7) == 0) {
-                        *reinterpret_cast<uint4*>(p) = v;
+                        store_past(p, v);
                     } else {
                         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                         #pragma unroll
@@ -534,7 +540,7 @@ __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1)
                 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     const int c = 4 * u + lane / 16, ch = lane % 16;
-                    *reinterpret_cast<uint4*>(g_out + 2 * ((32 * j + c) * g_ld + ch * 8)) = from_piece(piece, c, ch);
+                    store_past(g_out + 2 * ((32 * j + c) * g_ld + ch * 8), from_piece(piece, c, ch));
                 }
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             });
