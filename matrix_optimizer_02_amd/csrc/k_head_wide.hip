@@ -7,10 +7,11 @@
 // accumulation registers, which leaves the compiler none to move them about with: they
 // are named here, and the compiler does not know of them.  One wave a SIMD has nobody to
 // cover for it, so everything is issued between its products: a slab's 32 fragments one k-step
-// ahead, its 16 loads spread over three k-steps (all in one they take 10% longer: they
-// fill LDS against the fragments' reads), and its one barrier with a k-step's products on
-// their way and fragments of the next slab behind it.  The sequence of slabs runs on over the
-// tiles' ends, so the next tile's first two slabs load behind the epilogue.
+// ahead, its 16 loads spread over three k-steps (they fill LDS against the fragments' reads: all in
+// one they take 10% longer, 4 + 6 + 6 of them 4% than 8 + 6 + 2, which suits the gradients by 0.5%
+// and the cross entropy's statistics, with 6 + 6 + 4, not by 2%), and its one barrier with a k-step's
+// products on their way and fragments of the next slab behind it.  The sequence of slabs runs on
+// over the tiles' ends, so the next tile's first two slabs load behind the epilogue.
 //
 // What bounds it: the matrix cores with the loads' way into LDS.  8192 tokens, hidden
 // 4096, vocabulary 128256, statistics of softmax and entropy: 6.29 ms, 1368 TFLOP/s,
@@ -103,12 +104,12 @@ __device__ __forceinline__ void store_past(void* p, const uint4& v) {
     __builtin_nontemporal_store(u32x4_t{v.x, v.y, v.z, v.w}, static_cast<u32x4_t*>(p));
 }
 
-constexpr int kLoads3 = 6, kLoads0 = 6, kLoads1 = 16 - kLoads3 - kLoads0;
-
 template <int MODE>
 __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void head_wide_kernel(HeadGemmArgs args) {
     __shared__ __attribute__((aligned(1024))) char smem[2 * kWStage + (is_grad(MODE) || MODE == kHeadDw ? kWPiece * 4 : 0)];
     asm volatile("" ::: "a0", "a255");
+    // loads of a slab that k-step 3 of the slab before the last one issues, k-step 0, k-step 1
+    constexpr int kLoads3 = is_stats(MODE) ? 6 : 8, kLoads0 = 6, kLoads1 = 16 - kLoads3 - kLoads0;
     constexpr bool PW = MODE == kHeadDh || is_dw(MODE), QW = is_dw(MODE);  // K-major operands
     using WP = Wide<kWT>;
 
