@@ -61,6 +61,48 @@ def exported_symbols(header: str = "dmuon_ns.h"):
     return re.findall(r"^DMUON_API\s+[\w\s\*]*?\b(\w+)\s*\(", text, flags=re.M)
 
 
+# Sources whose accumulators are registers that only their assembly text names.
+ASM_ACCUMULATORS = ["k_head_wide.hip"]
+
+
+def check_accumulators(assembly: str, what: str) -> None:
+    """Refuses device assembly in which anything but the products and the reads of
+    their sums touches an accumulation register: the sums lie there without the
+    compiler's knowledge, and what it kept or moved there itself would be lost, or
+    would overwrite them."""
+    import re
+
+    n = r"(?:0x[0-9a-f]+|\d+)"
+    products, refused = 0, []
+    for line in assembly.splitlines():
+        code = line.split(";")[0].split("//")[0].strip()
+        if code.startswith(".") or not re.search(r"\ba(\d+\b|\[)", code):
+            continue
+        if re.fullmatch(rf"v_mfma_\w+ (a\[{n}:{n}\]), v\[\d+:\d+\], v\[\d+:\d+\], (\1|0)", code):
+            products += 1
+        elif not re.fullmatch(rf"v_accvgpr_read_b32 v\d+, a(\d+|\[{n}\])", code):
+            refused.append(code)
+    if refused:
+        raise RuntimeError(f"{what}: the compiler uses accumulation registers, which hold the kernel's sums: "
+                           + "; ".join(refused[:8]))
+    if products == 0:
+        raise RuntimeError(f"{what}: no product found")
+
+
+def _device_assembly(bdir: str, src: str) -> str:
+    """What -save-temps=obj left of a source's device code."""
+    with open(os.path.join(bdir, f"{os.path.splitext(src)[0]}-hip-amdgcn-amd-amdhsa-{ARCH}.s")) as f:
+        return f.read()
+
+
+def compile_hip(src: str, obj: str, extra_flags=(), verbose: bool = False) -> None:
+    """One HIP source of csrc/ to an object file."""
+    temps = ["-save-temps=obj"] if src in ASM_ACCUMULATORS else []
+    _run([hipcc(), *HIP_FLAGS, *extra_flags, *temps, f"-I{INCLUDE}", "-c", os.path.join(CSRC, src), "-o", obj], verbose)
+    if temps:
+        check_accumulators(_device_assembly(os.path.dirname(obj), src), src)
+
+
 def build(verbose: bool = False, extra_flags=(), out: str = None, build_dir: str = None) -> str:
     """Compile every source and link libdmuon_ns.so; returns the library path.
     ``extra_flags`` (e.g. -D tuning macros) go to every hipcc compile; ``out``
@@ -72,8 +114,7 @@ def build(verbose: bool = False, extra_flags=(), out: str = None, build_dir: str
     cc = hipcc()
     for src in HIP_SOURCES:
         obj = os.path.join(bdir, src + ".o")
-        _run([cc, *HIP_FLAGS, *extra_flags, f"-I{INCLUDE}", "-c", os.path.join(CSRC, src), "-o", obj],
-             verbose)
+        compile_hip(src, obj, extra_flags, verbose)
         objs.append(obj)
     for src in CXX_SOURCES:
         obj = os.path.join(bdir, src + ".o")

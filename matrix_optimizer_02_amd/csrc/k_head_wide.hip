@@ -5,7 +5,7 @@
 // Eight waves of 128 x 64 read 192 KB of fragments from LDS for every 64 KB that a slab
 // brings; four of 128 x 128 read 128 KB.  Their 256 accumulators a lane are all of the
 // accumulation registers, which leaves the compiler none to move them about with: they
-// are named here, and the compiler does not know of them.  One wave a SIMD has nobody to
+// are named here, and it learns only what each product writes (mma).  One wave a SIMD has nobody to
 // cover for it, so everything is issued between its products: a slab's 32 fragments one k-step
 // ahead, its 16 loads spread over three k-steps (they fill LDS against the fragments' reads: all in
 // one they take 10% longer, 4 + 6 + 6 of them 4% than 8 + 6 + 2, which suits the gradients by 0.5%
@@ -55,15 +55,43 @@ __device__ __forceinline__ void each(F&& f) {
 }
 
 // The accumulators are AGPRs that the compiler does not allocate: tuple (i, j) is
-// a[16 (4 i + j)] to the 15 after it.
+// a[16 (4 i + j)] to the 15 after it.  (As operands they cannot be had: given 16 of them
+// the compiler moves them about and keeps up to 160 words of them in memory.)  A product
+// names the tuple that it writes, so that nothing of the compiler's own lives in one across
+// the main loop; that it uses none between the products and acc_at either is checked on
+// every build's assembly (check_accumulators in build.py).
 template <int N>
-__device__ __forceinline__ void mma(const bf16x8& a, const bf16x8& b) {
-    asm volatile("v_mfma_f32_32x32x16_bf16 a[%2:%3], %0, %1, a[%2:%3]" ::"v"(a), "v"(b), "n"(16 * N), "n"(16 * N + 15));
-}
+__device__ __forceinline__ void mma(const bf16x8& a, const bf16x8& b);
 template <int N>
-__device__ __forceinline__ void mma_first(const bf16x8& a, const bf16x8& b) {
-    asm volatile("v_mfma_f32_32x32x16_bf16 a[%2:%3], %0, %1, 0" ::"v"(a), "v"(b), "n"(16 * N), "n"(16 * N + 15));
-}
+__device__ __forceinline__ void mma_first(const bf16x8& a, const bf16x8& b);
+#define HEAD_TUPLE(N, ...)                                                                                            \
+    template <>                                                                                                       \
+    __device__ __forceinline__ void mma<N>(const bf16x8& a, const bf16x8& b) {                                        \
+        asm volatile("v_mfma_f32_32x32x16_bf16 a[%2:%3], %0, %1, a[%2:%3]" ::"v"(a), "v"(b), "n"(16 * N), "n"(16 * N + 15) \
+                     : __VA_ARGS__);                                                                                  \
+    }                                                                                                                 \
+    template <>                                                                                                       \
+    __device__ __forceinline__ void mma_first<N>(const bf16x8& a, const bf16x8& b) {                                  \
+        asm volatile("v_mfma_f32_32x32x16_bf16 a[%2:%3], %0, %1, 0" ::"v"(a), "v"(b), "n"(16 * N), "n"(16 * N + 15)     \
+                     : __VA_ARGS__);                                                                                  \
+    }
+HEAD_TUPLE(0, "a0", "a1", "a2", "a3", "a4", "a5", "a6", "a7", "a8", "a9", "a10", "a11", "a12", "a13", "a14", "a15")
+HEAD_TUPLE(1, "a16", "a17", "a18", "a19", "a20", "a21", "a22", "a23", "a24", "a25", "a26", "a27", "a28", "a29", "a30", "a31")
+HEAD_TUPLE(2, "a32", "a33", "a34", "a35", "a36", "a37", "a38", "a39", "a40", "a41", "a42", "a43", "a44", "a45", "a46", "a47")
+HEAD_TUPLE(3, "a48", "a49", "a50", "a51", "a52", "a53", "a54", "a55", "a56", "a57", "a58", "a59", "a60", "a61", "a62", "a63")
+HEAD_TUPLE(4, "a64", "a65", "a66", "a67", "a68", "a69", "a70", "a71", "a72", "a73", "a74", "a75", "a76", "a77", "a78", "a79")
+HEAD_TUPLE(5, "a80", "a81", "a82", "a83", "a84", "a85", "a86", "a87", "a88", "a89", "a90", "a91", "a92", "a93", "a94", "a95")
+HEAD_TUPLE(6, "a96", "a97", "a98", "a99", "a100", "a101", "a102", "a103", "a104", "a105", "a106", "a107", "a108", "a109", "a110", "a111")
+HEAD_TUPLE(7, "a112", "a113", "a114", "a115", "a116", "a117", "a118", "a119", "a120", "a121", "a122", "a123", "a124", "a125", "a126", "a127")
+HEAD_TUPLE(8, "a128", "a129", "a130", "a131", "a132", "a133", "a134", "a135", "a136", "a137", "a138", "a139", "a140", "a141", "a142", "a143")
+HEAD_TUPLE(9, "a144", "a145", "a146", "a147", "a148", "a149", "a150", "a151", "a152", "a153", "a154", "a155", "a156", "a157", "a158", "a159")
+HEAD_TUPLE(10, "a160", "a161", "a162", "a163", "a164", "a165", "a166", "a167", "a168", "a169", "a170", "a171", "a172", "a173", "a174", "a175")
+HEAD_TUPLE(11, "a176", "a177", "a178", "a179", "a180", "a181", "a182", "a183", "a184", "a185", "a186", "a187", "a188", "a189", "a190", "a191")
+HEAD_TUPLE(12, "a192", "a193", "a194", "a195", "a196", "a197", "a198", "a199", "a200", "a201", "a202", "a203", "a204", "a205", "a206", "a207")
+HEAD_TUPLE(13, "a208", "a209", "a210", "a211", "a212", "a213", "a214", "a215", "a216", "a217", "a218", "a219", "a220", "a221", "a222", "a223")
+HEAD_TUPLE(14, "a224", "a225", "a226", "a227", "a228", "a229", "a230", "a231", "a232", "a233", "a234", "a235", "a236", "a237", "a238", "a239")
+HEAD_TUPLE(15, "a240", "a241", "a242", "a243", "a244", "a245", "a246", "a247", "a248", "a249", "a250", "a251", "a252", "a253", "a254", "a255")
+#undef HEAD_TUPLE
 template <int N>
 __device__ __forceinline__ float acc_at() {
     float x;
@@ -107,7 +135,6 @@ __device__ __forceinline__ void store_past(void* p, const uint4& v) {
 template <int MODE>
 __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void head_wide_kernel(HeadGemmArgs args) {
     __shared__ __attribute__((aligned(1024))) char smem[2 * kWStage + (is_grad(MODE) || MODE == kHeadDw ? kWPiece * 4 : 0)];
-    asm volatile("" ::: "a0", "a255");
     // loads of a slab that k-step 3 of the slab before the last one issues, k-step 0, k-step 1
     constexpr int kLoads3 = is_stats(MODE) ? 6 : 8, kLoads0 = 6, kLoads1 = 16 - kLoads3 - kLoads0;
     constexpr bool PW = MODE == kHeadDh || is_dw(MODE), QW = is_dw(MODE);  // K-major operands
