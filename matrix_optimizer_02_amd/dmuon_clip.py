@@ -4,8 +4,8 @@
     grad_norm_batched(grads, norm, workspace=norm_workspace_for(grads))
     grad_clip_batched(grads, norm, 1.0)                  # in place; then the optimizer's step
 
-or, for gradients that stay where they are from step to step (their addresses are
-gathered once):
+or, for gradients that stay where they are from step to step (zeroed in place: their
+sizes, types and addresses are gathered once):
 
     batch = GradBatch(grads)
     batch.norm(norm)
@@ -44,6 +44,9 @@ def _declare():
 _declare()
 
 
+_address = torch.Tensor.data_ptr
+
+
 class _Table:
     """The host arrays of a list of tensors: sizes, types and addresses."""
 
@@ -58,7 +61,16 @@ class _Table:
         self.device = tensors[0].device if n else None
         self.numels = (ctypes.c_int64 * max(1, n))(*[t.numel() for t in tensors])
         self.dtypes = (ctypes.c_int32 * max(1, n))(*[_DTYPE_CODE[t.dtype] for t in tensors])
-        self.pointers = (ctypes.c_void_p * max(1, n))(*[t.data_ptr() for t in tensors])
+        self.addresses = list(map(_address, tensors))
+        self.pointers = (ctypes.c_void_p * max(1, n))(*self.addresses)
+
+    def check(self, tensors: Sequence[torch.Tensor], what: str) -> None:
+        """The tensors still lie where they were, on the device that is current."""
+        if self.device is not None and self.device.index != torch.cuda.current_device():
+            raise ValueError(f"{what} are on {self.device}; the current device is cuda:{torch.cuda.current_device()}")
+        if list(map(_address, tensors)) != self.addresses:
+            i = next(i for i, (t, a) in enumerate(zip(tensors, self.addresses)) if t.data_ptr() != a)
+            raise ValueError(f"{what}[{i}] does not lie where it was when the batch was built; build another one")
 
 
 def _outputs(grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]], table: _Table) -> _Table:
@@ -133,20 +145,29 @@ def grad_clip_batched(grads: Sequence[torch.Tensor], norm: torch.Tensor, max_nor
 class GradBatch:
     """A list of gradients that stay where they are (and, to clip into other buffers,
     their outputs), with the norm's workspace.  The batch keeps the tensors alive;
-    its calls on different streams must not overlap in time."""
+    its calls on different streams must not overlap in time.
+
+    Every call is refused where a tensor's memory was replaced since (``.data``,
+    ``set_``, a resized storage) or another device is current.  A parameter that was
+    given a new ``.grad`` tensor is not seen: zero gradients in place
+    (``zero_grad(set_to_none=False)``), or take the list calls."""
 
     def __init__(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None):
-        self._kept = list(grads), None if outs is None else list(outs)
-        self._table = _Table(self._kept[0], "grads")
-        self._outs = _outputs(self._kept[0], self._kept[1], self._table)
+        self._grads, self._outs = list(grads), None if outs is None else list(outs)
+        self._table = _Table(self._grads, "grads")
+        self._to = _outputs(self._grads, self._outs, self._table)
         self.workspace = torch.empty(max(1, _workspace_bytes(self._table)), dtype=torch.uint8,
                                      device=self._table.device or "cuda")
 
     def norm(self, norm: torch.Tensor, *, stream=None) -> None:
+        self._table.check(self._grads, "grads")
         _norm(self._table, norm, self.workspace, stream)
 
     def clip(self, norm: torch.Tensor, max_norm: float, *, eps: float = 1e-6, stream=None) -> None:
-        _clip(self._table, self._outs, norm, max_norm, eps, stream)
+        self._table.check(self._grads, "grads")
+        if self._outs is not None:
+            self._to.check(self._outs, "outs")
+        _clip(self._table, self._to, norm, max_norm, eps, stream)
 
 
 __all__ = ["norm_workspace_for", "grad_norm_batched", "grad_clip_batched", "GradBatch"]
