@@ -45,7 +45,9 @@
  * parts.  An alternative is found by the logit that its product formed; where several of
  * a row's alternatives lie in one group of 16 words, all but the first of them are by
  * logits formed again in another order of summation, which may differ in the last bits
- * and so order what those bits decide otherwise.
+ * and so order what those bits decide otherwise.  How sums are cut follows from the
+ * call's sizes, so a row's last bits may differ between calls of other sizes; a call with
+ * alternatives takes as many tokens at a time as 1 GiB holds what it keeps of them.
  *
  * Conventions are those of dmuon_head.h: status codes, dense row-major arrays,
  * 16-byte aligned device pointers of the current device, a 256-byte aligned
