@@ -502,6 +502,7 @@ dmuon_status backward(const Call& c, const Upstream& u, void* grad_hidden, void*
         a.g = v.ws + L.off_g;
         a.g_plane = 2 * L.t_pad * L.piece;
         a.g_ld = (int32_t)L.piece;
+        a.g_cached = L.g_cached && grad_hidden != nullptr;
         HEAD_TRY(launch_logits(entropy ? kHeadGradEntropy : kHeadGrad, c, v, v0, L.piece, a, round_up(L.tokens, kHeadSlab)));
         if (distill) {
             HeadFixArgs f{};

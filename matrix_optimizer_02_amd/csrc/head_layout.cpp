@@ -13,6 +13,7 @@ namespace {
 // once and read by two products, so it should stay in the 256 MB last-level
 // cache next to what those stream.
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
+constexpr int64_t kCachedBytes = int64_t(240) << 20;  // ... and does, with those streams' share left
 constexpr int64_t kLowTokens = 128;
 // Bytes that a forward call of the log probabilities holds for its alternatives.
 constexpr int64_t kProbsBytes = int64_t(1) << 30;
@@ -145,6 +146,14 @@ HeadLayout head_layout_of(dmuon_head_desc d, bool backward, bool split_live) {
     L.dh_tile = pick_split_tile(d.hidden, ds_rows, (double)(k / kHeadSlab) * parts, max_tq, true, &splits);
     L.split_k = round_up(ceil_div(k, std::min(splits, k / kHeadSlab)), kHeadSlab);
     L.splits = (int32_t)ceil_div(k, L.split_k);
+
+    // ds is written past the caches, which the tiles of its operands are read from again.  Not
+    // where dH, in 64 x 64 tiles for want of columns, is bound by reading ds, and ds stays in the
+    // last-level cache.  Backward, us, written through the caches against past them: 2048 x 128 x
+    // 50257 197 / 223, 1024 x 320 x 50257 201 / 224, 4096 x 64 x 30000 (236 MB of ds) 196 / 206; 4096 x
+    // 64 x 32700 (256 MB) 229 / 221; with larger tiles 1024 x 320 x 120000 427 / 410, 8192 x 256 x
+    // 128256 2482 / 2381.
+    L.g_cached = backward && !f32 && L.dh_tile.tp == 64 && 2 * L.t_pad * L.piece <= kCachedBytes;
 
     size_t at = 0;
     auto take = [&](int64_t bytes) {

@@ -126,13 +126,15 @@ __device__ __forceinline__ uint4 from_piece(const char* piece, int c, int ch) {
     return *reinterpret_cast<const uint4*>(piece + c * 256 + ((ch ^ (c & 15)) << 4));
 }
 
-// ds and dW are written past the L2, which the operands' tiles are read from again: 8192 tokens,
-// hidden 4096, vocabulary 128256, forward and backward 19.68 ms for 19.84.
+// ds (but for g_cached: head_layout.cpp) and dW are written past the caches, which the operands'
+// tiles are read from again: 8192 tokens, hidden 4096, vocabulary 128256, forward and backward 19.68
+// ms for 19.84.
 __device__ __forceinline__ void store_past(void* p, const uint4& v) {
     __builtin_nontemporal_store(u32x4_t{v.x, v.y, v.z, v.w}, static_cast<u32x4_t*>(p));
 }
 
-template <int MODE>
+// CACHED: ds is written through the caches (args.g_cached).
+template <int MODE, bool CACHED = false>
 __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void head_wide_kernel(HeadGemmArgs args) {
     __shared__ __attribute__((aligned(1024))) char smem[2 * kWStage + (is_grad(MODE) || MODE == kHeadDw ? kWPiece * 4 : 0)];
     // loads of a slab that k-step 3 of the slab before the last one issues, k-step 0, k-step 1
@@ -568,7 +570,9 @@ __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1)
                 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     const int c = 4 * u + lane / 16, ch = lane % 16;
-                    store_past(g_out + 2 * ((32 * j + c) * g_ld + ch * 8), from_piece(piece, c, ch));
+                    char* const to = g_out + 2 * ((32 * j + c) * g_ld + ch * 8);
+                    if constexpr (CACHED) *reinterpret_cast<uint4*>(to) = from_piece(piece, c, ch);
+                    else store_past(to, from_piece(piece, c, ch));
                 }
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             });
@@ -582,15 +586,22 @@ __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1)
 hipError_t launch_head_wide(int mode, const HeadGemmArgs& a, int64_t max_tiles, hipStream_t stream) {
     const int64_t per_xcd = (max_tiles + kXcds - 1) / kXcds, most = head_slots(kWT) / kXcds;
     const dim3 grid(kXcds * (int)(per_xcd < most ? per_xcd : most)), block(kWThreads);
+    auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
     switch (mode) {
-        case kHeadLse: hipLaunchKernelGGL((head_wide_kernel<kHeadLse>), grid, block, 0, stream, a); break;
-        case kHeadProbs: hipLaunchKernelGGL((head_wide_kernel<kHeadProbs>), grid, block, 0, stream, a); break;
-        case kHeadTop: hipLaunchKernelGGL((head_wide_kernel<kHeadTop>), grid, block, 0, stream, a); break;
-        case kHeadGrad: hipLaunchKernelGGL((head_wide_kernel<kHeadGrad>), grid, block, 0, stream, a); break;
-        case kHeadGradEntropy: hipLaunchKernelGGL((head_wide_kernel<kHeadGradEntropy>), grid, block, 0, stream, a); break;
-        case kHeadDh: hipLaunchKernelGGL((head_wide_kernel<kHeadDh>), grid, block, 0, stream, a); break;
-        case kHeadDw: hipLaunchKernelGGL((head_wide_kernel<kHeadDw>), grid, block, 0, stream, a); break;
-        case kHeadDwSum: hipLaunchKernelGGL((head_wide_kernel<kHeadDwSum>), grid, block, 0, stream, a); break;
+        case kHeadLse: launch(head_wide_kernel<kHeadLse>); break;
+        case kHeadProbs: launch(head_wide_kernel<kHeadProbs>); break;
+        case kHeadTop: launch(head_wide_kernel<kHeadTop>); break;
+        case kHeadGrad:
+            if (a.g_cached) launch(head_wide_kernel<kHeadGrad, true>);
+            else launch(head_wide_kernel<kHeadGrad>);
+            break;
+        case kHeadGradEntropy:
+            if (a.g_cached) launch(head_wide_kernel<kHeadGradEntropy, true>);
+            else launch(head_wide_kernel<kHeadGradEntropy>);
+            break;
+        case kHeadDh: launch(head_wide_kernel<kHeadDh>); break;
+        case kHeadDw: launch(head_wide_kernel<kHeadDw>); break;
+        case kHeadDwSum: launch(head_wide_kernel<kHeadDwSum>); break;
         default: return hipErrorInvalidValue;
     }
     return hipGetLastError();

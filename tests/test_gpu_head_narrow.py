@@ -1,0 +1,49 @@
+"""Narrow heads: the gradient of the hidden states in 64 x 64 tiles beside 256 x 256 tiles of
+ds, which is then written through the caches; and sizes next to them where it is not."""
+
+import sys
+
+import pytest
+import torch
+
+import head_device as dev
+import probs_device as pd
+from matrix_optimizer_02_amd import dmuon_head as hd
+from head_device import BF16, IGN
+
+pytestmark = pytest.mark.gpu
+
+CACHED = [(600, 256, 16000), (1024, 100, 16000), (1536, 384, 8000), (4096, 64, 8000)]
+PAST = [(1024, 512, 16000), (2048, 256, 32000)]
+
+
+def say(*a):
+    print(*a, flush=True)
+    sys.stdout.flush()
+
+
+@pytest.mark.parametrize("t,d,v", CACHED + PAST)
+def test_losses(t, d, v):
+    say("losses", t, d, v)
+    h, w, y, up = dev.inputs(t, d, v, BF16, t + d, edges=(0, v - 1), dead=0.2)
+    got = dev.run(h, w, up, y=y)
+    dev.check(f"{t}x{d}x{v}", got, h, w, up, y=y)
+    # one gradient alone: the same bits
+    ws = dev.workspace(t, d, v, BF16)
+    for name in ("dh", "dw"):
+        out = torch.full_like(got[name], float("nan"))
+        hd.head_cross_entropy_backward(h, w, y, got["lse"], up, out if name == "dh" else None,
+                                       out if name == "dw" else None, ignore_index=IGN, workspace=ws)
+        assert torch.equal(out, got[name]), name
+    ids, z = dev.teacher(t, 6, v, t, edges=(0, v - 1))
+    h, w, _, up = dev.inputs(t, d, v, BF16, t + d + 1)
+    got = dev.run(h, w, up, ids=ids, z=z, tau=2.0)
+    dev.check(f"{t}x{d}x{v} distilled", got, h, w, up, ids=ids, z=z, tau=2.0)
+
+
+@pytest.mark.parametrize("t,d,v", CACHED + PAST)
+def test_log_probabilities(t, d, v):
+    say("log probabilities", t, d, v)
+    h, w, y, g, e = pd.inputs(t, d, v, BF16, t + d, 0.2)
+    got = pd.run(h, w, y, 0, 0.9, g, e)
+    pd.check(f"{t}x{d}x{v}", got, h, w, y, 0, 0.9, g, e, block=256)

@@ -7,6 +7,7 @@ import subprocess
 
 import pytest
 
+import test_gpu_head_narrow as narrow
 import test_gpu_logprobs_reach as reach
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -91,3 +92,16 @@ def test_splits_fit_their_room(layouts):
         cost = lambda n: up(n * tiles, 256) * (up(slabs, n) + SUM_SLABS)
         assert cost(s) == min(cost(n) for n in range(1, MOST_SPLITS + 1) if n <= slabs and n * tiles <= L["room"])
     assert seen > 100
+
+
+def test_where_ds_stays_in_the_caches(layouts):
+    """dH in 64 x 64 tiles reads ds at the memory's rate: there ds is written through the last-level cache, as
+    long as it stays in it."""
+    sizes = [(*c, True) for c in narrow.CACHED] + [(*c, False) for c in narrow.PAST]
+    sizes += [(2048, 128, 50257, True), (4096, 128, 50257, True), (4096, 64, 30000, True), (4096, 64, 32700, False),
+              (8192, 4096, 128256, False), (8192, 128, 128256, False)]
+    for (t, d, v, cached), L in zip(sizes, layouts([backward(t, d, v, t) for t, d, v, _ in sizes])):
+        assert (L["s_tp"], L["s_tq"]) == (256, 256), (t, d, v)  # (whose kernel it is for)
+        assert L["cached"] == cached == (L["dh_tp"] == 64 and 2 * L["t_pad"] * L["piece"] <= 240 << 20), (t, d, v)
+    L, = layouts([backward(2048, 128, 50257, 2048, F32)])
+    assert not L["cached"]
