@@ -502,7 +502,7 @@ dmuon_status backward(const Call& c, const Upstream& u, void* grad_hidden, void*
         a.g = v.ws + L.off_g;
         a.g_plane = 2 * L.t_pad * L.piece;
         a.g_ld = (int32_t)L.piece;
-        a.g_cached = L.g_cached && grad_hidden != nullptr;
+        a.cached = L.g_cached && grad_hidden != nullptr;
         HEAD_TRY(launch_logits(entropy ? kHeadGradEntropy : kHeadGrad, c, v, v0, L.piece, a, round_up(L.tokens, kHeadSlab)));
         if (distill) {
             HeadFixArgs f{};
@@ -559,6 +559,7 @@ dmuon_status backward(const Call& c, const Upstream& u, void* grad_hidden, void*
             g.dw = static_cast<char*>(grad_weight) + v0 * L.hidden * L.esize;
             g.dw_rows = left;
             g.dw_ld = (int32_t)L.hidden;
+            g.cached = L.dw_cached;
             g.splits = L.dw_splits;
             g.sums = v.at<float>(L.off_dw);
             HEAD_TRY(launch_head_gemm(g.splits > 1 ? kHeadDwSum : kHeadDw, L.dw_tile, g, (int64_t)g.tiles_i * g.tiles_j * g.splits, c.stream));

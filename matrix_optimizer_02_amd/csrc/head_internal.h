@@ -72,7 +72,7 @@ struct HeadGemmArgs {
     char* g;                     // ds out
     int64_t g_plane;             // bytes
     int32_t g_ld;
-    int32_t g_cached;            // Grad in 256 x 256 tiles: ds is written through the caches
+    int32_t cached;              // Grad, dW in 256 x 256 tiles: written through the caches
     float* sums;                 // fp32 sums (dH; dW in splits), tile by tile in the accumulators' own order
     int32_t accumulate;          // dH: add to what earlier pieces left
     void* dw;                    // dW out (row v0 of it is at dw)

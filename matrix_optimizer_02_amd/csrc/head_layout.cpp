@@ -14,6 +14,7 @@ namespace {
 // cache next to what those stream.
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
 constexpr int64_t kCachedBytes = int64_t(240) << 20;  // ... and does, with those streams' share left
+constexpr int64_t kCachedDwBytes = int64_t(112) << 20;
 constexpr int64_t kLowTokens = 128;
 // Bytes that a forward call of the log probabilities holds for its alternatives.
 constexpr int64_t kProbsBytes = int64_t(1) << 30;
@@ -154,6 +155,12 @@ HeadLayout head_layout_of(dmuon_head_desc d, bool backward, bool split_live) {
     // 64 x 32700 (256 MB) 229 / 221; with larger tiles 1024 x 320 x 120000 427 / 410, 8192 x 256 x
     // 128256 2482 / 2381.
     L.g_cached = backward && !f32 && L.dh_tile.tp == 64 && 2 * L.t_pad * L.piece <= kCachedBytes;
+    // So is dW, but for rows that are not whole 128-byte lines: past the caches their ends are
+    // written in parts.  What that takes shows where few tokens leave dW bound by its writes, and
+    // the caches hold it.  Backward, us, through against past them: 16 x 1000 x 32000 69 / 75, 96 x 712 x
+    // 50257 116 / 123, 48 x 1672 x 32000 118 / 126; 48 x 1416 x 50257 (142 MB) 147 / 145, 96 x 2760 x 32000
+    // (177 MB) 248 / 227; 200 x 1112 x 50257 182 / 180; whole lines 100 x 1024 x 32000 87 / 85.
+    L.dw_cached = backward && !f32 && d.tokens <= kLowTokens && d.hidden % 64 != 0 && 2 * d.hidden * d.vocab <= kCachedDwBytes;
 
     size_t at = 0;
     auto take = [&](int64_t bytes) {

@@ -64,7 +64,7 @@ struct HeadLayout {
     int64_t split_k;        // dH: vocab rows of a split (multiple of 64)
     int32_t splits;         // ... splits of a full piece
     int32_t dh_room;        // tiles that the sums of dH hold, where the device chooses the splits (else 0)
-    int32_t g_cached;       // 256 x 256 tiles of bf16 ds are written through the caches
+    int32_t g_cached, dw_cached;  // 256 x 256 tiles of bf16 ds, of dW, are written through the caches
     int32_t dw_splits;      // dW: splits of the tokens
     int32_t keep_logits;    // distillation, small vocabularies: see head_layout.cpp
     // byte offsets

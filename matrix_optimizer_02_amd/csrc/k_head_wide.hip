@@ -126,14 +126,15 @@ __device__ __forceinline__ uint4 from_piece(const char* piece, int c, int ch) {
     return *reinterpret_cast<const uint4*>(piece + c * 256 + ((ch ^ (c & 15)) << 4));
 }
 
-// ds (but for g_cached: head_layout.cpp) and dW are written past the caches, which the operands'
-// tiles are read from again: 8192 tokens, hidden 4096, vocabulary 128256, forward and backward 19.68
-// ms for 19.84.
-__device__ __forceinline__ void store_past(void* p, const uint4& v) {
-    __builtin_nontemporal_store(u32x4_t{v.x, v.y, v.z, v.w}, static_cast<u32x4_t*>(p));
+// ds and dW are written past the caches, which the operands' tiles are read from again (8192
+// tokens, hidden 4096, vocabulary 128256, forward and backward 19.68 ms for 19.84), or, where the
+// layout says so, through them (head_layout.cpp).
+template <bool CACHED>
+__device__ __forceinline__ void store(void* p, const uint4& v) {
+    if (CACHED) *static_cast<uint4*>(p) = v;
+    else __builtin_nontemporal_store(u32x4_t{v.x, v.y, v.z, v.w}, static_cast<u32x4_t*>(p));
 }
 
-// CACHED: ds is written through the caches (args.g_cached).
 template <int MODE, bool CACHED = false>
 __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void head_wide_kernel(HeadGemmArgs args) {
     __shared__ __attribute__((aligned(1024))) char smem[2 * kWStage + (is_grad(MODE) || MODE == kHeadDw ? kWPiece * 4 : 0)];
@@ -499,7 +500,7 @@ __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1)
                     if (row >= dw_rows || col >= dw_ld) continue;
                     uint16_t* const p = dw + row * dw_ld + col;
                     if ((dw_ld & 7) == 0) {
-                        store_past(p, v);
+                        store<CACHED>(p, v);
                     } else {
                         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                         #pragma unroll
@@ -570,9 +571,7 @@ __global__ __launch_bounds__(kWThreads) __attribute__((amdgpu_waves_per_eu(1, 1)
                 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     const int c = 4 * u + lane / 16, ch = lane % 16;
-                    char* const to = g_out + 2 * ((32 * j + c) * g_ld + ch * 8);
-                    if constexpr (CACHED) *reinterpret_cast<uint4*>(to) = from_piece(piece, c, ch);
-                    else store_past(to, from_piece(piece, c, ch));
+                    store<CACHED>(g_out + 2 * ((32 * j + c) * g_ld + ch * 8), from_piece(piece, c, ch));
                 }
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             });
@@ -592,15 +591,18 @@ hipError_t launch_head_wide(int mode, const HeadGemmArgs& a, int64_t max_tiles, 
         case kHeadProbs: launch(head_wide_kernel<kHeadProbs>); break;
         case kHeadTop: launch(head_wide_kernel<kHeadTop>); break;
         case kHeadGrad:
-            if (a.g_cached) launch(head_wide_kernel<kHeadGrad, true>);
+            if (a.cached) launch(head_wide_kernel<kHeadGrad, true>);
             else launch(head_wide_kernel<kHeadGrad>);
             break;
         case kHeadGradEntropy:
-            if (a.g_cached) launch(head_wide_kernel<kHeadGradEntropy, true>);
+            if (a.cached) launch(head_wide_kernel<kHeadGradEntropy, true>);
             else launch(head_wide_kernel<kHeadGradEntropy>);
             break;
         case kHeadDh: launch(head_wide_kernel<kHeadDh>); break;
-        case kHeadDw: launch(head_wide_kernel<kHeadDw>); break;
+        case kHeadDw:
+            if (a.cached) launch(head_wide_kernel<kHeadDw, true>);
+            else launch(head_wide_kernel<kHeadDw>);
+            break;
         case kHeadDwSum: launch(head_wide_kernel<kHeadDwSum>); break;
         default: return hipErrorInvalidValue;
     }

@@ -28,10 +28,11 @@ int main() {
         const int tiles = (int)(ceil_div(L.hidden, kHeadTile) * ceil_div(live, kHeadTile));
         const int slabs = (int)(round_up(std::min(L.piece, L.vocab), kHeadSlab) / kHeadSlab);
         std::printf("refused=0 chunk=%lld last=%lld keep=%d s_tp=%d s_tq=%d last_s_tp=%d last_s_tq=%d stream=%d last_stream=%d "
-                    "pieces=%d piece=%lld low=%d dh_tq=%d splits=%d room=%d live_splits=%d cached=%d dh_tp=%d t_pad=%lld\n",
+                    "pieces=%d piece=%lld low=%d dh_tq=%d splits=%d room=%d live_splits=%d cached=%d dw_cached=%d dw_tp=%d dw_tq=%d dw_splits=%d dh_tp=%d t_pad=%lld\n",
                     (long long)chunk, (long long)last, P.keep_logits, L.s_tile.tp, L.s_tile.tq, E.s_tile.tp, E.s_tile.tq,
                     L.stream_weight, E.stream_weight, L.pieces, (long long)L.piece, L.low, L.dh_tile.tq, L.splits, L.dh_room,
-                    L.dh_room == 0 ? 0 : head_dh_splits(tiles, slabs, L.dh_room), L.g_cached, L.dh_tile.tp,
+                    L.dh_room == 0 ? 0 : head_dh_splits(tiles, slabs, L.dh_room), L.g_cached, L.dw_cached,
+                    L.dw_tile.tp, L.dw_tile.tq, L.dw_splits, L.dh_tile.tp,
                     (long long)L.t_pad);
     }
     return 0;

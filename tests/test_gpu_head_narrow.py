@@ -1,5 +1,6 @@
 """Narrow heads: the gradient of the hidden states in 64 x 64 tiles beside 256 x 256 tiles of
-ds, which is then written through the caches; and sizes next to them where it is not."""
+ds, which is then written through the caches, and sizes next to them where it is not; few
+tokens with rows of the weight's gradient that are not whole cache lines."""
 
 import sys
 
@@ -15,6 +16,7 @@ pytestmark = pytest.mark.gpu
 
 CACHED = [(600, 256, 16000), (1024, 100, 16000), (1536, 384, 8000), (4096, 64, 8000)]
 PAST = [(1024, 512, 16000), (2048, 256, 32000)]
+SPLIT_LINES = [(1, 1000, 32000), (16, 1000, 32001), (100, 1672, 32000), (128, 328, 50257)]
 
 
 def say(*a):
@@ -22,7 +24,7 @@ def say(*a):
     sys.stdout.flush()
 
 
-@pytest.mark.parametrize("t,d,v", CACHED + PAST)
+@pytest.mark.parametrize("t,d,v", CACHED + PAST + SPLIT_LINES)
 def test_losses(t, d, v):
     say("losses", t, d, v)
     h, w, y, up = dev.inputs(t, d, v, BF16, t + d, edges=(0, v - 1), dead=0.2)
@@ -41,7 +43,7 @@ def test_losses(t, d, v):
     dev.check(f"{t}x{d}x{v} distilled", got, h, w, up, ids=ids, z=z, tau=2.0)
 
 
-@pytest.mark.parametrize("t,d,v", CACHED + PAST)
+@pytest.mark.parametrize("t,d,v", CACHED + PAST + SPLIT_LINES)
 def test_log_probabilities(t, d, v):
     say("log probabilities", t, d, v)
     h, w, y, g, e = pd.inputs(t, d, v, BF16, t + d, 0.2)
