@@ -22,9 +22,13 @@ constexpr int64_t kPieceMin = 8192;  // vocab rows: fewer would leave dW's launc
 
 // Tiles with the time a workgroup takes for 64 of K, in microseconds, when it has
 // the chip to itself (loads' latency) and when every slot is taken, and per tile.
-// Taken with loops that read, wait and multiply; the loops pipelined in registers
-// since are 1 to 10% faster in every shape, and a three-part fp32 slab is counted as
-// six bf16 ones, which it beats by some 20%.  Only the order of the shapes is used.
+// Taken with loops that read, wait and multiply.  The loops pipelined in registers
+// since are 1 to 10% faster, that of 256 x 256 bf16 tiles, by four waves, 17% (1.57 for
+// 1.9); a three-part fp32 slab is counted as six bf16 ones, which it beats by some
+// 20%.  Only the order of the shapes is used, and the first is put too low in it where it
+// and the second lie close: with 1.57, forward and backward, 640 x 4096 x 128256 would take
+// 2.55 ms for 2.77, 777 x 1536 x 50257 587 us for 600, 1100 x 1024 x 32000 348 for 367, and
+// nothing measured longer.  (Another tile changes a call's last bits.)
 struct TileCost {
     HeadTile tile;
     double alone, full, fixed;
