@@ -31,11 +31,12 @@
  * A row with a logit that is NaN or +inf, or with none above -inf, has NaN
  * outputs and -1 as its alternatives' ids.  Where fewer than K logits are above
  * -inf the further alternatives have id -1 and value -inf.  Terms of the entropy
- * with p = 0 are 0.  Words are masked by weights that make their logits low: in bf16
- * by -inf or the type's lowest value, in fp32 by finite ones of magnitude up to 3e38,
- * whose logits may overflow to -inf.  fp32 inputs are multiplied in parts, which
- * neither an infinity nor fp32's lowest value has: one in H or W makes the rows that it
- * meets NaN.
+ * with p = 0 are 0.  Words are masked by weights that make their logits low: finite
+ * ones, of the type's lowest value in bf16 and of magnitude up to 3e38 in fp32, whose
+ * logits may overflow to -inf; in bf16's forward calls also -inf.  (dH is dx W: an
+ * infinite weight makes it NaN where dx is 0.  fp32 inputs are multiplied in parts, which
+ * neither an infinity nor fp32's lowest value has: one in H or W makes the rows that
+ * it meets NaN.)
  *
  * Arithmetic as in dmuon_head.h: sums and softmax statistics are fp32; log
  * probabilities and entropies are formed from the distances of logits from the

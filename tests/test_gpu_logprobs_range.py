@@ -1,5 +1,5 @@
-"""Words that a mask pushes to the end of the range, in fp32: inputs are finite there, of
-magnitude up to 3e38, and logits may still be -inf."""
+"""Words that a mask pushes to the end of the range by finite weights (fp32: of magnitude up
+to 3e38): logits may still be -inf, and gradients are those of the words left."""
 
 import math
 import sys
@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import probs_device as pd
-from probs_device import F32
+from probs_device import BF16, F32
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +62,31 @@ def test_masked_words_fp32(t, first):
     want[0] += 1.0
     assert bool((got["dw"][4:] == 0).all())
     assert torch.allclose(got["dw"][:, 0].double(), want * float(g.double().sum()) * first, rtol=1e-5, atol=1e-9)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("t", [1, 70, 300, 1100])
+@pytest.mark.parametrize("first", [1.0, 2.0])
+def test_gradients_of_masked_words(t, first, dtype):
+    """dH and dW with and without entropy's gradient, against a head of the open words alone."""
+    print("masked gradients", t, first, dtype, flush=True)
+    v, dd = 700, 64
+    gen = torch.Generator("cuda").manual_seed(t)
+    low = torch.finfo(BF16).min if dtype == BF16 else -3e38
+    w = torch.randn(v, dd, device="cuda", generator=gen).mul_(0.2).to(dtype)
+    h = torch.randn(t, dd, device="cuda", generator=gen).to(dtype)
+    h[:, 0] = first
+    mask = torch.rand(v, device="cuda", generator=gen) < 0.3
+    mask[:300] = False
+    w[mask] = 0
+    w[mask, 0] = low
+    y = torch.randint(0, 300, (t,), device="cuda", generator=gen)
+    g = torch.randn(t, device="cuda", generator=gen) / t
+    e = torch.randn(t, device="cuda", generator=gen) * 0.1 / t
+    left = w[~mask].contiguous()
+    new = torch.cumsum(~mask, 0) - 1
+    for up in ((g, None), (None, e), (g, e)):
+        got = pd.run(h, w, y, 0, 1.0, *up)
+        of_left = {n: x if n != "dw" else x[~mask] for n, x in got.items()}
+        pd.check(f"{t} masked", of_left, h, left, new[y], 0, 1.0, *up)
+        assert bool((got["dw"][mask] == 0).all())
