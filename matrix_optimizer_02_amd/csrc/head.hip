@@ -18,15 +18,11 @@
 
 #include "../../include/dmuon_logprobs.h"
 #include "head_internal.h"
+#include "spans.h"
 
 using namespace dmuon;
 
 namespace {
-
-struct Span {
-    uintptr_t lo, hi;
-    bool written;
-};
 
 // Non-null, aligned, and no written buffer overlapping another one.
 struct Buffers {
@@ -38,14 +34,7 @@ struct Buffers {
         if (p == nullptr || (a & 15u) != 0) ok = false;
         spans.push_back({a, a + (uintptr_t)bytes, written});
     }
-    bool good() const {
-        if (!ok) return false;
-        for (size_t i = 0; i < spans.size(); ++i)
-            for (size_t j = 0; j < i; ++j)
-                if ((spans[i].written || spans[j].written) && spans[i].lo < spans[j].hi && spans[j].lo < spans[i].hi)
-                    return false;
-        return true;
-    }
+    bool good() { return ok && disjoint_where_written(spans); }
 };
 
 enum Kind { kCrossEntropy, kDistill, kLogProbs };
