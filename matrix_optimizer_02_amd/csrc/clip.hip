@@ -10,6 +10,10 @@
 // thread has all its loads of a piece in flight; the groups that its ends cut are read
 // an element a thread.  Workgroup b takes
 // pieces b, b + grid, ...: the launch sweeps over the tensors.
+//
+// What bounds it: memory.  28 bf16 tensors of 1.75 GB: squares 280 us, 6.2 TB/s; clipping 641
+// us, 5.5 TB/s, by reads and writes.  Of small tensors the launches, 4 and 2 us for 96 of 98 KB, and
+// the host's time for them.
 #include <hip/hip_runtime.h>
 
 #include <cmath>

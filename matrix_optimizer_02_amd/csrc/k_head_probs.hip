@@ -18,7 +18,7 @@
 //
 // What bounds it: latency.  The largest of n values are found by counting how many reach
 // a threshold, two bits of it a round.  A row of 128256 words, 20 alternatives: 15 us (5 of
-// them the statistics), 27 where a group is opened; 2048 rows with 5 55 us, 4096 with 64 125.
+// them the statistics), 27 where a group is opened; 2048 rows with 5 49 us, 4096 with 64 120.
 #include "head_internal.h"
 #include "kcommon.h"
 

@@ -2,13 +2,13 @@
 // states packed together, the join of the softmax statistics, the coefficients
 // of the gradient and the hidden states' gradient scattered back.
 //
-// All of them move bytes, and few: of 31 ms for 8192 tokens, hidden 4096 and
+// All of them move bytes, and few: of 26 ms for 8192 tokens, hidden 4096 and
 // vocabulary 128256, forward and backward, 0.2 ms.  The exceptions: the student's
 // logits at the teacher's ids, a row of W each (4096 tokens of 64 entries, 2.1 GB of
-// rows, half of them from the caches: 363 us of 16 ms), and the packing of W for fp32
-// (32000 x 1536: 95 us forward, 139 backward).  For few tokens launches count: up to
-// 1024 of them one launch finds the rows and packs them (8 us for 777 x 1536; scoring
-// one token 211 us in all, with two launches 224).
+// rows, half of them from the caches: 347 us of 13.5 ms), and the packing of W for fp32
+// (32000 x 1536: 97 us forward, 143 backward).  For few tokens launches count: up to
+// 1024 of them one launch finds the rows and packs them (8 us for 777 x 1536; two
+// launches made scoring one token, 202 us in all, 13 us longer).
 #include "head_internal.h"
 #include "kcommon.h"
 

@@ -16,8 +16,8 @@
 // What bounds it: the matrix cores with the loads' way into LDS.  8192 tokens, hidden
 // 4096, vocabulary 128256, statistics of softmax and entropy: 6.29 ms, 1368 TFLOP/s,
 // where eight waves take 6.96 to 7.15 on the same cards; 5.8 without its loads.  5734
-// tokens of that size, a piece of 16384 vocabulary rows: ds 633 us for 712, dH 772 for 829, dW
-// 591 for 625.  Lines touched ahead of the loads cost 10%.
+// tokens of that size, a piece of 16384 vocabulary rows: ds 627 us for 712, dH 772 for 829 (627
+// with its splits cut by the rows that take part), dW 559 for 625.  Lines touched ahead of the loads cost 10%.
 #include "head_tile.h"
 
 #include <type_traits>
