@@ -14,7 +14,6 @@ namespace {
 // cache next to what those stream.
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
 constexpr int64_t kCachedBytes = int64_t(240) << 20;  // ... and does, with those streams' share left
-constexpr int64_t kCachedDwBytes = int64_t(112) << 20;
 constexpr int64_t kLowTokens = 128;
 // Bytes that a forward call of the log probabilities holds for its alternatives.
 constexpr int64_t kProbsBytes = int64_t(1) << 30;
@@ -163,8 +162,11 @@ HeadLayout head_layout_of(dmuon_head_desc d, bool backward, bool split_live) {
     // written in parts.  What that takes shows where few tokens leave dW bound by its writes, and
     // the caches hold it.  Backward, us, through against past them: 16 x 1000 x 32000 69 / 75, 96 x 712 x
     // 50257 116 / 123, 48 x 1672 x 32000 118 / 126; 48 x 1416 x 50257 (142 MB) 147 / 145, 96 x 2760 x 32000
-    // (177 MB) 248 / 227; 200 x 1112 x 50257 182 / 180; whole lines 100 x 1024 x 32000 87 / 85.
-    L.dw_cached = backward && !f32 && d.tokens <= kLowTokens && d.hidden % 64 != 0 && 2 * d.hidden * d.vocab <= kCachedDwBytes;
+    // (177 MB) 248 / 227; whole lines 100 x 1024 x 32000 87 / 85.  Up to 256 tokens it shows while
+    // less of the caches is dW's: 200 x 1000 x 32000 (64 MB) 97 / 103, 256 x 1112 x 32000 (71 MB) 119 / 121,
+    // 200 x 1288 x 32000 (82 MB) 131 / 129, 200 x 1112 x 50257 (112 MB) 182 / 180.
+    const int64_t dw_held = d.tokens <= kLowTokens ? int64_t(112) << 20 : d.tokens <= 256 ? int64_t(72) << 20 : 0;
+    L.dw_cached = backward && !f32 && d.hidden % 64 != 0 && 2 * d.hidden * d.vocab <= dw_held;
 
     size_t at = 0;
     auto take = [&](int64_t bytes) {

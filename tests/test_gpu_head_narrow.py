@@ -16,7 +16,7 @@ pytestmark = pytest.mark.gpu
 
 CACHED = [(600, 256, 16000), (1024, 100, 16000), (1536, 384, 8000), (4096, 64, 8000)]
 PAST = [(1024, 512, 16000), (2048, 256, 32000)]
-SPLIT_LINES = [(1, 1000, 32000), (16, 1000, 32001), (100, 1672, 32000), (128, 328, 50257)]
+SPLIT_LINES = [(1, 1000, 32000), (16, 1000, 32001), (100, 1672, 32000), (128, 328, 50257), (200, 1000, 32000)]
 
 
 def say(*a):

@@ -110,7 +110,8 @@ def test_where_ds_stays_in_the_caches(layouts):
 def test_where_dw_is_written_through_the_caches(layouts):
     """Rows of dW that are not whole 128-byte lines, of few tokens, as long as the caches hold dW."""
     sizes = [(*c, True) for c in narrow.SPLIT_LINES] + [(16, 1024, 32000, False), (100, 4096, 32000, False),
-                                                       (96, 2760, 32000, False), (200, 1112, 50257, False)]
+                                                       (96, 2760, 32000, False), (200, 1112, 50257, False),
+                                                       (256, 1288, 32000, False), (300, 1000, 32000, False)]
     for (t, d, v, cached), L in zip(sizes, layouts([backward(t, d, v, t) for t, d, v, _ in sizes])):
         assert (L["dw_tp"], L["dw_tq"], L["dw_splits"]) == (256, 256, 1), (t, d, v)  # (whose kernel it is for)
         assert L["dw_cached"] == cached, (t, d, v)
